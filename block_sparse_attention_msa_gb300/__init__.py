@@ -9,6 +9,9 @@ Stage 1  ``index_score_topk``        block scores + top-k selection per (query r
                                      strided per-head KV view
 Stage 2  ``paged_sparse_decode``     paged decode attention over the selected pages
          ``sparse_prefill``          KV-block-major prefill attention + LSE merge
+Serving  ``build_page_tables``       page tables, lengths and slot maps from request lengths
+batch    ``append_kv``               new tokens into the paged caches
+         ``shared_prefix_decode``    dense paged decode for requests that share a prefix
 Pieces   ``prefill_bucket``, ``lse_merge``, ``device_error``
 """
 from __future__ import annotations
@@ -21,6 +24,7 @@ from . import _lib
 from ._lib import MSAError, library_path, load
 
 __all__ = ["index_score_topk", "index_score_topk_noalloc", "build_sparse_page_table", "paged_sparse_decode", "sparse_prefill",
+           "build_page_tables", "append_kv", "shared_prefix_decode",
            "prefill_bucket", "lse_merge", "device_error", "Workspace", "MSAError", "load",
            "library_path", "BLOCK"]
 
@@ -341,6 +345,167 @@ def sparse_prefill_paged(q, k_cache, v_cache, page_table, block_ids, S_kv: int,
                                       _ptr(block_ids), T, S_kv, Hq, Hkv, D, topk, _ptr(o),
                                       _ptr(lse), _ptr(buf), buf.numel(), _stream(dev))
     _lib.check("msa_sparse_prefill_paged", rc)
+    return o, lse
+
+
+# ------------------------------------------------------------------------------ serving batch
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, expected {dev}")
+
+
+def build_page_tables(prev_lens, new_lens, page_table, free_pages, pages_used, T: int,
+                      num_pages: int, shared_pages=None, out=None):
+    """Page tables, lengths and slot maps of a step, from lengths (``msa_build_page_tables``).
+
+    prev_lens, new_lens [B] int32 (tokens held, tokens added); page_table [B, max_blocks] int32,
+    updated in place; free_pages [F] int32, taken in order from index pages_used [1] int32 on;
+    T token rows (those behind the last token get -1); shared_pages [n] int32: a cached prefix's
+    whole pages, entered for every request that holds at least n*128 tokens. Returns (seq_lens
+    [B], cu_tokens [B+1], slot_map [T], positions [T], pages_used [1]), all int32, written into
+    ``out`` when given (no output may be an input).
+    """
+    _need(prev_lens, "prev_lens", torch.int32, 1)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(free_pages, "free_pages", torch.int32, 1)
+    _need(pages_used, "pages_used", torch.int32, 1)
+    if shared_pages is not None:
+        _need(shared_pages, "shared_pages", torch.int32, 1)
+    B, max_blocks = page_table.shape
+    if prev_lens.numel() != B or new_lens.numel() != B or pages_used.numel() != 1 or T < 0:
+        raise ValueError("build_page_tables: inconsistent shapes")
+    dev = page_table.device
+    _same_device(dev, prev_lens=prev_lens, new_lens=new_lens, free_pages=free_pages,
+                 pages_used=pages_used, shared_pages=shared_pages)
+    sizes = (B, B + 1, T, T, 1)
+    if out is None:
+        out = tuple(torch.empty((n,), dtype=torch.int32, device=dev) for n in sizes)
+    else:
+        for name, t, n in zip(("seq_lens", "cu_tokens", "slot_map", "positions", "pages_used"), out,
+                              sizes, strict=True):
+            _need(t, f"out {name}", torch.int32, 1)
+            _same_device(dev, **{f"out {name}": t})
+            if t.numel() != n:
+                raise ValueError(f"build_page_tables: out {name} has {t.numel()} elements, expected {n}")
+    seq_lens, cu_tokens, slot_map, positions, used_out = out
+    with torch.cuda.device(dev):
+        rc = load().msa_build_page_tables(
+            _ptr(prev_lens), _ptr(new_lens), B, max_blocks, _ptr(page_table), _ptr(free_pages),
+            free_pages.numel(), _ptr(pages_used), _ptr(shared_pages),
+            0 if shared_pages is None else shared_pages.numel(), num_pages, T, _ptr(seq_lens),
+            _ptr(cu_tokens), _ptr(slot_map), _ptr(positions), _ptr(used_out), _stream(dev))
+    _lib.check("msa_build_page_tables", rc)
+    return seq_lens, cu_tokens, slot_map, positions, used_out
+
+
+def _need_rows(t, name: str, T: int, Hkv: int, d: int, dev):
+    """A [T, Hkv, d] bf16 tensor whose token rows are dense; returns the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if tuple(t.shape) != (T, Hkv, d):
+        raise ValueError(f"{name}: expected shape {(T, Hkv, d)}, got {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token row must be contiguous")
+    _same_device(dev, **{name: t})
+    return t.stride(0) if T > 1 else Hkv * d
+
+
+def append_kv(k, v, k_idx, slot_map, k_cache, v_cache, k_idx_pages):
+    """Write new tokens into the paged caches, in place (``msa_append_kv``).
+
+    k, v [T, Hkv, D] and k_idx [T, Hkv, Di] bf16, token rows dense but their stride free (slices
+    of a fused projection); slot_map [T] int32 from ``build_page_tables`` (negative: skipped;
+    non-negative slots must differ); k_cache, v_cache [P, 128, Hkv, D], k_idx_pages
+    [P, 128, Hkv, Di] bf16. k, v and their caches, or k_idx and its pages, may be None.
+    """
+    _need(slot_map, "slot_map", torch.int32, 1)
+    if (k is None) != (v is None) or (k is None) != (k_cache is None) or \
+            (k is None) != (v_cache is None) or (k_idx is None) != (k_idx_pages is None) or \
+            (k is None and k_idx is None):
+        raise ValueError("append_kv: k, v and their caches, or k_idx and its pages, come together")
+    dev = slot_map.device
+    T = slot_map.numel()
+    ks = vs = xs = 0
+    D = Di = BLOCK
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache), ("k_idx_pages", k_idx_pages)):
+        if c is not None:
+            _need(c, name, torch.bfloat16, 4)
+            _same_device(dev, **{name: c})
+    P, page, Hkv = (k_cache if k is not None else k_idx_pages).shape[:3]
+    if page != BLOCK:
+        raise ValueError("append_kv: caches must have 128-token pages")
+    if k is not None:
+        D = k_cache.shape[3]
+        if v_cache.shape != k_cache.shape:
+            raise ValueError("append_kv: inconsistent shapes")
+        ks = _need_rows(k, "k", T, Hkv, D, dev)
+        vs = _need_rows(v, "v", T, Hkv, D, dev)
+    if k_idx is not None:
+        Di = k_idx_pages.shape[3]
+        if k_idx_pages.shape[:3] != (P, page, Hkv):
+            raise ValueError("append_kv: inconsistent shapes")
+        xs = _need_rows(k_idx, "k_idx", T, Hkv, Di, dev)
+    with torch.cuda.device(dev):
+        rc = load().msa_append_kv(_ptr(k), ks, _ptr(v), vs, _ptr(k_idx), xs, _ptr(slot_map), T, Hkv, D,
+                                  Di, P, _ptr(k_cache), _ptr(v_cache), _ptr(k_idx_pages),
+                                  _stream(dev))
+    _lib.check("msa_append_kv", rc)
+
+
+def shared_prefix_decode(q, k_cache, v_cache, page_table, seq_lens, shared_len, N: int = 1,
+                         with_lse: bool = True, workspace: Workspace | None = None, out=None):
+    """Dense paged decode for requests that share a prefix (``msa_shared_prefix_decode``).
+
+    q [B*N, Hq, D] bf16 (the last N positions of each request); caches [P, 128, Hkv, D] bf16;
+    page_table [B, max_blocks] int32; seq_lens [B] int32 (0: a padding request); shared_len [1]
+    int32: leading tokens that hold the same keys and values for every request. Returns
+    (o [B*N, Hq, D] bf16, lse [B*N, Hq] fp32 or None), written into ``out`` when given. Without
+    ``workspace`` the scratch comes from the caching allocator for this call alone, so captured
+    graphs and other streams do not share it.
+    """
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(shared_len, "shared_len", torch.int32, 1)
+    R, Hq, D = q.shape
+    P, page, Hkv, Dk = k_cache.shape
+    B, max_blocks = page_table.shape
+    if R != B * N or v_cache.shape != k_cache.shape or Dk != D or page != BLOCK \
+            or seq_lens.numel() != B or shared_len.numel() != 1:
+        raise ValueError("shared_prefix_decode: inconsistent shapes")
+    dev = q.device
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seq_lens=seq_lens,
+                 shared_len=shared_len)
+    if out is None:
+        o = torch.empty((R, Hq, D), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((R, Hq), dtype=torch.float32, device=dev) if with_lse else None
+    else:
+        o, lse = out
+        _need(o, "out o", torch.bfloat16, 3)
+        _same_device(dev, **{"out o": o, "out lse": lse})
+        if lse is not None:
+            _need(lse, "out lse", torch.float32, 2)
+        if o.shape != q.shape or (lse is not None and lse.shape != (R, Hq)):
+            raise ValueError("shared_prefix_decode: output shapes do not match")
+    lib = load()
+    with torch.cuda.device(dev):
+        nbytes = max(256, lib.msa_shared_prefix_decode_workspace_size(B, N, Hq, Hkv))
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None \
+            else workspace.get("shared_prefix", nbytes, dev)
+        rc = lib.msa_shared_prefix_decode(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
+            _ptr(shared_len), B, N, Hq, Hkv, D, max_blocks, P, _ptr(o), _ptr(lse), _ptr(buf),
+            buf.numel(), _stream(dev))
+    _lib.check("msa_shared_prefix_decode", rc)
     return o, lse
 
 

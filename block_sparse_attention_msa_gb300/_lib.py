@@ -40,6 +40,13 @@ SIGNATURES = [
     ("msa_prefill_bucket_workspace_size", SZ, [I32, I32, I32, I32]),
     ("msa_prefill_bucket", ctypes.c_int, [P, I32, I32, I32, I32, P, P, P, SZ, P]),
     ("msa_lse_merge", ctypes.c_int, [P, I32, P, I64, I32, I32, I32, P, P, P]),
+    ("msa_build_page_tables", ctypes.c_int,
+     [P, P, I32, I32, P, P, I32, P, P, I32, I64, I32, P, P, P, P, P, P]),
+    ("msa_append_kv", ctypes.c_int,
+     [P, I64, P, I64, P, I64, P, I32, I32, I32, I32, I64, P, P, P, P]),
+    ("msa_shared_prefix_decode_workspace_size", SZ, [I32, I32, I32, I32]),
+    ("msa_shared_prefix_decode", ctypes.c_int,
+     [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, P, P, P, SZ, P]),
     ("msa_last_error", ctypes.c_char_p, []),
     ("msa_device_error", ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     ("msa_version", ctypes.c_char_p, []),

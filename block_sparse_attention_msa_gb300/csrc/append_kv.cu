@@ -1,0 +1,92 @@
+// Appends new tokens to the paged caches: row t of K, V and K-index goes to cell slot_map[t] of
+// its cache (cell = page * 128 + offset; a negative slot is a padding row and is skipped).
+//
+// A pure copy: 2 * T * Hkv * (2 D + Di) * 2 bytes move, so HBM bounds long chunks and the launch
+// bounds decode steps. One launch covers the three tensors (grid.y); a thread owns one 16-byte
+// piece of kUnroll rows, whose slots and pieces are all requested before the first store. The
+// rows may be strided (slices of a fused projection), which saves the caller a copy as large as
+// the append itself.
+#include "common.cuh"
+#include "host_util.h"
+#include "kernels.h"
+
+MSA_DEFINE_ERROR_WORD(append)
+
+namespace msa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+struct AppendTensor {
+  const uint4* src;
+  uint4* dst;
+  int64_t src_stride;  // uint4 per token row of src
+  int32_t shift;       // log2 of the row's 16-byte pieces
+};
+struct AppendParams {
+  AppendTensor t[3];
+  const int32_t* slot_map;
+  int32_t T;
+  int64_t cells;
+};
+
+__global__ void __launch_bounds__(kThreads) append_kv_kernel(const __grid_constant__ AppendParams p) {
+  const AppendTensor& x = p.t[blockIdx.y];
+  const int64_t n = (int64_t)p.T << x.shift;
+  const int64_t base = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  if (base >= n) return;
+  const int64_t mask = ((int64_t)1 << x.shift) - 1;
+  int32_t slot[kUnroll];
+  uint4 v[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = base + u * kThreads;
+    slot[u] = i < n ? p.slot_map[i >> x.shift] : -1;
+    if (i < n) v[u] = __ldcs(x.src + (i >> x.shift) * x.src_stride + (i & mask));
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = base + u * kThreads;
+    if (slot[u] < 0) continue;
+    if (slot[u] < p.cells) x.dst[((int64_t)slot[u] << x.shift) + (i & mask)] = v[u];
+    else if ((i & mask) == 0) msa_record_error(kErrBadPage);
+  }
+}
+
+int32_t log2_of(int64_t x) {
+  int32_t s = 0;
+  while (((int64_t)1 << s) < x) ++s;
+  return s;
+}
+
+}  // namespace
+
+cudaError_t launch_append_kv(const AppendArgs& a, cudaStream_t stream) {
+  AppendParams p{};
+  int n = 0;
+  int32_t widest = 0;
+  auto add = [&](const uint16_t* src, uint16_t* dst, int64_t stride, int32_t row) {
+    AppendTensor& t = p.t[n++];
+    t.src = reinterpret_cast<const uint4*>(src);
+    t.dst = reinterpret_cast<uint4*>(dst);
+    t.src_stride = stride / 8;
+    t.shift = log2_of(row / 8);
+    if (t.shift > widest) widest = t.shift;
+  };
+  if (a.k) {
+    add(a.k, a.k_cache, a.k_stride, a.Hkv * a.D);
+    add(a.v, a.v_cache, a.v_stride, a.Hkv * a.D);
+  }
+  if (a.k_idx) add(a.k_idx, a.k_idx_pages, a.idx_stride, a.Hkv * a.Di);
+  p.slot_map = a.slot_map;
+  p.T = a.T;
+  p.cells = a.num_pages * MSA_BLOCK_TOKENS;
+  const int64_t pieces = (int64_t)a.T << widest;
+  const int64_t grid = (pieces + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+  append_kv_kernel<<<dim3((unsigned)grid, (unsigned)n), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace msa

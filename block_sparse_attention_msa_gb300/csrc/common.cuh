@@ -15,6 +15,7 @@ namespace msa {
 constexpr uint32_t kErrBadPage = 1u;
 constexpr uint32_t kErrBadBlock = 2u;
 constexpr uint32_t kErrTimeout = 4u;
+constexpr uint32_t kErrNoPage = 8u;
 
 // Upper bound on polls of one mbarrier phase before a kernel gives up (several seconds
 // with the hardware's suspend hint); a timeout is recorded and the kernel returns.
@@ -122,6 +123,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint64_t* bar,
                                             int32_t c0, int32_t c1, int32_t c2, int32_t c3,
                                             int32_t c4) {

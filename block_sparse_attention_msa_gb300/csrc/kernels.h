@@ -227,6 +227,51 @@ struct PrefillArgs {
 };
 cudaError_t launch_sparse_prefill(const PrefillArgs& a, cudaStream_t stream);
 
+// ------------------------------------------------------------------ serving batch
+constexpr int kMaxRequests = 16384;  // requests per build_page_tables call (two scans in smem)
+struct PageTablesArgs {
+  const int32_t* prev_lens;     // [B]
+  const int32_t* new_lens;      // [B]
+  int32_t* page_table;          // [B, max_blocks], updated in place
+  const int32_t* free_pages;    // [num_free]
+  const int32_t* pages_used;    // [1]
+  const int32_t* shared_pages;  // [num_shared]
+  int32_t B, max_blocks, num_free, num_shared, T;
+  int64_t num_pages;
+  int32_t* seq_lens;            // [B]
+  int32_t* cu_tokens;           // [B + 1]
+  int32_t* slot_map;            // [T]
+  int32_t* positions;           // [T]
+  int32_t* pages_used_out;      // [1]
+};
+cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream);
+
+struct AppendArgs {
+  const uint16_t *k, *v, *k_idx;              // [T, Hkv, D] / [T, Hkv, Di] or null
+  int64_t k_stride, v_stride, idx_stride;     // elements between token rows
+  const int32_t* slot_map;                    // [T]
+  int32_t T, Hkv, D, Di;
+  int64_t num_pages;
+  uint16_t *k_cache, *v_cache, *k_idx_pages;
+};
+cudaError_t launch_append_kv(const AppendArgs& a, cudaStream_t stream);
+
+struct SharedPrefixArgs {
+  const uint16_t* q;           // [B*N, Hq, 128]
+  const uint16_t* k_cache;     // [num_pages, 128, Hkv, 128]
+  const uint16_t* v_cache;
+  const int32_t* page_table;   // [B, max_blocks]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* shared_len;   // [1]
+  int32_t B, N, Hq, Hkv, max_blocks;
+  int64_t num_pages;
+  uint16_t* o;                 // [B*N, Hq, 128]
+  float* lse;                  // [B*N, Hq] or null
+  uint8_t* workspace;
+};
+size_t shared_prefix_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas);
+cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device errors
 cudaError_t read_device_errors(uint32_t* word);
 

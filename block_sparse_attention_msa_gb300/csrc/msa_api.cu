@@ -19,6 +19,9 @@ cudaError_t msa_read_error_dec(uint32_t* w);
 cudaError_t msa_read_error_pre(uint32_t* w);
 cudaError_t msa_read_error_dense(uint32_t* w);
 cudaError_t msa_read_error_stage(uint32_t* w);
+cudaError_t msa_read_error_tables(uint32_t* w);
+cudaError_t msa_read_error_append(uint32_t* w);
+cudaError_t msa_read_error_spd(uint32_t* w);
 
 namespace {
 
@@ -270,6 +273,160 @@ int msa_paged_sparse_decode(const uint16_t* q, const uint16_t* k_cache, const ui
   return cuda_status(msa::launch_paged_decode(a, as_stream(stream)), "msa_paged_sparse_decode");
 }
 
+// ------------------------------------------------------------------------------ serving batch
+int msa_build_page_tables(const int32_t* prev_lens, const int32_t* new_lens, int32_t B,
+                          int32_t max_blocks, int32_t* page_table, const int32_t* free_pages,
+                          int32_t num_free, const int32_t* pages_used,
+                          const int32_t* shared_pages, int32_t num_shared, int64_t num_pages,
+                          int32_t T, int32_t* seq_lens, int32_t* cu_tokens, int32_t* slot_map,
+                          int32_t* positions, int32_t* pages_used_out, void* stream) {
+  const char* name = "msa_build_page_tables";
+  if (B == 0 && T == 0) return ok();
+  if (B <= 0 || T < 0 || max_blocks <= 0 || num_free < 0 || num_shared < 0 || num_pages <= 0)
+    return fail(MSA_ERR_ARG, "%s: B=%d T=%d max_blocks=%d num_free=%d num_shared=%d num_pages=%lld",
+                name, B, T, max_blocks, num_free, num_shared, (long long)num_pages);
+  if (!prev_lens || !new_lens || !page_table || (num_free > 0 && !free_pages) || !pages_used ||
+      (num_shared > 0 && !shared_pages))
+    return fail(MSA_ERR_ARG, "%s: null input pointer", name);
+  if (!seq_lens || !cu_tokens || (T > 0 && (!slot_map || !positions)) || !pages_used_out)
+    return fail(MSA_ERR_ARG, "%s: null output pointer", name);
+  // every CTA reads the lengths while one of them writes the outputs
+  const int32_t* ins[] = {prev_lens, new_lens, pages_used, free_pages, shared_pages};
+  const int32_t* outs[] = {seq_lens, cu_tokens, slot_map, positions, pages_used_out, page_table};
+  for (auto i : ins)
+    for (auto x : outs)
+      if (i && i == x) return fail(MSA_ERR_ARG, "%s: an output is also an input", name);
+  if (B > msa::kMaxRequests)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: B=%d (at most %d)", name, B, msa::kMaxRequests);
+  if (num_shared > max_blocks)
+    return fail(MSA_ERR_SHAPE, "%s: num_shared=%d > max_blocks=%d", name, num_shared, max_blocks);
+  if (num_pages * 128 > kInt32Max || (int64_t)max_blocks * 128 > kInt32Max ||
+      (int64_t)B * max_blocks > kInt32Max)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: slots or table entries exceed int32", name);
+  msa::PageTablesArgs a{};
+  a.prev_lens = prev_lens;
+  a.new_lens = new_lens;
+  a.page_table = page_table;
+  a.free_pages = free_pages;
+  a.pages_used = pages_used;
+  a.shared_pages = shared_pages;
+  a.B = B;
+  a.max_blocks = max_blocks;
+  a.num_free = num_free;
+  a.num_shared = num_shared;
+  a.T = T;
+  a.num_pages = num_pages;
+  a.seq_lens = seq_lens;
+  a.cu_tokens = cu_tokens;
+  a.slot_map = slot_map;
+  a.positions = positions;
+  a.pages_used_out = pages_used_out;
+  return cuda_status(msa::launch_page_tables(a, as_stream(stream)), name);
+}
+
+int msa_append_kv(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                  const uint16_t* k_idx, int64_t k_idx_stride, const int32_t* slot_map, int32_t T,
+                  int32_t Hkv, int32_t D, int32_t Di, int64_t num_pages, uint16_t* k_cache,
+                  uint16_t* v_cache, uint16_t* k_idx_pages, void* stream) {
+  const char* name = "msa_append_kv";
+  if (T == 0) return ok();
+  if (T < 0 || num_pages <= 0)
+    return fail(MSA_ERR_ARG, "%s: T=%d num_pages=%lld", name, T, (long long)num_pages);
+  if (!slot_map || (!k && !v && !k_idx)) return fail(MSA_ERR_ARG, "%s: null tensor pointer", name);
+  if ((k == nullptr) != (v == nullptr) || (k && (!k_cache || !v_cache)) || (k_idx && !k_idx_pages))
+    return fail(MSA_ERR_ARG, "%s: k, v and their caches, or k_idx and its pages, must come together",
+                name);
+  if (!pow2_upto(Hkv, 16)) return fail(MSA_ERR_UNSUPPORTED, "%s: Hkv=%d", name, Hkv);
+  if (k && D != 128) return fail(MSA_ERR_UNSUPPORTED, "%s: D=%d (only 128)", name, D);
+  if (k_idx && Di != 64 && Di != 128) return fail(MSA_ERR_UNSUPPORTED, "%s: Di=%d", name, Di);
+  if (num_pages * 128 > kInt32Max)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: num_pages*128 exceeds int32", name);
+  const void* ptrs[] = {k, v, k_idx, k ? k_cache : nullptr, v ? v_cache : nullptr,
+                        k_idx ? k_idx_pages : nullptr};
+  for (auto x : ptrs)
+    if (reinterpret_cast<uintptr_t>(x) & 15)
+      return fail(MSA_ERR_ARG, "%s: tensors must be 16-byte aligned", name);
+  if ((k && ((k_stride | v_stride) < 0 || ((k_stride | v_stride) & 7))) ||
+      (k_idx && (k_idx_stride < 0 || (k_idx_stride & 7))))
+    return fail(MSA_ERR_ARG, "%s: row strides must be non-negative multiples of 8 elements", name);
+  msa::AppendArgs a{};
+  a.k = k;
+  a.v = v;
+  a.k_idx = k_idx;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.idx_stride = k_idx_stride;
+  a.slot_map = slot_map;
+  a.T = T;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.Di = Di;
+  a.num_pages = num_pages;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_idx_pages = k_idx_pages;
+  return cuda_status(msa::launch_append_kv(a, as_stream(stream)), name);
+}
+
+size_t msa_shared_prefix_decode_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv) {
+  if (B <= 0 || N <= 0 || N > 16 || !pow2_upto(Hkv, 16) || Hq <= 0 || Hq % Hkv ||
+      !pow2_upto(Hq / Hkv, 16) || (int64_t)B * N * Hq > kInt32Max)
+    return 0;
+  return msa::shared_prefix_workspace_bytes(B, N, Hq, Hkv, msa::sm_count());
+}
+
+int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
+                             const int32_t* page_table, const int32_t* seq_lens,
+                             const int32_t* shared_len, int32_t B, int32_t N, int32_t Hq,
+                             int32_t Hkv, int32_t D, int32_t max_blocks, int64_t num_pages,
+                             uint16_t* o, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const char* name = "msa_shared_prefix_decode";
+  if (B == 0) return ok();
+  if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !shared_len || !o)
+    return fail(MSA_ERR_ARG, "%s: null tensor pointer", name);
+  if (B < 0 || N < 1 || max_blocks < 1 || num_pages <= 0)
+    return fail(MSA_ERR_ARG, "%s: B=%d N=%d max_blocks=%d num_pages=%lld", name, B, N, max_blocks,
+                (long long)num_pages);
+  if (N > 16) return fail(MSA_ERR_UNSUPPORTED, "%s: N=%d (at most 16)", name, N);
+  if (D != 128) return fail(MSA_ERR_UNSUPPORTED, "%s: D=%d (only 128)", name, D);
+  if (!pow2_upto(Hkv, 16) || Hq <= 0 || Hq % Hkv != 0 || !pow2_upto(Hq / Hkv, 16))
+    return fail(MSA_ERR_UNSUPPORTED, "%s: Hq=%d Hkv=%d", name, Hq, Hkv);
+  if (num_pages * 128 > kInt32Max || (int64_t)max_blocks * 128 > kInt32Max - 128)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: num_pages*128 or max_blocks*128 exceeds int32", name);
+  // key steps of the whole call, counted in int32 on the device: two per block and tile
+  const int64_t tiles = (int64_t)B * ((N * (Hq / Hkv) + 127) / 128) + 1;
+  const int64_t ptiles = ((int64_t)B * N * (Hq / Hkv) + 127) / 128;
+  if ((int64_t)B * N * Hq > kInt32Max || (tiles > ptiles ? tiles : ptiles) > kInt32Max / 64 ||
+      (tiles > ptiles ? tiles : ptiles) * Hkv * 2 * max_blocks > kInt32Max)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: B=%d N=%d Hkv=%d max_blocks=%d: too many key blocks", name,
+                B, N, Hkv, max_blocks);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) |
+                         reinterpret_cast<uintptr_t>(v_cache) | reinterpret_cast<uintptr_t>(o);
+  if (bits & 15) return fail(MSA_ERR_ARG, "%s: tensors must be 16-byte aligned", name);
+  const size_t need = msa_shared_prefix_decode_workspace_size(B, N, Hq, Hkv);
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return fail(MSA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", name,
+                workspace, workspace_bytes, need);
+  msa::SharedPrefixArgs a{};
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.shared_len = shared_len;
+  a.B = B;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.max_blocks = max_blocks;
+  a.num_pages = num_pages;
+  a.o = o;
+  a.lse = lse;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  return cuda_status(msa::launch_shared_prefix_decode(a, as_stream(stream)), name);
+}
+
 // ------------------------------------------------------------------------------ prefill
 size_t msa_sparse_prefill_workspace_size(int32_t T, int64_t S_kv, int32_t Hq, int32_t Hkv,
                                          int32_t topk) {
@@ -460,7 +617,9 @@ int msa_device_error(uint32_t* word) {
   uint32_t all = 0, w = 0;
   cudaError_t (*readers[])(uint32_t*) = {msa_read_error_score, msa_read_error_ptm,
                                          msa_read_error_dec, msa_read_error_pre,
-                                         msa_read_error_dense, msa_read_error_stage};
+                                         msa_read_error_dense, msa_read_error_stage,
+                                         msa_read_error_tables, msa_read_error_append,
+                                         msa_read_error_spd};
   for (auto rd : readers) {
     w = 0;
     e = rd(&w);

@@ -1,0 +1,932 @@
+// Decode attention for a batch whose requests share a prefix (a cached prompt): the keys of the
+// prefix are read and multiplied once for all requests, the rest request by request.
+//
+// Softmax attention over a key set that is split into parts needs of each part only
+//   m = max s,  l = sum 2^(s - m),  O = sum 2^(s - m) v      (s in log2 units)
+// and the parts join as M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l. So the work is cut
+// into segments (a tile of query rows x a run of 64-key steps) that any CTA may compute, and a
+// second kernel joins each row's segments in a fixed order.
+//
+//  * Prefix. The B*N*G query rows of a KV group form tiles of 128 rows (the M of tcgen05.mma).
+//    Two tiles share each K/V step a CTA loads; an odd last tile is handled like private work.
+//  * Private keys. A tile is one request's N*G rows (padded to M): the MMAs run far below their
+//    rate, but a step's 32 KB take longer to arrive than the padded MMAs take.
+//  * Both kinds are dealt as one line of equal steps: CTAs [0, n_s) cut the prefix steps of all
+//    tile pairs into equal runs, each of the other CTAs' two "lanes" an equal run of the
+//    private steps, and n_s follows from the two totals. No length is read on the host, so the
+//    call can be captured once and replayed with other lengths.
+//  * Only whole 64-key steps below every active request's first visible row go to the prefix;
+//    its remainder is read through each request's own page table, where it also stands. So the
+//    prefix pass needs no mask, and shared_len is a hint about sharing, never about visibility.
+//
+// Per lane: S = Q K^T (128 x 64 x 128) and O += P V run on tcgen05 with S, P and O in tensor
+// memory; one softmax warpgroup per lane keeps the running max and sum (O rescaled only when the
+// max grows by more than 2^8) in fp32. P is rounded to bf16 for its product, as tensor cores
+// take it; its sum l is taken before that rounding. A step is 64 keys because then S has two
+// buffers per lane next to O (2 lanes x (2 x 64 + 128) = 512 columns): S(i+1) is ready when the
+// softmax of step i ends, and the chain S -> softmax -> O of one step no longer bounds the rate.
+#include "common.cuh"
+#include "host_util.h"
+#include "kernels.h"
+#include "softmax_math.cuh"
+
+MSA_DEFINE_ERROR_WORD(spd)
+
+namespace msa {
+
+namespace {
+
+constexpr int kThreads = 384;                    // 4 control warps, 2 softmax warpgroups
+constexpr int kStep = 64;                        // keys per step
+constexpr uint32_t kQHalf = 128 * 128;           // 128 rows x 64 channels bf16
+constexpr uint32_t kQTile = 2 * kQHalf;
+constexpr uint32_t kKvHalf = kStep * 128;        // 64 keys x 64 channels bf16
+constexpr uint32_t kSlot = 2 * kKvHalf;          // K or V of one step: 16 KB
+constexpr int kRing = 10;                        // slots of a pair of tiles; half per private lane
+constexpr int kLaneRing = kRing / 2;
+constexpr uint32_t kOffRing = 2 * kQTile;
+constexpr uint32_t kOffBar = kOffRing + kRing * kSlot;
+constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;                 // log2 headroom before O is rescaled
+constexpr uint32_t kIssuerNap = 100;             // ns an idle MMA issuer blocks on a barrier
+
+struct Bars {
+  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t q_full[2], q_empty[2], o_free[2];
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][step & 1]
+  uint64_t drained;
+  uint32_t tmem_base;
+  int32_t fail;
+  // plan
+  int32_t w_min[kThreads / 32], w_first[kThreads / 32], w_sum[kThreads / 32];
+  int32_t start_b[2], start_rem[2];
+};
+constexpr size_t kSmemBytes = 1024 + kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+// What the join needs of the plan, written by CTA 0 of the attention kernel.
+struct PlanOut {
+  int32_t prefix, w_s, w_p, ts, tp, tpl;
+};
+
+struct KParams {
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* shared_len;
+  int32_t B, N, G, Hq, Hkv, max_blocks;
+  int64_t num_pages;
+  int32_t rows_g;     // B*N*G: query rows of a group
+  int32_t tpt;        // tokens per tile: 128 / G
+  int32_t pairs;      // pairs of prefix tiles per group
+  int32_t odd;        // 1: a last unpaired prefix tile
+  int32_t units;      // tiles of one request's rows
+  int32_t rows_u;     // rows of a request tile (box height): G * min(N, tpt)
+  // partials: O as [32 channel quads][rows][4] fp32, then (m, l) per row
+  float *po_s, *po_l, *po_u;
+  float2 *ml_s, *ml_l, *ml_u;
+  PlanOut* plan;
+  int32_t* cum;       // [B + 1] private steps before request b
+  uint16_t* o;
+  float* lse;
+};
+
+__device__ __forceinline__ int32_t seq_of(const KParams& p, int b) {
+  const int32_t s = p.seq_lens[b];
+  const int32_t hi = p.max_blocks * MSA_BLOCK_TOKENS;
+  return s < 0 ? 0 : (s > hi ? hi : s);
+}
+// Private steps of one tile of request b.
+__device__ __forceinline__ int32_t private_steps(int32_t seq, int32_t prefix) {
+  return seq > prefix ? (seq - prefix + kStep - 1) / kStep : 0;
+}
+// First item of worker w when `total` items are cut into n equal runs, and the worker of item x.
+__device__ __forceinline__ int32_t run_start(int32_t total, int32_t w, int32_t n) {
+  return (int32_t)((int64_t)total * w / n);
+}
+__device__ __forceinline__ int32_t run_of(int32_t total, int32_t x, int32_t n) {
+  return (int32_t)((((int64_t)x + 1) * n - 1) / total);
+}
+
+struct Plan {
+  int32_t prefix;        // tokens of the prefix pass, a multiple of kStep
+  int32_t first;         // an active request (its page table gives the prefix's pages)
+  int32_t nst;           // prefix steps
+  int32_t ts, tp, tpl;   // steps: paired prefix tiles; private space; of it the odd tiles
+  int32_t n_s, n_p;      // CTAs of either kind
+  int32_t w_s, w_p;      // workers of either kind, none of them without a step
+};
+
+// A run of steps of one tile.
+struct Seg {
+  int32_t kind;   // 0: pair of prefix tiles, 1: odd prefix tile, 2: one request
+  int32_t index;  // tile (pair) index within its kind
+  int32_t step0, n;
+  int32_t b, u, g;
+  int32_t seq;    // kind 2: the request's length
+};
+
+// Walks the segments of one worker's run of steps.
+struct Walker {
+  int32_t kind, left, index, step, b, u, g, seq, nst;
+
+  __device__ __forceinline__ void to_request(const KParams& p, const Plan& pl, int32_t from) {
+    kind = 2;
+    u = g = step = 0;
+    b = from;
+    nst = 0;
+    while (b < p.B) {
+      seq = seq_of(p, b);
+      nst = private_steps(seq, pl.prefix);
+      if (nst > 0) break;
+      ++b;
+    }
+    if (b >= p.B) left = 0;
+  }
+  // Worker w of its kind; sb/srem: request and offset in it where the run starts, when it
+  // starts in a request.
+  __device__ __forceinline__ void init(const KParams& p, const Plan& pl, bool shared, int32_t w,
+                                       int32_t sb, int32_t srem) {
+    const int32_t n = shared ? pl.w_s : pl.w_p, total = shared ? pl.ts : pl.tp;
+    const int32_t x0 = w < n ? run_start(total, w, n) : 0;
+    left = w < n ? run_start(total, w + 1, n) - x0 : 0;
+    u = g = b = seq = 0;
+    if (shared || x0 < pl.tpl) {
+      kind = shared ? 0 : 1;
+      nst = pl.nst;
+      index = left > 0 ? x0 / nst : 0;
+      step = left > 0 ? x0 % nst : 0;
+    } else {
+      kind = 2;
+      index = step = nst = 0;
+      if (left > 0) {
+        b = sb;
+        seq = seq_of(p, b);
+        nst = private_steps(seq, pl.prefix);
+        const int32_t t = srem / nst;
+        step = srem % nst;
+        u = t / p.Hkv;
+        g = t % p.Hkv;
+      }
+    }
+  }
+  __device__ __forceinline__ bool next(const KParams& p, const Plan& pl, Seg& s) {
+    if (left <= 0) return false;
+    s.kind = kind;
+    s.step0 = step;
+    s.n = min(left, nst - step);
+    left -= s.n;
+    if (kind != 2) {
+      s.index = index;
+      s.b = pl.first;
+      s.u = kind == 0 ? index % p.pairs : 0;
+      s.g = kind == 0 ? index / p.pairs : index;
+      s.seq = 0;
+      ++index;
+      step = 0;
+      if (kind == 1 && index == p.Hkv && left > 0) to_request(p, pl, 0);
+    } else {
+      s.index = (b * p.units + u) * p.Hkv + g;
+      s.b = b;
+      s.u = u;
+      s.g = g;
+      s.seq = seq;
+      step = 0;
+      if (++g == p.Hkv) {
+        g = 0;
+        if (++u == p.units && left > 0) to_request(p, pl, b + 1);
+      }
+    }
+    return true;
+  }
+};
+
+// Loads are queued in the order the MMAs use them: K0, K1, V0, K2, V1, ..., V(n-1).
+__device__ __forceinline__ int32_t seq_of_v(int32_t i, int32_t n) {
+  return i < n - 1 ? 2 * i + 2 : 2 * n - 1;
+}
+// Position in a ring of `len` slots: slot and the parity of its current use.
+struct RingPos {
+  int32_t slot;
+  uint32_t use;
+  __device__ __forceinline__ void advance(int32_t k, int32_t len) {
+    slot += k;
+    if (slot >= len) {
+      slot -= len;
+      ++use;
+    }
+  }
+};
+
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
+  if (*fail) return false;
+  if (mbar_wait(bar, parity)) return true;
+  msa_record_error(kErrTimeout);
+  *fail = 1;
+  return false;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap qmap_t,
+                         const __grid_constant__ CUtensorMap qmap_u,
+                         const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const KParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  Bars& B = *reinterpret_cast<Bars*>(smem + kOffBar);
+  volatile int32_t* fail = &B.fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the join may be scheduled as CTAs of this kernel leave; it waits for all of their stores
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&B.kv_full[i], 1);
+      mbar_init(&B.kv_empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&B.q_full[x], 1);
+      mbar_init(&B.q_empty[x], 1);
+      mbar_init(&B.o_free[x], 4);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&B.s_full[x][i], 1);
+        mbar_init(&B.o_full[x][i], 1);
+        mbar_init(&B.p_full[x][i], 4);
+      }
+    }
+    mbar_init(&B.drained, 1);
+    B.fail = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&B.tmem_base)), "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // ------------------------------------------------------------------ plan
+  Plan pl;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int pb0 = min(p.B, tid * per), pb1 = min(p.B, pb0 + per);
+  {
+    int32_t vis = INT32_MAX, first = INT32_MAX;  // keys every active row sees; first active request
+    bool bad = false;
+    for (int b = pb0; b < pb1; ++b) {
+      const int32_t s = seq_of(p, b);
+      bad |= s != p.seq_lens[b];
+      if (s > 0) {
+        vis = min(vis, max(0, s - p.N + 1));
+        first = min(first, b);
+      }
+    }
+    if (bad && blockIdx.x == 0) msa_record_error(kErrBadBlock);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      vis = min(vis, __shfl_xor_sync(0xffffffffu, vis, o));
+      first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+    }
+    if (lane == 0) {
+      B.w_min[warp] = vis;
+      B.w_first[warp] = first;
+    }
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) {
+      vis = min(vis, B.w_min[w]);
+      first = min(first, B.w_first[w]);
+    }
+    const bool any = first != INT32_MAX;
+    pl.first = any ? first : 0;
+    const int32_t want = p.shared_len[0];
+    pl.prefix = any ? max(0, min(want, vis)) / kStep * kStep : 0;
+    pl.nst = pl.prefix / kStep;
+    pl.ts = p.Hkv * p.pairs * pl.nst;
+    pl.tpl = p.odd ? p.Hkv * pl.nst : 0;
+    int32_t sum = 0;
+    for (int b = pb0; b < pb1; ++b) sum += private_steps(seq_of(p, b), pl.prefix);
+    sum *= p.units * p.Hkv;
+    int32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) B.w_sum[warp] = incl;
+    __syncthreads();
+    int32_t before = incl - sum, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += B.w_sum[w];
+      total += B.w_sum[w];
+    }
+    pl.tp = pl.tpl + total;
+    const int32_t C = gridDim.x;
+    if (pl.ts == 0) pl.n_p = C;
+    else if (pl.tp == 0) pl.n_p = 0;
+    else pl.n_p = min(C - 1, (int32_t)(((int64_t)C * pl.tp + pl.ts + pl.tp - 1) / ((int64_t)pl.ts + pl.tp)));
+    pl.n_s = C - pl.n_p;
+    pl.w_s = min(pl.n_s, pl.ts);
+    pl.w_p = min(2 * pl.n_p, pl.tp);
+    // where the two lanes of this CTA start, when they start in a request
+    const bool priv = (int)blockIdx.x >= pl.n_s;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int32_t wk = x * pl.n_p + (int)blockIdx.x - pl.n_s;
+      if (!priv || wk >= pl.w_p) break;
+      const int32_t at = run_start(pl.tp, wk, pl.w_p) - pl.tpl;
+      if (at >= before && at < before + sum) {
+        int32_t rem = at - before;
+        int b = pb0;
+        for (; b < pb1; ++b) {
+          const int32_t c = private_steps(seq_of(p, b), pl.prefix) * p.units * p.Hkv;
+          if (rem < c) break;
+          rem -= c;
+        }
+        B.start_b[x] = b;
+        B.start_rem[x] = rem;
+      }
+    }
+    if (blockIdx.x == 0) {
+      int32_t c = before;
+      for (int b = pb0; b < pb1; ++b) {
+        p.cum[b] = c;
+        c += private_steps(seq_of(p, b), pl.prefix) * p.units * p.Hkv;
+      }
+      if (tid == 0) {
+        p.cum[p.B] = total;
+        *p.plan = {pl.prefix, pl.w_s, pl.w_p, pl.ts, pl.tp, pl.tpl};
+      }
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = B.tmem_base;
+  const uint32_t sbase = smem_u32(smem);
+  const bool shared = (int)blockIdx.x < pl.n_s;
+  const int32_t rlen = shared ? kRing : kLaneRing;
+  // worker of lane X: the first n_p workers are the CTAs' lanes 0, so few steps spread over all
+  auto worker_of = [&](int X) {
+    return shared ? (int32_t)blockIdx.x : X * pl.n_p + (int32_t)blockIdx.x - pl.n_s;
+  };
+  auto start = [&](Walker& w, int X) {
+    w.init(p, pl, shared, worker_of(X), B.start_b[X], B.start_rem[X]);
+  };
+
+  if (warp == 0 || warp == 2) {
+    // ================================================================ K/V producers
+    const int X = warp >> 1;
+    const int32_t rbase = shared ? 0 : X * kLaneRing;
+    if (!(shared && X == 1)) {
+      if (lane == 0) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+      }
+      Walker w;
+      start(w, X);
+      RingPos r{0, 0};
+      int32_t v_tok = 0, v_g = 0;
+      bool have_v = false, good = true;
+      auto load = [&](const CUtensorMap* map, int32_t tok, int32_t g) {
+        uint64_t* full = &B.kv_full[rbase + r.slot];
+        if (r.use > 0 && !wait_or_fail(&B.kv_empty[rbase + r.slot], (r.use - 1) & 1, fail)) return false;
+        if (lane == 0) {
+          mbar_expect_tx(full, kSlot);
+          tma_load_4d(smem + kOffRing + (rbase + r.slot) * kSlot, map, full, 0, tok, 0, g);
+        }
+        __syncwarp();
+        r.advance(1, rlen);
+        return true;
+      };
+      Seg s;
+      while (good && w.next(p, pl, s)) {
+        const int32_t key0 = (s.kind == 2 ? pl.prefix : 0) + s.step0 * kStep;
+        const int32_t* table = p.page_table + (int64_t)s.b * p.max_blocks;
+        int32_t tok_l = 0;
+        for (int32_t j = 0; j < s.n && good; ++j) {
+          if ((j & 31) == 0) {  // the token rows of the next 32 steps, one per lane
+            const int32_t jj = j + lane;
+            bool bad = false;
+            if (jj < s.n) {
+              const int32_t key = key0 + jj * kStep;
+              int32_t page = table[key / MSA_BLOCK_TOKENS];
+              bad = page < 0 || page >= p.num_pages;
+              if (bad) page = 0;
+              tok_l = page * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+            }
+            if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
+          }
+          const int32_t tok = __shfl_sync(0xffffffffu, tok_l, j & 31);
+          good = load(&kmap, tok, s.g);
+          if (good && have_v) good = load(&vmap, v_tok, v_g);
+          v_tok = tok;
+          v_g = s.g;
+          have_v = true;
+        }
+      }
+      if (good && have_v) load(&vmap, v_tok, v_g);
+      if (*fail) {  // let the copies in flight land before the CTA leaves
+        for (int32_t i = 0; i < rlen; ++i) {
+          const uint32_t uses = r.use + (i < r.slot ? 1u : 0u);
+          if (uses > 0) mbar_wait(&B.kv_full[rbase + i], (uses - 1) & 1);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ================================================================ query tiles
+    Walker w[2];
+    Seg s[2];
+    bool more[2];
+    int32_t done[2] = {0, 0};
+#pragma unroll
+    for (int X = 0; X < 2; ++X) {
+      start(w[X], X);
+      more[X] = w[X].next(p, pl, s[X]);
+    }
+    uint32_t idle = 0;
+    while (more[0] || more[1]) {
+      bool progress = false;
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        if (!more[X]) continue;
+        if (done[X] > 0 &&
+            !__all_sync(0xffffffffu, mbar_test(&B.q_empty[X], (done[X] - 1) & 1)))
+          continue;
+        if (lane == 0) {
+          uint8_t* dst = smem + X * kQTile;
+          const bool req = s[X].kind == 2;
+          const CUtensorMap* map = req ? &qmap_u : &qmap_t;
+          const int32_t tile = s[X].kind == 0 ? 2 * s[X].u + X : 2 * p.pairs;
+          const int32_t r0 = req ? s[X].b * p.N + s[X].u * p.tpt : tile * p.tpt;
+          mbar_expect_tx(&B.q_full[X], (req ? p.rows_u : 128) * 256);
+          tma_load_5d(dst, map, &B.q_full[X], 0, 0, r0, 0, s[X].g);
+          tma_load_5d(dst + kQHalf, map, &B.q_full[X], 0, 0, r0, 1, s[X].g);
+        }
+        __syncwarp();
+        ++done[X];
+        more[X] = w[X].next(p, pl, s[X]);
+        progress = true;
+      }
+      if (progress) {
+        idle = 0;
+      } else {
+        __nanosleep(64);
+        if (__any_sync(0xffffffffu, *fail != 0)) break;
+        if (++idle > kWaitLimit) {
+          if (lane == 0) msa_record_error(kErrTimeout);
+          *fail = 1;
+          break;
+        }
+      }
+    }
+    if (*fail)
+      for (int X = 0; X < 2; ++X)
+        if (done[X] > 0) mbar_wait(&B.q_full[X], (done[X] - 1) & 1);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    // Lane X's order: S(0), S(1), then O(i), S(i+2): S(i+2) overwrites the tensor memory from
+    // which O(i) reads P(i); the tensor pipe runs one thread's MMAs in issue order. The whole
+    // warp runs the loop in lockstep (barrier states agreed by a vote), an elected lane issues.
+    const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
+    const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
+    Walker w[2];
+    int32_t total[2];
+    int32_t s_n[2] = {0, 0}, o_n[2] = {0, 0}, left[2] = {0, 0}, s_seg[2] = {-1, -1}, o_seg[2] = {-1, -1};
+    uint32_t first_bits[2] = {0, 0};  // bit i & 7: step i opens a segment
+    RingPos kp[2], vp[2];
+#pragma unroll
+    for (int X = 0; X < 2; ++X) {
+      start(w[X], X);
+      total[X] = w[X].left;
+      kp[X] = {0, 0};
+      vp[X] = {0, 0};
+      vp[X].advance(total[X] > 1 ? 2 : 1, rlen);
+    }
+    auto ready = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test(bar, parity));
+    };
+    uint32_t idle = 0;
+    while (o_n[0] < total[0] || o_n[1] < total[1]) {
+      bool progress = false;
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        const int32_t rbase = shared ? 0 : X * kLaneRing;
+        // ---- O_X(i) += P_X(i) V(i)
+        if (o_n[X] < s_n[X]) {
+          const int32_t i = o_n[X];
+          const bool opens = (first_bits[X] >> (i & 7)) & 1u;
+          uint64_t* vfull = &B.kv_full[rbase + vp[X].slot];
+          if (ready(&B.p_full[X][i & 1], (i >> 1) & 1) && ready(vfull, vp[X].use & 1) &&
+              (!opens || o_seg[X] < 0 || ready(&B.o_free[X], o_seg[X] & 1))) {
+            tmem_fence_after();
+            const uint64_t bd =
+                umma_desc_sw128(sbase + kOffRing + (rbase + vp[X].slot) * kSlot, kKvHalf, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kStep / 16; ++kk)
+              umma_bf16_ts_elect(tmem + 256 + X * 128, tmem + X * 128 + (i & 1) * 64 + kk * 8,
+                                 bd + kk * (2048 >> 4), idesc_o, (!opens || kk > 0) ? 1u : 0u);
+            umma_commit_elect(&B.o_full[X][i & 1]);
+            o_n[X] = i + 1;
+            if (opens) ++o_seg[X];
+            if (!shared || o_n[1 - X] >= o_n[X]) umma_commit_elect(&B.kv_empty[rbase + vp[X].slot]);
+            vp[X].advance(i + 2 < total[X] ? 2 : 1, rlen);
+            progress = true;
+          }
+        }
+        // ---- S_X(i) = Q_X K(i)^T
+        if (s_n[X] < total[X] && s_n[X] < o_n[X] + 2) {
+          const int32_t i = s_n[X];
+          if (left[X] == 0) {
+            Seg s;
+            w[X].next(p, pl, s);
+            left[X] = s.n;
+            ++s_seg[X];
+            first_bits[X] |= 1u << (i & 7);
+          }
+          uint64_t* kfull = &B.kv_full[rbase + kp[X].slot];
+          if (ready(kfull, kp[X].use & 1) && ready(&B.q_full[X], s_seg[X] & 1)) {
+            tmem_fence_after();
+            const uint64_t qd = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
+            const uint64_t kd =
+                umma_desc_sw128(sbase + kOffRing + (rbase + kp[X].slot) * kSlot, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t qoff = (kk >> 2) * kQHalf + (kk & 3) * 32;
+              const uint32_t koff = (kk >> 2) * kKvHalf + (kk & 3) * 32;
+              umma_bf16_elect(tmem + X * 128 + (i & 1) * 64, qd + (qoff >> 4), kd + (koff >> 4),
+                              idesc_s, kk > 0);
+            }
+            umma_commit_elect(&B.s_full[X][i & 1]);
+            s_n[X] = i + 1;
+            first_bits[X] &= ~(1u << ((i + 1) & 7));
+            if (--left[X] == 0) umma_commit_elect(&B.q_empty[X]);
+            if (!shared || s_n[1 - X] >= s_n[X]) umma_commit_elect(&B.kv_empty[rbase + kp[X].slot]);
+            kp[X].advance(i == 0 ? 1 : 2, rlen);
+            progress = true;
+          }
+        }
+      }
+      if (progress) {
+        idle = 0;
+      } else {
+        const int X = (o_n[0] < s_n[0]) ? 0 : 1;
+        if (o_n[X] < s_n[X]) mbar_try_wait_hint(&B.p_full[X][o_n[X] & 1], (o_n[X] >> 1) & 1, kIssuerNap);
+        else __nanosleep(32);
+        const bool failed = __any_sync(0xffffffffu, *fail != 0);
+        if (++idle > kWaitLimit || failed) {
+          if (!failed && lane == 0) msa_record_error(kErrTimeout);
+          *fail = 1;
+          // the MMAs in flight end before tensor memory is given back
+          umma_commit_elect(&B.drained);
+          mbar_wait(&B.drained, 0);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================================================================ softmax + partials
+    const int X = (warp - 4) >> 2;
+    const int row = (tid - 128) & 127;  // tile row = tensor memory lane
+    const uint32_t lane_addr = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_tmem = tmem + lane_addr + X * 128;
+    const uint32_t o_tmem = tmem + lane_addr + 256 + X * 128;
+    Walker w;
+    start(w, X);
+    const int32_t total = w.left;
+    const int32_t worker = worker_of(X);
+    int32_t n = 0;
+    Seg s;
+    while (!*fail && w.next(p, pl, s)) {
+      int32_t rows, lim = INT32_MAX, lim_min = INT32_MAX;  // valid rows; visible keys of this row
+      if (s.kind == 2) {
+        const int32_t t0 = s.u * p.tpt;
+        rows = min(p.rows_u, p.N * p.G - t0 * p.G);
+        lim_min = s.seq - p.N + t0 + 1;
+        lim = lim_min + row / p.G;
+      } else {
+        const int32_t tile = s.kind == 0 ? 2 * s.u + X : 2 * p.pairs;
+        rows = min(128, p.rows_g - tile * 128);
+      }
+      const bool act = 32 * (warp & 3) < rows;  // a warp of padding rows only keeps the barriers
+      float m_run = -INFINITY, l = 0.f;         // running max (log2 units) and sum
+      int32_t kb = (s.kind == 2 ? pl.prefix : 0) + s.step0 * kStep;
+      for (int32_t j = 0; j < s.n; ++j, ++n, kb += kStep) {
+        if (!wait_or_fail(&B.s_full[X][n & 1], (n >> 1) & 1, fail)) break;
+        tmem_fence_after();
+        const uint32_t sb = s_tmem + (n & 1) * 64;
+        float factor = 1.f;
+        bool need = false;
+        if (act) {
+          float v[kStep];
+          tmem_ld32(sb, v);
+          tmem_ld32(sb + 32, v + 32);
+          tmem_wait_ld();
+          if (kb + kStep > lim_min) {  // uniform: the step holds a key some row does not see
+            const int32_t vis = lim - kb;
+#pragma unroll
+            for (int x = 0; x < kStep; ++x)
+              if (x >= vis) v[x] = -INFINITY;
+          }
+          float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int x = 4; x < kStep; x += 2) m4[(x >> 1) & 3] = max3(m4[(x >> 1) & 3], v[x], v[x + 1]);
+          const float m2 = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * kLog2e;
+          if (m_run == -INFINITY) {
+            m_run = m2;  // nothing in O yet
+          } else if (m2 > m_run + kRescale) {
+            factor = ex2(m_run - m2);
+            need = true;
+            m_run = m2;
+            l *= factor;
+          }
+          const float off = m_run == -INFINITY ? 0.f : -m_run;
+          float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < kStep; x += 2) {
+            fma2(v[x], v[x + 1], v[x], v[x + 1], kLog2e, kLog2e, off, off);
+            v[x] = ex2(v[x]);
+            v[x + 1] = ex2(v[x + 1]);
+            add2(l8[(x >> 1) & 3], l8[4 + ((x >> 1) & 3)], v[x], v[x + 1]);
+            pk[x >> 1] = pack_bf16x2(v[x], v[x + 1]);
+          }
+          l += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
+          tmem_st32(sb, pk);
+          if (__any_sync(0xffffffffu, need)) {
+            // the max grew by more than 2^8: rescale O once O(n-1) has completed
+            if (!wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail)) break;
+            tmem_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld32(o_tmem + c * 32, o);
+              tmem_wait_ld();
+              uint32_t ob[32];
+#pragma unroll
+              for (int x = 0; x < 32; ++x) ob[x] = __float_as_uint(o[x] * factor);
+              tmem_st32(o_tmem + c * 32, ob);
+            }
+          }
+          tmem_wait_st();
+        }
+        if (s.kind == 2 && kb + kStep > s.seq) {
+          // the cache cells behind the request's last token may hold anything, NaN included, and
+          // 0 * NaN is NaN: their V rows become zero
+          const int32_t z0 = s.seq - kb;
+          const int32_t q = seq_of_v(n, total);
+          const int32_t slot = X * kLaneRing + q % kLaneRing;
+          if (!wait_or_fail(&B.kv_full[slot], (q / kLaneRing) & 1, fail)) break;
+          uint8_t* vrow = smem + kOffRing + slot * kSlot;
+          for (int32_t c = z0 * 16 + row; c < kStep * 16; c += 128)
+            *reinterpret_cast<uint4*>(vrow + ((c >> 3) & 1) * kKvHalf + (c >> 4) * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.p_full[X][n & 1]);
+      }
+      if (*fail) break;
+      // ---------------- the segment's partial. S of the last step says that O(n-3) has completed,
+      // so a barrier per step parity is at most one phase behind and its parity is unambiguous
+      if (!wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail)) break;
+      tmem_fence_after();
+      if (act) {
+        float* po;
+        float2* ml;
+        int32_t cap = 128;
+        if (s.kind == 0) {
+          const int64_t slot = ((int64_t)worker + s.index) * 2 + X;
+          po = p.po_s + slot * 128 * 128;
+          ml = p.ml_s + slot * 128;
+        } else if (s.kind == 1) {
+          const int64_t slot = (int64_t)worker + s.index;
+          po = p.po_l + slot * 128 * 128;
+          ml = p.ml_l + slot * 128;
+        } else {
+          const int64_t slot = (int64_t)worker + s.index;
+          cap = p.rows_u;
+          po = p.po_u + slot * cap * 128;
+          ml = p.ml_u + slot * cap;
+        }
+        const bool mine = row < rows;
+        if (mine) ml[row] = make_float2(m_run, l);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(o_tmem + c * 32, v);
+          tmem_wait_ld();
+          if (mine)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<float4*>(po + ((int64_t)(c * 8 + x) * cap + row) * 4) =
+                  make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+        }
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.o_free[X]);
+    }
+  }
+  // ------------------------------------------------------------------ teardown
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------------------ join
+// A CTA joins eight consecutive query rows of a group; a thread owns four channels of one row,
+// so a warp reads whole 128-byte lines of the partials' [channel quad][row][4] layout.
+constexpr int kJoinRows = 8;
+
+struct Parts {
+  const float* o;
+  const float2* ml;
+  int64_t o_step, ml_step;  // to the next segment of the row
+  int32_t n;
+};
+
+__device__ __forceinline__ void join_max(const Parts& s, float& m) {
+  for (int i = 0; i < s.n; ++i) m = fmaxf(m, s.ml[i * s.ml_step].x);
+}
+__device__ __forceinline__ void join_add(const Parts& s, float m, float& l, float4& acc) {
+#pragma unroll 4
+  for (int i = 0; i < s.n; ++i) {
+    const float2 ml = s.ml[i * s.ml_step];
+    const float4 o = *reinterpret_cast<const float4*>(s.o + i * s.o_step);
+    if (ml.x == -INFINITY && !(ml.y != ml.y)) continue;  // the row saw no key of this segment
+    const float w = ex2(ml.x - m);
+    l += w * ml.y;
+    acc.x += w * o.x;
+    acc.y += w * o.y;
+    acc.z += w * o.z;
+    acc.w += w * o.w;
+  }
+}
+
+__global__ void __launch_bounds__(kJoinRows * 32) shared_prefix_join_kernel(const KParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int32_t g = blockIdx.x % p.Hkv;
+  const int32_t pr = (int32_t)(blockIdx.x / p.Hkv) * kJoinRows + (threadIdx.x & (kJoinRows - 1));
+  const int32_t quad = threadIdx.x / kJoinRows;
+  if (pr >= p.rows_g) return;
+  const PlanOut pl = *p.plan;
+  const int32_t r = pr / p.G, e = pr % p.G, b = r / p.N, i = r % p.N;
+  const int32_t nst = pl.prefix / kStep;
+  Parts a{}, c{};
+  if (nst > 0 && p.seq_lens[b] > 0) {  // a padding request's rows sit in the prefix tiles too
+    const int32_t tile = pr >> 7, row = pr & 127;
+    if (tile < 2 * p.pairs) {
+      const int32_t index = g * p.pairs + (tile >> 1);
+      const int32_t w0 = run_of(pl.ts, index * nst, pl.w_s), w1 = run_of(pl.ts, index * nst + nst - 1, pl.w_s);
+      const int64_t slot = ((int64_t)w0 + index) * 2 + (tile & 1);
+      a = {p.po_s + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_s + slot * 128 + row,
+           2 * 128 * 128, 2 * 128, w1 - w0 + 1};
+    } else {
+      const int32_t w0 = run_of(pl.tp, g * nst, pl.w_p), w1 = run_of(pl.tp, g * nst + nst - 1, pl.w_p);
+      const int64_t slot = (int64_t)w0 + g;
+      a = {p.po_l + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_l + slot * 128 + row,
+           128 * 128, 128, w1 - w0 + 1};
+    }
+  }
+  const int32_t c0 = p.cum[b], per = (p.cum[b + 1] - c0) / (p.units * p.Hkv);
+  if (per > 0) {
+    const int32_t u = i / p.tpt, row = (i - u * p.tpt) * p.G + e;
+    const int32_t x0 = pl.tpl + c0 + (u * p.Hkv + g) * per;
+    const int32_t w0 = run_of(pl.tp, x0, pl.w_p), w1 = run_of(pl.tp, x0 + per - 1, pl.w_p);
+    const int64_t slot = (int64_t)w0 + ((int64_t)b * p.units + u) * p.Hkv + g;
+    const int64_t cap = p.rows_u;
+    c = {p.po_u + ((slot * 32 + quad) * cap + row) * 4, p.ml_u + slot * cap + row, cap * 128, cap,
+         w1 - w0 + 1};
+  }
+  float m = -INFINITY, l = 0.f;
+  join_max(a, m);
+  join_max(c, m);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  join_add(a, m, l, acc);
+  join_add(c, m, l, acc);
+  const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: o = 0, lse = -inf
+  const int64_t out = (int64_t)r * p.Hq + g * p.G + e;
+  uint2 u;
+  u.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  u.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.o + out * 128 + quad * 4) = u;
+  if (quad == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+struct Layout {
+  int32_t rows_g, tpt, pairs, odd, units, rows_u;
+  size_t po_s, po_l, po_u, ml_s, ml_l, ml_u, plan, cum, total;
+};
+
+Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
+  Layout y{};
+  const int32_t G = Hq / Hkv;
+  y.rows_g = B * N * G;
+  y.tpt = 128 / G;
+  const int32_t tiles = (y.rows_g + 127) / 128;
+  y.pairs = tiles / 2;
+  y.odd = tiles & 1;
+  y.units = (N + y.tpt - 1) / y.tpt;
+  y.rows_u = G * (N < y.tpt ? N : y.tpt);
+  // a worker's segments of one kind have distinct worker + tile sums
+  const size_t n_s = y.pairs ? (size_t)ctas + (size_t)Hkv * y.pairs : 0;
+  const size_t n_l = y.odd ? (size_t)2 * ctas + Hkv : 0;
+  const size_t n_u = (size_t)2 * ctas + (size_t)B * y.units * Hkv;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  y.plan = take(sizeof(PlanOut));
+  y.cum = take(((size_t)B + 1) * sizeof(int32_t));
+  y.ml_s = take(n_s * 256 * sizeof(float2));
+  y.ml_l = take(n_l * 128 * sizeof(float2));
+  y.ml_u = take(n_u * y.rows_u * sizeof(float2));
+  y.po_s = take(n_s * 256 * 128 * sizeof(float));
+  y.po_l = take(n_l * 128 * 128 * sizeof(float));
+  y.po_u = take(n_u * y.rows_u * 128 * sizeof(float));
+  y.total = at;
+  return y;
+}
+
+}  // namespace
+
+size_t shared_prefix_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
+  return layout_of(B, N, Hq, Hkv, ctas).total;
+}
+
+cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t stream) {
+  const int ctas = sm_count();
+  const Layout y = layout_of(a.B, a.N, a.Hq, a.Hkv, ctas);
+  const int32_t G = a.Hq / a.Hkv;
+  KParams p{};
+  p.page_table = a.page_table;
+  p.seq_lens = a.seq_lens;
+  p.shared_len = a.shared_len;
+  p.B = a.B;
+  p.N = a.N;
+  p.G = G;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.max_blocks = a.max_blocks;
+  p.num_pages = a.num_pages;
+  p.rows_g = y.rows_g;
+  p.tpt = y.tpt;
+  p.pairs = y.pairs;
+  p.odd = y.odd;
+  p.units = y.units;
+  p.rows_u = y.rows_u;
+  uint8_t* w = a.workspace;
+  p.plan = reinterpret_cast<PlanOut*>(w + y.plan);
+  p.cum = reinterpret_cast<int32_t*>(w + y.cum);
+  p.ml_s = reinterpret_cast<float2*>(w + y.ml_s);
+  p.ml_l = reinterpret_cast<float2*>(w + y.ml_l);
+  p.ml_u = reinterpret_cast<float2*>(w + y.ml_u);
+  p.po_s = reinterpret_cast<float*>(w + y.po_s);
+  p.po_l = reinterpret_cast<float*>(w + y.po_l);
+  p.po_u = reinterpret_cast<float*>(w + y.po_u);
+  p.o = a.o;
+  p.lse = a.lse;
+  // query rows as (channel half, head of the group, row, half, group): a box is G heads of
+  // consecutive rows, one 128-byte line each
+  CUtensorMap qt, qu, km, vm;
+  const uint64_t qd[5] = {64, (uint64_t)G, (uint64_t)a.B * a.N, 2, (uint64_t)a.Hkv};
+  const uint64_t qs[4] = {256, (uint64_t)a.Hq * 256, 128, (uint64_t)G * 256};
+  const uint32_t bt[5] = {64, (uint32_t)G, (uint32_t)y.tpt, 1, 1};
+  const uint32_t bu[5] = {64, (uint32_t)G, (uint32_t)(y.rows_u / G), 1, 1};
+  // cache cells as (channel half, token, half, group): a box is both halves of 64 tokens
+  const uint64_t kd[4] = {64, (uint64_t)a.num_pages * 128, 2, (uint64_t)a.Hkv};
+  const uint64_t ks[3] = {(uint64_t)a.Hkv * 256, 128, 256};
+  const uint32_t bk[4] = {64, kStep, 2, 1};
+  if (!encode_bf16_map(&qt, a.q, 5, qd, qs, bt, true) ||
+      !encode_bf16_map(&qu, a.q, 5, qd, qs, bu, true) ||
+      !encode_bf16_map(&km, a.k_cache, 4, kd, ks, bk, true) ||
+      !encode_bf16_map(&vm, a.v_cache, 4, kd, ks, bk, true))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(shared_prefix_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  shared_prefix_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(qt, qu, km, vm, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.Hkv * (((int64_t)y.rows_g + kJoinRows - 1) / kJoinRows)));
+  cfg.blockDim = dim3(kJoinRows * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel, p);
+}
+
+}  // namespace msa

@@ -355,14 +355,114 @@ MSA_API int msa_index_score_topk_noalloc(const uint16_t* q_idx, const uint16_t* 
                                          int32_t* block_ids, float* scores, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * Serving batch -- page tables, sequence lengths and slot maps of one step, from the requests'
+ * lengths, on the GPU (no length is read on the host, so the call can be captured once and
+ * replayed with other lengths).
+ *
+ * Request b holds prev_lens[b] tokens and gets new_lens[b] more (0 for an idle row). Its first
+ * held_b = ceil(prev_lens[b]/128) table entries are pages it already has; the
+ * need_b = ceil((prev_lens[b]+new_lens[b])/128) - held_b further ones are taken from free_pages
+ * in request order, from index pages_used[0] on:
+ *   page_table[b, held_b + j] = free_pages[pages_used + sum_{b'<b} need_b' + j],  j < need_b;
+ *   every other entry is left as it was.
+ *   seq_lens[b]  = prev_lens[b] + new_lens[b];  cu_tokens[b] = sum_{b'<b} new_lens[b'];
+ *   token row t of request b (cu_tokens[b] <= t < cu_tokens[b+1]) has
+ *   positions[t] = prev_lens[b] + t - cu_tokens[b] and
+ *   slot_map[t]  = page_table[b, positions[t]/128]*128 + positions[t]%128;
+ *   rows from cu_tokens[B] to T-1 (padding) get slot and position -1.
+ *   pages_used_out[0] = pages_used[0] + sum_b need_b.
+ * With shared_pages (num_shared > 0), entries 0..num_shared-1 of every request with
+ * prev_lens[b] >= num_shared*128 are set to them: a cached prefix of whole pages.
+ *
+ *   prev_lens, new_lens [B] int32; page_table [B, max_blocks] int32 (in/out);
+ *   free_pages [num_free] int32; pages_used [1] int32; shared_pages [num_shared] int32 or NULL
+ *   seq_lens [B], cu_tokens [B+1], slot_map [T], positions [T], pages_used_out [1] int32 (out)
+ * No output may be (or overlap) an input. B <= 16384; num_pages*128, max_blocks*128 and
+ * B*max_blocks < 2^31.
+ * Device-side checks: a negative length or one past max_blocks*128 is clamped, token rows past T
+ * are dropped, pages_used is clamped to [0, num_free] (all bit 1); a page outside
+ * [0, num_pages) becomes entry and slot -1 (bit 0). When the free list runs out (bit 3) the
+ * entries and slots that it cannot serve are -1, seq_lens[b] stops at the tokens the request's
+ * pages hold, and pages_used_out is num_free; cu_tokens and positions still count every token.
+ * ------------------------------------------------------------------------------------ */
+MSA_API int msa_build_page_tables(const int32_t* prev_lens, const int32_t* new_lens, int32_t B,
+                                  int32_t max_blocks, int32_t* page_table,
+                                  const int32_t* free_pages, int32_t num_free,
+                                  const int32_t* pages_used, const int32_t* shared_pages,
+                                  int32_t num_shared, int64_t num_pages, int32_t T,
+                                  int32_t* seq_lens, int32_t* cu_tokens, int32_t* slot_map,
+                                  int32_t* positions, int32_t* pages_used_out, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Serving batch -- append new tokens to the paged caches.
+ *
+ * For every token row t with slot_map[t] >= 0 (page*128 + offset, from msa_build_page_tables):
+ *   cache cell slot_map[t] = row t, for K, V and the key index in one launch. Rows with a
+ *   negative slot are skipped; every other cell of the caches is left as it was.
+ *
+ *   k, v [T, Hkv, D] bf16; k_idx [T, Hkv, Di] bf16: rows of Hkv*D (Hkv*Di) dense elements, the
+ *   row stride of each given in elements (a slice of a fused projection needs no copy); k and v
+ *   may both be NULL, or k_idx (a layer without a key index)
+ *   slot_map [T] int32; non-negative slots must differ: which row a repeated slot ends with is
+ *   not specified
+ *   k_cache, v_cache [num_pages, 128, Hkv, D], k_idx_pages [num_pages, 128, Hkv, Di] bf16 (out)
+ * Tensors are 16-byte aligned, strides multiples of 8 elements. A slot of num_pages*128 or more
+ * is not written and sets bit 0 of the device error word.
+ * ------------------------------------------------------------------------------------ */
+MSA_API int msa_append_kv(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                          const uint16_t* k_idx, int64_t k_idx_stride, const int32_t* slot_map,
+                          int32_t T, int32_t Hkv, int32_t D, int32_t Di, int64_t num_pages,
+                          uint16_t* k_cache, uint16_t* v_cache, uint16_t* k_idx_pages,
+                          void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Serving batch -- dense decode attention over the paged cache for requests that share a
+ * prefix (a cached prompt), whose keys are read and multiplied once for the whole batch.
+ *
+ * For query row r = b*N + i at position pos = seq_lens[b] - N + i and head h of group g:
+ *   s_n = q[r,h,:] . k_cache[page_table[b, n/128], n%128, g, :],  n = 0..pos;
+ *   o[r,h,:] = softmax(s) . V;  lse[r,h] = log sum_n exp(s_n).
+ * shared_len[0] tokens are the same for every request with seq_lens[b] > 0: for n < shared_len
+ * all of them hold the same keys and values (whole shared pages, and private copies of a partly
+ * filled one). It says only what may be read once, never what a row sees: the prefix pass takes
+ * the whole 64-token steps below min(shared_len, visible keys of the first row of every active
+ * request), and each request reads the rest through its own table. shared_len = 0 is a plain
+ * paged decode.
+ * A request with seq_lens[b] = 0 (a padding row of a captured batch), and any row at a negative
+ * position, sees no key: o = 0, lse = -inf. Cache cells past a request's length may hold
+ * anything, NaN included. (A non-finite V of one of the last N tokens of a request can reach
+ * the request's earlier rows too.)
+ *
+ *   q [B*N, Hq, D] bf16; k_cache, v_cache [num_pages, 128, Hkv, D] bf16
+ *   page_table [B, max_blocks] int32; seq_lens [B] int32 (0..max_blocks*128, else clamped: bit 1)
+ *   shared_len [1] int32
+ *   o [B*N, Hq, D] bf16 (out); lse [B*N, Hq] fp32 (out, may be NULL)
+ *   workspace >= msa_shared_prefix_decode_workspace_size(B, N, Hq, Hkv) bytes, 256-byte aligned,
+ *   any contents (its size goes with the current device's SM count). Calls that may run
+ *   concurrently need separate workspaces.
+ * 1 <= N <= 16. The result depends only on the inputs and the device's SM count (no run-to-run
+ * variation). Lengths and tables are read on the device: a captured call can be replayed with
+ * other values in the same buffers.
+ * ------------------------------------------------------------------------------------ */
+MSA_API size_t msa_shared_prefix_decode_workspace_size(int32_t B, int32_t N, int32_t Hq,
+                                                       int32_t Hkv);
+
+MSA_API int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache,
+                                     const uint16_t* v_cache, const int32_t* page_table,
+                                     const int32_t* seq_lens, const int32_t* shared_len, int32_t B,
+                                     int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t max_blocks, int64_t num_pages, uint16_t* o, float* lse,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Diagnostics.
  * ------------------------------------------------------------------------------------ */
 /* Thread-local message of the last failing call on this host thread ("" if none). */
 MSA_API const char* msa_last_error(void);
 
 /* Synchronises the current device, returns the device error word recorded by the kernels
- * (0 = none; bit 0 = out-of-range page id, bit 1 = out-of-range block id, bit 2 = a bounded
- * wait timed out) in *word (host pointer) and clears it. Returns MSA_OK, or MSA_ERR_DEVICE
+ * (0 = none; bit 0 = out-of-range page id, bit 1 = out-of-range block id or length, bit 2 = a
+ * bounded wait timed out, bit 3 = the free page list ran out) in *word (host pointer) and clears it. Returns MSA_OK, or MSA_ERR_DEVICE
  * when the word was non-zero, or MSA_ERR_CUDA. Not for the hot path. */
 MSA_API int msa_device_error(uint32_t* word);
 

@@ -1,0 +1,512 @@
+"""GPU tests of the serving-batch operators against plain 64-bit implementations written here:
+``build_page_tables`` (integers: equal), ``append_kv`` (copies: equal), ``shared_prefix_decode``,
+and a run of the three together with the sparse path on the same caches.
+
+Attention tolerance, per output element, from the roundings the kernel makes. With w the exact
+softmax weights, A = sum_n w_n |v_n| and ref the exact output:
+  * P = 2^(s - m) is rounded to bf16 for its product: at most 2^-8 of each term, 2^-8 A in all;
+  * o is rounded to bf16 once: 2^-8 of the value;
+  * a score is an fp32 sum of 128 exact products of bf16 numbers, at most 2^-23 of sum |q_d k_d| per
+    addition (truncating adds counted), then scaled to log2 units: ds = 2^-23 * 128 * max_n
+    sum_d |q_d k_nd| + 2^-21 * max |s|, which moves weights by at most 2 ds A;
+  * 2^x, the fp32 sums of P V and l and the joins: 2^-21 + n * 2^-24 per key count n, of A.
+LSE: ds + 2^-21 + n * 2^-24 absolute, + 2^-23 of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_msa_gb300 as msa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+PAGE = 128
+D = 128
+BAD_PAGE, BAD_LEN, NO_PAGE = 1, 2, 8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_sparse_attention_msa_gb300 import build
+    build.build()
+    msa.load()
+    assert msa.device_error() == 0  # nothing left over from earlier tests
+    yield
+    assert msa.device_error() == 0
+
+
+def i32(x):
+    return torch.from_numpy(np.array(x, dtype=np.int32))
+
+
+# ------------------------------------------------------------------------------ page tables
+
+def ref_tables(prev, new, table, free, used, T, shared=None, num_pages=1 << 30):
+    """The documented rules, one token at a time."""
+    table = table.copy()
+    B, mb = table.shape
+    seq, cu, slots, pos = [], [0], [-1] * T, [-1] * T
+    for b in range(B):
+        p = min(max(int(prev[b]), 0), mb * PAGE)
+        n = min(max(int(new[b]), 0), mb * PAGE - p)
+        if shared is not None and p >= len(shared) * PAGE:
+            table[b, :len(shared)] = shared
+        length = p
+        stopped = False
+        for i in range(n):
+            at = p + i
+            if at % PAGE == 0:
+                if used < len(free):
+                    page = int(free[used])
+                    used += 1
+                    table[b, at // PAGE] = page if 0 <= page < num_pages else -1
+                else:
+                    table[b, at // PAGE] = -1
+                    stopped = True
+            if not stopped:
+                length = at + 1
+            t = cu[-1] + i
+            if t < T:
+                pos[t] = at
+                page = -1 if stopped else int(table[b, at // PAGE])
+                slots[t] = page * PAGE + at % PAGE if 0 <= page < num_pages else -1
+        seq.append(length)
+        cu.append(cu[-1] + n)
+    return table, seq, cu, slots, pos, used
+
+
+def check_tables(prev, new, mb, free, used, T, shared=None, num_pages=1 << 20, expect=0, seed=0):
+    rng = np.random.default_rng(seed)
+    B = len(prev)
+    table = rng.integers(0, min(num_pages, 1 << 20), (B, mb)).astype(np.int32)
+    table_d = i32(table).to(DEV)
+    shared_d = None if shared is None else i32(shared).to(DEV)
+    free_d = i32(free).to(DEV)
+    ins = (i32(prev).to(DEV), i32(new).to(DEV), free_d, i32([used]).to(DEV))
+    copies = [x.clone() for x in ins]
+    got = msa.build_page_tables(ins[0], ins[1], table_d, free_d, ins[3], T=T, num_pages=num_pages,
+                                shared_pages=shared_d)
+    assert msa.device_error() == expect
+    want = ref_tables(prev, new, table, free, min(max(used, 0), len(free)), T, shared, num_pages)
+    assert np.array_equal(table_d.cpu().numpy(), want[0])
+    for name, g, w in zip(("seq_lens", "cu_tokens", "slot_map", "positions"), got, want[1:5]):
+        assert np.array_equal(g.cpu().numpy(), np.asarray(w, dtype=np.int32)), name
+    assert int(got[4]) == want[5]
+    for a, b in zip(ins, copies):
+        assert torch.equal(a, b)  # inputs are left alone
+    return got
+
+
+@pytest.mark.parametrize("prev,new,pad", [
+    ([0], [1], 0),                                   # the first token of a request
+    ([0], [0], 3),                                   # nothing to do, padding rows only
+    ([127], [1], 0), ([128], [1], 0), ([127], [2], 5),   # around a page border
+    ([0, 5, 128, 255, 300], [0, 1, 1, 1, 0], 2),     # idle rows in a decode step
+    ([700, 0, 1, 129], [300, 513, 0, 128], 0),       # chunks
+    ([0] * 7, [0, 0, 1000, 0, 0, 1, 0], 9),          # empty requests around a long one
+])
+def test_page_tables_small(prev, new, pad):
+    total = sum(new)
+    check_tables(prev, new, 12, np.arange(100, 140)[::-1], 3, total + pad)
+
+
+@pytest.mark.parametrize("B,hi,mb", [(61, 900, 40), (255, 3, 9), (256, 5, 9), (257, 300, 16), (1500, 2, 10)])
+def test_page_tables_ragged(B, hi, mb):
+    rng = np.random.default_rng(B)
+    prev = rng.integers(0, (mb - 8) * PAGE, B)
+    new = rng.integers(0, hi + 1, B)
+    free = rng.permutation(1 << 16)[:B * 9 + 5]
+    check_tables(prev, new, mb, free, 2, int(new.sum()) + 11, seed=B)
+
+
+def test_page_tables_shared_prefix():
+    shared = np.array([9, 3, 77, 5])
+    prev = [512, 512, 600, 511, 0, 512]   # requests 3 and 4 do not hold the whole prefix
+    check_tables(prev, [1, 0, 200, 1, 130, 129], 16, np.arange(50, 90), 0, 470, shared=shared)
+
+
+def test_page_tables_free_list_runs_out():
+    # 6 fresh pages needed, 4 left: request 1 is cut after its first fresh page, request 2 gets none
+    check_tables([128, 128, 128], [256, 256, 256], 8, np.arange(20, 30), 7, 768, expect=NO_PAGE)
+    check_tables([130, 100], [1, 1], 8, np.zeros(0, dtype=np.int32), 0, 2)  # none needed
+
+
+def test_page_tables_bad_values():
+    # lengths out of range are clamped, rows past T dropped, a bad index into the list clamped
+    check_tables([-5, 10, 4 * PAGE + 9], [3, -1, 7], 4, np.arange(9), 0, 30, expect=BAD_LEN)
+    check_tables([0], [4 * PAGE + 50], 4, np.arange(9), 0, 4 * PAGE, expect=BAD_LEN)
+    check_tables([0, 5], [100, 100], 4, np.arange(9), 1, 150, expect=BAD_LEN)
+    check_tables([0], [3], 4, np.arange(9), -4, 3, expect=BAD_LEN)
+    # a page of the free list outside the cache
+    check_tables([0, 0], [200, 100], 4, np.array([5, 64, 7, -1]), 0, 300, num_pages=64,
+                 expect=BAD_PAGE)
+
+
+def test_page_tables_captured_and_replayed_with_other_lengths():
+    B, mb, T = 5, 8, 64
+    prev = torch.zeros(B, dtype=torch.int32, device=DEV)
+    new = torch.ones(B, dtype=torch.int32, device=DEV)
+    table = torch.zeros((B, mb), dtype=torch.int32, device=DEV)
+    free = torch.arange(100, dtype=torch.int32, device=DEV)
+    used = torch.zeros(1, dtype=torch.int32, device=DEV)
+    msa.build_page_tables(prev, new, table, free, used, T=T, num_pages=100)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = msa.build_page_tables(prev, new, table, free, used, T=T, num_pages=100)
+    for seed in range(3):
+        rng = np.random.default_rng(seed)
+        pv, nw = rng.integers(0, 700, B), rng.integers(0, 14, B)
+        prev.copy_(i32(pv))
+        new.copy_(i32(nw))
+        used.fill_(seed)
+        table.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref_tables(pv, nw, np.full((B, mb), 7, dtype=np.int32), np.arange(100), seed, T)
+        assert np.array_equal(table.cpu().numpy(), want[0])
+        for g, w in zip(out, want[1:5]):
+            assert np.array_equal(g.cpu().numpy(), np.asarray(w, dtype=np.int32))
+        assert int(out[4]) == want[5]
+
+
+# ------------------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("T,Hkv,Di,strided", [
+    (1, 8, 128, False), (3, 1, 64, True), (37, 2, 64, True), (513, 16, 128, False),
+    (1000, 4, 128, True), (129, 8, 64, True),
+])
+def test_append_kv(T, Hkv, Di, strided):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    P = T // PAGE + 3
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV).to(torch.bfloat16)
+    if strided:
+        qkv = rnd(T, 3 * Hkv * D + Hkv * Di)
+        k = qkv[:, Hkv * D:2 * Hkv * D].unflatten(1, (Hkv, D))
+        v = qkv[:, 2 * Hkv * D:3 * Hkv * D].unflatten(1, (Hkv, D))
+        x = qkv[:, 3 * Hkv * D:].unflatten(1, (Hkv, Di))
+    else:
+        k, v, x = rnd(T, Hkv, D), rnd(T, Hkv, D), rnd(T, Hkv, Di)
+    k[0, 0, 0], v[0, 0, 1] = float("nan"), float("-inf")  # bits are copied, whatever they say
+    slots = torch.randperm(P * PAGE, generator=g, device=DEV)[:T].to(torch.int32)
+    slots[T // 3::7] = -1
+    caches = [rnd(P, PAGE, Hkv, D), rnd(P, PAGE, Hkv, D), rnd(P, PAGE, Hkv, Di)]
+    want = [c.clone() for c in caches]
+    live = slots >= 0
+    for c, rows in zip(want, (k, v, x)):
+        c.view(-1, *c.shape[2:])[slots[live].long()] = rows[live]
+    msa.append_kv(k, v, x, slots, *caches)
+    for c, w in zip(caches, want):
+        assert torch.equal(c.view(torch.int16), w.view(torch.int16))
+    # K/V alone, and the key index alone
+    again = [torch.zeros_like(c) for c in caches]
+    msa.append_kv(k, v, None, slots, again[0], again[1], None)
+    msa.append_kv(None, None, x, slots, None, None, again[2])
+    cells = slots[live].long()
+    for c, w in zip(again, want):
+        flat, ref = c.view(-1, *c.shape[2:]), w.view(-1, *w.shape[2:])
+        assert torch.equal(flat[cells].view(torch.int16), ref[cells].view(torch.int16))
+        flat[cells] = 0
+        assert not flat.any()
+
+
+def test_append_kv_skips_bad_slots_and_empty_batches():
+    k = torch.ones((3, 2, D), dtype=torch.bfloat16, device=DEV)
+    caches = [torch.zeros((2, PAGE, 2, D), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    msa.append_kv(k, k, k, i32([2 * PAGE, -7, 2 * PAGE - 1]).to(DEV), *caches)
+    assert msa.device_error() == BAD_PAGE
+    for c in caches:
+        assert c.view(-1, 2, D)[-1].eq(1).all() and c.view(-1, 2, D)[:-1].eq(0).all()
+    none = k[:0]
+    msa.append_kv(none, none, none, i32([]).to(DEV), *caches)
+
+
+# ------------------------------------------------------------------------------ decode
+
+def make_decode(seq, shared, N, Hq, Hkv, seed, scale=1.0):
+    """Caches whose unused cells are NaN, one page table per request, shared pages in common."""
+    g = torch.Generator().manual_seed(seed)
+    B = len(seq)
+    whole = shared // PAGE
+    blocks = [(n + PAGE - 1) // PAGE for n in seq]
+    mb = max(1, max(blocks), whole)
+    pages = whole + sum(max(0, n - whole) for n in blocks) + 2
+    perm = torch.randperm(pages, generator=g).to(torch.int32)
+    table = torch.randint(0, pages, (B, mb), generator=g).to(torch.int32)  # unused entries: any page
+    kc = torch.full((pages, PAGE, Hkv, D), float("nan"), dtype=torch.bfloat16)
+    vc = kc.clone()
+    rnd = lambda n: (torch.randn((n, Hkv, D), generator=g) * scale).to(torch.bfloat16)
+    pk, pv = rnd(shared), torch.randn((shared, Hkv, D), generator=g).to(torch.bfloat16)
+    used = whole
+    for b, n in enumerate(seq):
+        if n == 0:
+            continue
+        table[b, :whole] = perm[:whole]
+        for j in range(whole, blocks[b]):
+            table[b, j] = perm[used]
+            used += 1
+        own = n - shared
+        k = torch.cat([pk, rnd(own)]) if own >= 0 else rnd(n)
+        v = torch.cat([pv, rnd(own)]) if own >= 0 else rnd(n)
+        for j in range(blocks[b]):
+            m = min(PAGE, n - j * PAGE)
+            kc[table[b, j], :m] = k[j * PAGE:j * PAGE + m]
+            vc[table[b, j], :m] = v[j * PAGE:j * PAGE + m]
+    q = (torch.randn((B * N, Hq, D), generator=g) * D ** -0.5).to(torch.bfloat16)
+    return dict(q=q, kc=kc, vc=vc, table=table, seq=i32(seq), N=N, shared=shared)
+
+
+def ref_decode(w):
+    """o, lse, and per element / row the tolerances of the module docstring, in 64 bits."""
+    q, N = w["q"].double(), w["N"]
+    R, Hq, _ = q.shape
+    Hkv = w["kc"].shape[2]
+    G = Hq // Hkv
+    o = torch.zeros((R, Hq, D), dtype=torch.float64)
+    lse = torch.full((R, Hq), float("-inf"), dtype=torch.float64)
+    to, tl = torch.zeros_like(o), torch.zeros_like(lse)
+    for b, n in enumerate(w["seq"].tolist()):
+        pages = w["table"][b, :(n + PAGE - 1) // PAGE].long()
+        k = w["kc"][pages].flatten(0, 1)[:n].double().permute(1, 2, 0)
+        v = w["vc"][pages].flatten(0, 1)[:n].double().transpose(0, 1)
+        for i in range(N):
+            vis = n - N + i + 1
+            if vis <= 0:
+                continue
+            qi = q[b * N + i].view(Hkv, G, D)
+            s = qi @ k[:, :, :vis]
+            z = torch.logsumexp(s, -1, keepdim=True)
+            p = torch.exp(s - z)
+            ref = p @ v[:, :vis]
+            A = p @ v[:, :vis].abs()
+            dots = (qi.abs() @ k[:, :, :vis].abs()).amax(-1, keepdim=True)
+            ds = 2.0 ** -23 * 128 * dots + 2.0 ** -21 * s.abs().amax(-1, keepdim=True)
+            acc = 2.0 ** -21 + vis * 2.0 ** -24
+            r = b * N + i
+            o[r], lse[r] = ref.reshape(Hq, D), z.reshape(Hq)
+            to[r] = (2.0 ** -8 * (ref.abs() + A) * (1 + 2.0 ** -7) + (2 * ds + acc) * A).reshape(Hq, D)
+            tl[r] = (ds + acc + 2.0 ** -23 * z.abs()).reshape(Hq)
+    return o, lse, to, tl
+
+
+def run_decode(w, shared=None, **kw):
+    d = {k: x.to(DEV) for k, x in w.items() if isinstance(x, torch.Tensor)}
+    sl = i32([w["shared"] if shared is None else shared]).to(DEV)
+    return msa.shared_prefix_decode(d["q"], d["kc"], d["vc"], d["table"], d["seq"], sl, N=w["N"], **kw)
+
+
+def check_decode(got, ref):
+    o, lse, to, tl = ref
+    go, gl = got[0].double().cpu(), got[1].double().cpu()
+    err = (go - o).abs()
+    assert (err <= to).all(), f"o: worst error / tolerance {(err / to.clamp_min(1e-300)).max():.3f}"
+    empty = torch.isneginf(lse)
+    assert torch.equal(torch.isneginf(gl), empty)
+    assert (go[empty] == 0).all()
+    err = (gl - lse).abs()[~empty]
+    assert (err <= tl[~empty]).all(), f"lse: worst error / tolerance {(err / tl[~empty]).max():.3f}"
+
+
+CASES = [
+    # seq, shared, N, Hq, Hkv
+    ([1], 0, 1, 8, 2),                               # one token, one request
+    ([1], 1, 1, 1, 1),                               # ... all of it shared: below a step, private
+    ([64], 64, 1, 8, 2), ([65], 64, 1, 8, 2),        # exactly the prefix; one key more
+    ([2048], 1000, 1, 8, 2),                         # one odd tile, private remainder
+    ([300, 301, 427, 1000, 256], 256, 1, 64, 8),     # shared pages, ragged
+    ([700, 645, 641, 1500], 640, 3, 32, 4),          # several rows per request, causal
+    ([777] * 9, 513, 1, 16, 16),                     # one head per group
+    ([129, 200, 190], 129, 16, 16, 1),               # G 16, N 16: two tiles per request
+    ([400 + 3 * i for i in range(20)], 384, 1, 64, 4),    # 320 rows per group: a pair and an odd tile
+    ([520 + i for i in range(32)], 500, 1, 64, 8),   # 256 rows per group: one pair exactly
+    ([1030 + 7 * i for i in range(48)], 1024, 2, 16, 2),  # 768 rows: three pairs
+    ([0, 90, 0, 700, 5, 0], 0, 1, 8, 1),             # padding requests
+    ([0, 900, 0, 700, 650, 0] * 9, 600, 1, 8, 1),    # ... in the prefix tiles too
+    ([2, 500, 16, 1], 0, 8, 8, 2),                   # rows at negative positions
+    ([60, 300, 200], 190, 4, 16, 2),                 # a request shorter than shared_len claims
+    ([5000, 3, 70, 4100], 0, 1, 64, 8),              # private only, one short among long
+    ([9000], 8960, 1, 64, 8),                        # a long prefix cut over every CTA
+    ([130 + (i * 37) % 200 for i in range(300)], 128, 1, 8, 2),   # many requests
+    ([0, 0, 0], 128, 2, 8, 2),                       # nobody is active
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_shared_prefix_decode(case):
+    seq, shared, N, Hq, Hkv = CASES[case]
+    w = make_decode(seq, shared if min([n for n in seq if n] or [0]) >= shared else 0, N, Hq, Hkv,
+                    seed=case)
+    check_decode(run_decode(w, shared=shared), ref_decode(w))
+
+
+@pytest.mark.parametrize("shared", [-3, 0, 63, 64, 100, 511, 512, 1 << 30])
+def test_shared_len_changes_the_work_not_the_answer(shared):
+    # every request holds 512 shared tokens; any claim up to them (or past every row) must agree
+    w = make_decode([512, 513, 600, 1000], 512, 1, 32, 4, seed=5)
+    if shared > 512:
+        w = make_decode([700] * 3, 700, 1, 32, 4, seed=6)
+    check_decode(run_decode(w, shared=shared), ref_decode(w))
+
+
+def test_large_scores_rescale_the_output():
+    # scores of +-150 that keep growing along the keys: the running max moves many times
+    w = make_decode([1500, 1100, 1283], 1024, 1, 32, 4, seed=7, scale=20.0)
+    ramp = torch.linspace(0.1, 3.0, 12)
+    for j in range(11):
+        for b in range(3):
+            if j < w["table"].shape[1] and (j >= 8 or b == 0):
+                w["kc"][w["table"][b, j]] = (w["kc"][w["table"][b, j]].float() * ramp[j]).to(torch.bfloat16)
+    check_decode(run_decode(w), ref_decode(w))
+
+
+def test_runs_agree_bit_for_bit_and_inputs_stay():
+    w = make_decode([900 + 13 * i for i in range(40)], 800, 1, 64, 4, seed=8)
+    d = {k: x.to(DEV) for k, x in w.items() if isinstance(x, torch.Tensor)}
+    copies = {k: x.clone() for k, x in d.items()}
+    sl = i32([800]).to(DEV)
+    args = (d["q"], d["kc"], d["vc"], d["table"], d["seq"], sl)
+    o1, l1 = msa.shared_prefix_decode(*args)
+    ws = msa.Workspace()
+    nbytes = msa.load().msa_shared_prefix_decode_workspace_size(40, 1, 64, 4)
+    buf = ws.get("shared_prefix", nbytes + 4096, DEV)
+    buf.fill_(0xff)                                  # scratch of any contents: here, NaN patterns
+    out = (torch.full_like(o1, 3.0), torch.full_like(l1, 3.0))
+    o2, l2 = msa.shared_prefix_decode(*args, workspace=ws, out=out)
+    assert o2.data_ptr() == out[0].data_ptr()
+    assert torch.equal(o1.view(torch.int16), o2.view(torch.int16)) and torch.equal(l1, l2)
+    assert (buf[nbytes:] == 0xff).all()              # nothing written past the stated size
+    o3, l3 = msa.shared_prefix_decode(*args, with_lse=False)
+    assert l3 is None and torch.equal(o1.view(torch.int16), o3.view(torch.int16))
+    for k, x in d.items():
+        assert torch.equal(x.view(torch.int16), copies[k].view(torch.int16))
+
+
+def test_captured_decode_replays_with_other_lengths_and_two_graphs_overlap():
+    cases = [([900, 1000, 640, 777], 640), ([1100, 0, 700, 701], 512), ([64, 65, 66, 67], 64)]
+    ws = [make_decode(seq, sh, 1, 32, 4, seed=20 + i) for i, (seq, sh) in enumerate(cases)]
+    pages = max(w["kc"].shape[0] for w in ws)
+    mb = max(w["table"].shape[1] for w in ws)
+
+    def buffers():
+        return dict(q=torch.zeros((4, 32, D), dtype=torch.bfloat16, device=DEV),
+                    kc=torch.zeros((pages, PAGE, 4, D), dtype=torch.bfloat16, device=DEV),
+                    vc=torch.zeros((pages, PAGE, 4, D), dtype=torch.bfloat16, device=DEV),
+                    table=torch.zeros((4, mb), dtype=torch.int32, device=DEV),
+                    seq=torch.zeros(4, dtype=torch.int32, device=DEV),
+                    sl=torch.zeros(1, dtype=torch.int32, device=DEV))
+
+    def fill(d, w):
+        for k in ("q", "kc", "vc", "table", "seq"):
+            x = w[k]
+            d[k][tuple(slice(0, n) for n in x.shape)] = x.to(DEV)
+        d["sl"].fill_(w["shared"])
+
+    sets, graphs, outs = [buffers(), buffers()], [], []
+    for d in sets:
+        fill(d, ws[0])
+        call = lambda: msa.shared_prefix_decode(d["q"], d["kc"], d["vc"], d["table"], d["seq"], d["sl"])
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call())
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for a, b in ((0, 1), (1, 2), (2, 0)):
+        fill(sets[0], ws[a])
+        fill(sets[1], ws[b])
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        check_decode(outs[0], ref_decode(ws[a]))
+        check_decode(outs[1], ref_decode(ws[b]))
+
+
+def test_out_of_range_page_reads_page_zero():
+    w = make_decode([300, 520], 256, 1, 16, 2, seed=9)
+    bad = dict(w, table=w["table"].clone())
+    bad["table"][1, 3] = w["kc"].shape[0] + 5
+    bad["table"][0, 2] = -1
+    ref = dict(w, table=w["table"].clone())
+    ref["table"][1, 3] = 0
+    ref["table"][0, 2] = 0
+    for c in ("kc", "vc"):
+        ref[c] = torch.nan_to_num(w[c], nan=0.25)
+        bad[c] = ref[c]
+    got = run_decode(bad)
+    assert msa.device_error() == BAD_PAGE
+    check_decode(got, ref_decode(ref))
+
+
+def test_length_past_the_table_is_clamped():
+    w = make_decode([256, 384], 128, 1, 16, 2, seed=10)
+    bad = dict(w, seq=i32([256, 5000]))
+    got = run_decode(bad)
+    assert msa.device_error() == BAD_LEN
+    check_decode(got, ref_decode(w))
+
+
+# ------------------------------------------------------------------------------ together
+
+def test_steps_of_a_batch_behind_a_cached_prompt():
+    """Prompt once, then admission on its pages, chunks and decode steps: tables, append and the
+    shared decode against attention over the tokens kept on the host; the sparse path reads the
+    same caches (with every block selected it equals the dense answer)."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    Hq, Hkv, Di, B, P, mb = 16, 2, 64, 5, 64, 12
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV).to(torch.bfloat16)
+    kc, vc = (torch.full((P, PAGE, Hkv, D), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    xc = torch.zeros((P, PAGE, Hkv, Di), dtype=torch.bfloat16, device=DEV)
+    free = torch.randperm(P, generator=g, device=DEV).to(torch.int32)
+    used = torch.zeros(1, dtype=torch.int32, device=DEV)
+    # the prompt: 384 tokens of one request
+    t0 = torch.zeros((1, mb), dtype=torch.int32, device=DEV)
+    n = 384
+    pk, pv, px = rnd(n, Hkv, D), rnd(n, Hkv, D), rnd(n, Hkv, Di)
+    _, _, slots, _, used = msa.build_page_tables(i32([0]).to(DEV), i32([n]).to(DEV), t0, free, used,
+                                                 T=n, num_pages=P)
+    msa.append_kv(pk, pv, px, slots, kc, vc, xc)
+    shared_pages = t0[0, :3].clone()
+    # five requests behind it; the last is a padding row
+    table = torch.zeros((B, mb), dtype=torch.int32, device=DEV)
+    lens = i32([n, n, n, n, 0]).to(DEV)
+    hist = [[pk.cpu()] for _ in range(4)], [[pv.cpu()] for _ in range(4)]
+    for step, new in enumerate(([200, 1, 130, 64, 0], [1, 1, 1, 1, 0], [1, 1, 1, 1, 0], [3, 3, 3, 3, 0])):
+        T = sum(new) + 6
+        k, v, x = rnd(T, Hkv, D), rnd(T, Hkv, D), rnd(T, Hkv, Di)
+        lens, cu, slots, _, used = msa.build_page_tables(
+            lens, i32(new).to(DEV), table, free, used, T=T, num_pages=P,
+            shared_pages=shared_pages if step == 0 else None)
+        msa.append_kv(k, v, x, slots, kc, vc, xc)
+        at = 0
+        for b in range(4):
+            hist[0][b].append(k[at:at + new[b]].cpu())
+            hist[1][b].append(v[at:at + new[b]].cpu())
+            at += new[b]
+        assert lens.tolist() == [sum(len(c) for c in hist[0][b]) for b in range(4)] + [0]
+        N = 1 if step < 3 else 3
+        q = (rnd(B * N, Hq, D).float() * D ** -0.5).to(torch.bfloat16)
+        got = msa.shared_prefix_decode(q, kc, vc, table, lens, i32([n]).to(DEV), N=N)
+        # the same keys as a contiguous one-request-per-page-run cache on the host
+        flat = dict(q=q.cpu(), seq=lens.cpu(), N=N,
+                    table=torch.arange(B * mb, dtype=torch.int32).view(B, mb),
+                    kc=torch.zeros((B * mb, PAGE, Hkv, D), dtype=torch.bfloat16),
+                    vc=torch.zeros((B * mb, PAGE, Hkv, D), dtype=torch.bfloat16))
+        for c, h in zip(("kc", "vc"), hist):
+            for b in range(4):
+                rows = torch.cat(h[b])
+                flat[c].view(B, mb * PAGE, Hkv, D)[b, :len(rows)] = rows
+        ref = ref_decode(flat)
+        check_decode(got, ref)
+        if N == 1:  # the sparse path over every block of the same caches
+            qi = rnd(4, Hkv, Di)
+            ids, _ = msa.index_score_topk(qi, xc, table[:4].contiguous(), lens[:4].contiguous(), N=1, topk=mb)
+            fpt, kl = msa.build_sparse_page_table(ids, table[:4].contiguous(), lens[:4].contiguous(), N=1,
+                                                  num_pages=P)
+            o, lse = msa.paged_sparse_decode(q[:4].contiguous(), torch.nan_to_num(kc), torch.nan_to_num(vc),
+                                             fpt, kl)
+            check = [r[:4] for r in ref]
+            assert (lse.double().cpu() - check[1]).abs().max() <= 1e-3
+            assert (o.double().cpu() - check[0]).abs().max() <= 2e-2

@@ -1,0 +1,112 @@
+"""The serving-batch entry points without a GPU: every refusal happens on the host, before any
+device work, through the C ABI and through the Python binding."""
+import ctypes
+
+import pytest
+import torch
+
+import block_sparse_attention_msa_gb300 as msa
+
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: every call below fails host validation
+OUT = [ctypes.c_void_p(0x2000 + 0x100 * i) for i in range(6)]
+ARG, SHAPE, UNSUPPORTED, WORKSPACE = -1, -2, -3, -4
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from block_sparse_attention_msa_gb300 import build
+    build.build()
+    return msa.load()
+
+
+def tables(lib, **kw):
+    a = dict(prev=FAKE, new=FAKE, B=4, mb=8, table=OUT[5], free=FAKE, nfree=10, used=FAKE, shared=None,
+             nshared=0, pages=64, T=16, seq=OUT[0], cu=OUT[1], slots=OUT[2], pos=OUT[3], out=OUT[4])
+    a.update(kw)
+    return lib.msa_build_page_tables(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(prev=None), ARG), (dict(new=None), ARG), (dict(table=None), ARG), (dict(free=None), ARG),
+    (dict(used=None), ARG), (dict(nshared=2), ARG), (dict(seq=None), ARG), (dict(cu=None), ARG),
+    (dict(slots=None), ARG), (dict(pos=None), ARG), (dict(out=None), ARG),
+    (dict(B=-1), ARG), (dict(B=0), ARG), (dict(T=-1), ARG), (dict(mb=0), ARG), (dict(nfree=-1), ARG),
+    (dict(nshared=-1), ARG), (dict(pages=0), ARG),
+    (dict(seq=FAKE), ARG), (dict(out=FAKE), ARG), (dict(table=FAKE), ARG),    # an output is an input
+    (dict(shared=FAKE, nshared=9), SHAPE),
+    (dict(B=16385), UNSUPPORTED), (dict(pages=1 << 24), UNSUPPORTED),
+    (dict(mb=1 << 24), UNSUPPORTED), (dict(B=16384, mb=1 << 18), UNSUPPORTED),
+])
+def test_page_tables_refuse(lib, change, code):
+    assert tables(lib, **change) == code
+    assert lib.msa_last_error()
+
+
+def append(lib, **kw):
+    a = dict(k=FAKE, ks=1024, v=FAKE, vs=1024, x=FAKE, xs=1024, slots=FAKE, T=4, Hkv=8, D=128, Di=128,
+             pages=16, kc=OUT[0], vc=OUT[1], xc=OUT[2])
+    a.update(kw)
+    return lib.msa_append_kv(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(k=None), ARG), (dict(v=None), ARG), (dict(k=None, v=None, x=None), ARG), (dict(slots=None), ARG),
+    (dict(kc=None), ARG), (dict(vc=None), ARG), (dict(xc=None), ARG), (dict(T=-1), ARG),
+    (dict(pages=0), ARG), (dict(ks=1028), ARG), (dict(vs=-8), ARG), (dict(xs=4), ARG),
+    (dict(k=ctypes.c_void_p(0x1008)), ARG), (dict(xc=ctypes.c_void_p(0x1002)), ARG),
+    (dict(Hkv=3), UNSUPPORTED), (dict(Hkv=32), UNSUPPORTED), (dict(D=64), UNSUPPORTED),
+    (dict(Di=96), UNSUPPORTED), (dict(pages=1 << 24), UNSUPPORTED),
+])
+def test_append_refuses(lib, change, code):
+    assert append(lib, **change) == code
+    assert lib.msa_last_error()
+
+
+def decode(lib, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, table=FAKE, seq=FAKE, shared=FAKE, B=4, N=1, Hq=64, Hkv=8, D=128, mb=16,
+             pages=64, o=FAKE, lse=None, ws=ctypes.c_void_p(0x10000), nbytes=1 << 30)
+    a.update(kw)
+    return lib.msa_shared_prefix_decode(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(q=None), ARG), (dict(k=None), ARG), (dict(v=None), ARG), (dict(table=None), ARG),
+    (dict(seq=None), ARG), (dict(shared=None), ARG), (dict(o=None), ARG), (dict(B=-1), ARG),
+    (dict(N=0), ARG), (dict(mb=0), ARG), (dict(pages=0), ARG), (dict(q=ctypes.c_void_p(0x1008)), ARG),
+    (dict(N=17), UNSUPPORTED), (dict(D=64), UNSUPPORTED), (dict(Hkv=3, Hq=24), UNSUPPORTED),
+    (dict(Hq=60), UNSUPPORTED), (dict(Hq=256), UNSUPPORTED), (dict(Hq=0), UNSUPPORTED),
+    (dict(pages=1 << 24), UNSUPPORTED), (dict(mb=1 << 24), UNSUPPORTED),
+    (dict(B=1 << 16, mb=1 << 13), UNSUPPORTED), (dict(B=1 << 30), UNSUPPORTED),
+    (dict(ws=None), WORKSPACE), (dict(nbytes=1024), WORKSPACE),
+    (dict(ws=ctypes.c_void_p(0x10010)), WORKSPACE),
+])
+def test_decode_refuses(lib, change, code):
+    assert decode(lib, **change) == code
+    assert lib.msa_last_error()
+
+
+def test_empty_batches_are_a_no_op(lib):
+    assert tables(lib, B=0, T=0) == 0
+    assert append(lib, T=0) == 0
+    assert decode(lib, B=0) == 0
+
+
+def test_decode_workspace_size(lib):
+    size = lib.msa_shared_prefix_decode_workspace_size
+    # at least one fp32 partial of every row
+    assert size(64, 1, 64, 8) >= 64 * 64 * 128 * 4
+    assert size(256, 4, 64, 8) > size(256, 1, 64, 8) > size(1, 1, 64, 8) > 0
+    for bad in ((0, 1, 64, 8), (4, 0, 64, 8), (4, 17, 64, 8), (4, 1, 60, 8), (4, 1, 0, 8), (4, 1, 96, 3)):
+        assert size(*bad) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_shapes(lib):
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        msa.build_page_tables(i, i, torch.zeros((2, 4), dtype=torch.int32), i, i[:1], T=2, num_pages=4)
+    b = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    c = torch.zeros((1, 128, 8, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        msa.append_kv(b, b, None, i, c, c, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        msa.shared_prefix_decode(b, c, c, torch.zeros((2, 1), dtype=torch.int32), i, i[:1])
