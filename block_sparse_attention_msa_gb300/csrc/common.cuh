@@ -83,17 +83,20 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parit
       : "memory");
   return done != 0;
 }
-// Non-blocking test of a phase's completion.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+// Non-blocking test of a phase's completion (by shared-memory address, or by pointer).
+__device__ __forceinline__ bool mbar_test_addr(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n .reg .pred p;\n"
       " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  return mbar_test_addr(smem_u32(bar), parity);
 }
 // Bounded wait: true when the phase with the given parity completed, false on timeout.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {

@@ -36,27 +36,29 @@ namespace msa {
 
 namespace {
 
-constexpr int kThreads = 384;                    // 4 control warps, 2 softmax warpgroups
+constexpr int kThreads = 416;                    // 4 control warps, 2 softmax warpgroups, 1 more issuer
 constexpr int kStep = 64;                        // keys per step
 constexpr uint32_t kQHalf = 128 * 128;           // 128 rows x 64 channels bf16
 constexpr uint32_t kQTile = 2 * kQHalf;
 constexpr uint32_t kKvHalf = kStep * 128;        // 64 keys x 64 channels bf16
-constexpr uint32_t kSlot = 2 * kKvHalf;          // K or V of one step: 16 KB
-constexpr int kRing = 10;                        // slots of a pair of tiles; half per private lane
-constexpr int kLaneRing = kRing / 2;
+constexpr uint32_t kKvTile = 2 * kKvHalf;        // K or V of one step: 16 KB
+constexpr uint32_t kStage = 2 * kKvTile;         // one load stage: V(i) and K(i + 2)
+constexpr int kRing = 5;                         // stages of a pair of tiles
+constexpr int kLaneRing = 2;                     // stages of a private lane
 constexpr uint32_t kOffRing = 2 * kQTile;
-constexpr uint32_t kOffBar = kOffRing + kRing * kSlot;
+constexpr uint32_t kOffBar = kOffRing + kRing * kStage;
+constexpr int kSmallRows = 64;                   // request tiles up to this are double-buffered
 constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;                 // log2 headroom before O is rescaled
-constexpr uint32_t kIssuerNap = 100;             // ns an idle MMA issuer blocks on a barrier
 
 struct Bars {
   uint64_t kv_full[kRing], kv_empty[kRing];
-  uint64_t q_full[2], q_empty[2], o_free[2];
-  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][step & 1]
-  uint64_t drained;
+  uint64_t q_full[2][2], q_empty[2][2];  // [lane][segment & 1]
+  uint64_t s_full[2][2], p_full[2][2];  // [lane][step & 1]
+  uint64_t o_full[2], o_free[2];        // per segment: O complete, O read
+  uint64_t drained[2];
   uint32_t tmem_base;
   int32_t fail;
   // plan
@@ -202,29 +204,71 @@ struct Walker {
   }
 };
 
-// Loads are queued in the order the MMAs use them: K0, K1, V0, K2, V1, ..., V(n-1).
-__device__ __forceinline__ int32_t seq_of_v(int32_t i, int32_t n) {
-  return i < n - 1 ? 2 * i + 2 : 2 * n - 1;
-}
-// Position in a ring of `len` slots: slot and the parity of its current use.
+// A worker of n steps loads n + 1 stages, in the order in which the MMAs use them: stage 0 holds
+// K(0) and K(1), stage i + 1 holds V(i) and K(i + 2).
 struct RingPos {
   int32_t slot;
-  uint32_t use;
-  __device__ __forceinline__ void advance(int32_t k, int32_t len) {
-    slot += k;
-    if (slot >= len) {
-      slot -= len;
-      ++use;
+  uint32_t phase;  // parity of the slot's current use
+  __device__ __forceinline__ void advance(int32_t len) {
+    if (++slot == len) {
+      slot = 0;
+      phase ^= 1u;
     }
   }
 };
 
+// Bounded wait of a converged warp; every thread gets the same answer. The flag that another
+// role's timeout sets is read only while the phase is open: on the way through a barrier that
+// has completed it would cost a second shared-memory trip.
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
-  if (*fail) return false;
-  if (mbar_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *fail != 0)) return false;
+  }
   msa_record_error(kErrTimeout);
   *fail = 1;
   return false;
+}
+
+// S = Q K^T: eight K-16 products of 128-byte-swizzled tiles whose channel halves lie kQHalf and
+// kKvHalf apart, issued by one elected lane of the converged warp.
+__device__ __forceinline__ void issue_s(uint32_t d, uint64_t qd, uint64_t kd, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 t, 0, 1;\n setp.eq.b32 f, 0, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, %4;\n add.s64 b, %2, %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, %4 + 2;\n add.s64 b, %2, %5 + 2;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, %4 + 4;\n add.s64 b, %2, %5 + 4;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, %4 + 6;\n add.s64 b, %2, %5 + 6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(d),
+      "l"(qd), "l"(kd), "r"(idesc), "n"(kQHalf >> 4), "n"(kKvHalf >> 4)
+      : "memory");
+}
+// O (+)= P V: four K-16 products, P in tensor memory (8 columns per 16 keys), V rows 2 KB apart.
+__device__ __forceinline__ void issue_o(uint32_t d, uint32_t p_tmem, uint64_t vd, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, t, f;\n .reg .b64 b;\n .reg .b32 a;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 t, 0, 1;\n setp.ne.b32 f, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
+      " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 16;\n add.s64 b, %2, 256;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 24;\n add.s64 b, %2, 384;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(d),
+      "r"(p_tmem), "l"(vd), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -240,25 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the join may be scheduled as CTAs of this kernel leave; it waits for all of their stores
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&B.kv_full[i], 1);
-      mbar_init(&B.kv_empty[i], 1);
-    }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&B.q_full[x], 1);
-      mbar_init(&B.q_empty[x], 1);
-      mbar_init(&B.o_free[x], 4);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&B.s_full[x][i], 1);
-        mbar_init(&B.o_full[x][i], 1);
-        mbar_init(&B.p_full[x][i], 4);
-      }
-    }
-    mbar_init(&B.drained, 1);
-    B.fail = 0;
-    mbar_fence_init();
-  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&B.tmem_base)), "n"(kTmemCols)
@@ -357,12 +382,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  const bool shared = (int)blockIdx.x < pl.n_s;
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&B.kv_full[i], 1);
+      mbar_init(&B.kv_empty[i], shared ? 2 : 1);  // lanes that read the slot
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&B.o_full[x], 1);
+      mbar_init(&B.o_free[x], 4);
+      mbar_init(&B.drained[x], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&B.q_full[x][i], 1);
+        mbar_init(&B.q_empty[x][i], 1);
+        mbar_init(&B.s_full[x][i], 1);
+        mbar_init(&B.p_full[x][i], 4);
+      }
+    }
+    B.fail = 0;
+    mbar_fence_init();
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = B.tmem_base;
   const uint32_t sbase = smem_u32(smem);
-  const bool shared = (int)blockIdx.x < pl.n_s;
   const int32_t rlen = shared ? kRing : kLaneRing;
   // worker of lane X: the first n_p workers are the CTAs' lanes 0, so few steps spread over all
   auto worker_of = [&](int X) {
@@ -383,27 +427,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       Walker w;
       start(w, X);
+      const int32_t total = w.left;
       RingPos r{0, 0};
-      int32_t v_tok = 0, v_g = 0;
-      bool have_v = false, good = true;
-      auto load = [&](const CUtensorMap* map, int32_t tok, int32_t g) {
-        uint64_t* full = &B.kv_full[rbase + r.slot];
-        if (r.use > 0 && !wait_or_fail(&B.kv_empty[rbase + r.slot], (r.use - 1) & 1, fail)) return false;
-        if (lane == 0) {
-          mbar_expect_tx(full, kSlot);
-          tma_load_4d(smem + kOffRing + (rbase + r.slot) * kSlot, map, full, 0, tok, 0, g);
-        }
+      int32_t used = 0;                                 // stages begun
+      int32_t tok1 = 0, g1 = 0, tok2 = 0, g2 = 0;       // steps i - 1 and i - 2
+      bool good = true;
+      auto begin = [&](uint32_t bytes) {
+        if (used >= rlen && !wait_or_fail(&B.kv_empty[rbase + r.slot], r.phase ^ 1u, fail)) return false;
+        if (lane == 0) mbar_expect_tx(&B.kv_full[rbase + r.slot], bytes);
         __syncwarp();
-        r.advance(1, rlen);
+        ++used;
         return true;
       };
+      auto load = [&](const CUtensorMap* map, uint32_t off, int32_t tok, int32_t g) {
+        if (lane == 0)
+          tma_load_4d(smem + kOffRing + (rbase + r.slot) * kStage + off, map,
+                      &B.kv_full[rbase + r.slot], 0, tok, 0, g);
+      };
       Seg s;
+      int32_t i = 0;
       while (good && w.next(p, pl, s)) {
         const int32_t key0 = (s.kind == 2 ? pl.prefix : 0) + s.step0 * kStep;
         const int32_t* table = p.page_table + (int64_t)s.b * p.max_blocks;
         int32_t tok_l = 0;
-        for (int32_t j = 0; j < s.n && good; ++j) {
-          if ((j & 31) == 0) {  // the token rows of the next 32 steps, one per lane
+        for (int32_t j = 0; j < s.n; ++j, ++i) {
+          if ((j & 31) == 0) {  // the token rows of the next 32 steps, one per thread
             const int32_t jj = j + lane;
             bool bad = false;
             if (jj < s.n) {
@@ -416,28 +464,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
           }
           const int32_t tok = __shfl_sync(0xffffffffu, tok_l, j & 31);
-          good = load(&kmap, tok, s.g);
-          if (good && have_v) good = load(&vmap, v_tok, v_g);
-          v_tok = tok;
-          v_g = s.g;
-          have_v = true;
+          if (i == 0) {
+            begin(total > 1 ? kStage : kKvTile);
+            load(&kmap, 0, tok, s.g);
+            if (total == 1) r.advance(rlen);
+          } else if (i == 1) {
+            load(&kmap, kKvTile, tok, s.g);
+            r.advance(rlen);
+          } else {
+            if (!(good = begin(kStage))) break;
+            load(&vmap, 0, tok2, g2);
+            load(&kmap, kKvTile, tok, s.g);
+            r.advance(rlen);
+          }
+          tok2 = tok1;
+          g2 = g1;
+          tok1 = tok;
+          g1 = s.g;
         }
       }
-      if (good && have_v) load(&vmap, v_tok, v_g);
-      if (*fail) {  // let the copies in flight land before the CTA leaves
-        for (int32_t i = 0; i < rlen; ++i) {
-          const uint32_t uses = r.use + (i < r.slot ? 1u : 0u);
-          if (uses > 0) mbar_wait(&B.kv_full[rbase + i], (uses - 1) & 1);
-        }
+      if (good && total > 1 && (good = begin(kKvTile))) {
+        load(&vmap, 0, tok2, g2);
+        r.advance(rlen);
+      }
+      if (good && total > 0 && (good = begin(kKvTile))) {
+        load(&vmap, 0, tok1, g1);
+        r.advance(rlen);
+      }
+      if (!good) {  // let the copies in flight land before the CTA leaves
+        for (int32_t k = max(0, used - rlen); k < used; ++k)
+          mbar_wait(&B.kv_full[rbase + k % rlen], (k / rlen) & 1);
       }
     }
     __syncwarp();
   } else if (warp == 3) {
     // ================================================================ query tiles
+    // Tiles of at most 64 rows alternate between two halves of the lane's query area, so that the
+    // next request's rows are there before the current one's last S.
     Walker w[2];
     Seg s[2];
     bool more[2];
     int32_t done[2] = {0, 0};
+    bool alone[2] = {true, true};  // the last tile loaded fills the area
 #pragma unroll
     for (int X = 0; X < 2; ++X) {
       start(w[X], X);
@@ -449,21 +517,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int X = 0; X < 2; ++X) {
         if (!more[X]) continue;
-        if (done[X] > 0 &&
-            !__all_sync(0xffffffffu, mbar_test(&B.q_empty[X], (done[X] - 1) & 1)))
+        const bool req = s[X].kind == 2, small = req && p.rows_u <= kSmallRows;
+        // the segment whose S must have completed before this tile's rows may be overwritten
+        const int32_t after = done[X] - (small && !alone[X] ? 2 : 1);
+        if (after >= 0 &&
+            !__all_sync(0xffffffffu, mbar_test(&B.q_empty[X][after & 1], (after >> 1) & 1)))
           continue;
+        uint64_t* full = &B.q_full[X][done[X] & 1];
         if (lane == 0) {
-          uint8_t* dst = smem + X * kQTile;
-          const bool req = s[X].kind == 2;
+          uint8_t* dst = smem + X * kQTile + (small ? (done[X] & 1) * kSmallRows * 128 : 0);
           const CUtensorMap* map = req ? &qmap_u : &qmap_t;
           const int32_t tile = s[X].kind == 0 ? 2 * s[X].u + X : 2 * p.pairs;
           const int32_t r0 = req ? s[X].b * p.N + s[X].u * p.tpt : tile * p.tpt;
-          mbar_expect_tx(&B.q_full[X], (req ? p.rows_u : 128) * 256);
-          tma_load_5d(dst, map, &B.q_full[X], 0, 0, r0, 0, s[X].g);
-          tma_load_5d(dst + kQHalf, map, &B.q_full[X], 0, 0, r0, 1, s[X].g);
+          mbar_expect_tx(full, (req ? p.rows_u : 128) * 256);
+          tma_load_5d(dst, map, full, 0, 0, r0, 0, s[X].g);
+          tma_load_5d(dst + kQHalf, map, full, 0, 0, r0, 1, s[X].g);
         }
         __syncwarp();
         ++done[X];
+        alone[X] = !small;
         more[X] = w[X].next(p, pl, s[X]);
         progress = true;
       }
@@ -479,110 +551,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (*fail)
+    if (more[0] || more[1])  // gave up: let the copies in flight land before the CTA leaves
       for (int X = 0; X < 2; ++X)
-        if (done[X] > 0) mbar_wait(&B.q_full[X], (done[X] - 1) & 1);
+        for (int32_t k = max(0, done[X] - 2); k < done[X]; ++k)
+          mbar_wait(&B.q_full[X][k & 1], (k >> 1) & 1);
     __syncwarp();
-  } else if (warp == 1) {
-    // ================================================================ MMA issuer
+  } else if (warp == 1 || warp == 12) {
+    // ================================================================ MMA issuers, one per lane
     // Lane X's order: S(0), S(1), then O(i), S(i+2): S(i+2) overwrites the tensor memory from
-    // which O(i) reads P(i); the tensor pipe runs one thread's MMAs in issue order. The whole
-    // warp runs the loop in lockstep (barrier states agreed by a vote), an elected lane issues.
+    // which O(i) reads P(i); the tensor pipe runs one thread's MMAs in issue order, and the
+    // commit that signals S(i+2) covers O(i). The warp runs in lockstep, an elected lane issues.
+    // The pipe queues only a few MMAs, so the time between two groups is lost unless the other
+    // lane's group runs meanwhile: hence two issuers, and two waits and two commits per step.
+    const int X = warp == 12;
+    const int32_t rbase = shared ? 0 : X * kLaneRing;
     const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
     const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
-    Walker w[2];
-    int32_t total[2];
-    int32_t s_n[2] = {0, 0}, o_n[2] = {0, 0}, left[2] = {0, 0}, s_seg[2] = {-1, -1}, o_seg[2] = {-1, -1};
-    uint32_t first_bits[2] = {0, 0};  // bit i & 7: step i opens a segment
-    RingPos kp[2], vp[2];
-#pragma unroll
-    for (int X = 0; X < 2; ++X) {
-      start(w[X], X);
-      total[X] = w[X].left;
-      kp[X] = {0, 0};
-      vp[X] = {0, 0};
-      vp[X].advance(total[X] > 1 ? 2 : 1, rlen);
-    }
-    auto ready = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_test(bar, parity));
+    const uint64_t qd0 = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
+    const uint64_t kd0 = umma_desc_sw128(sbase + kOffRing + rbase * kStage, 16, 1024);
+    const uint64_t vd0 = umma_desc_sw128(sbase + kOffRing + rbase * kStage, kKvHalf, 1024);
+    const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
+    Walker w;
+    start(w, X);
+    const int32_t total = w.left;
+    int32_t seg = -1, left = 0;      // segment of the next S and its steps left
+    uint64_t qd = qd0;
+    uint32_t opens = 0, closes = 0;  // bit k: step i + k opens / closes a segment
+    int32_t o_seg = 0;
+    bool good = true;
+    // S of the step that bit `bit` of the flags stands for
+    auto issue_step_s = [&](int32_t i, uint64_t kd, int bit) {
+      if (left == 0) {
+        Seg s;
+        w.next(p, pl, s);
+        left = s.n;
+        ++seg;
+        qd = qd0 + (s.kind == 2 && p.rows_u <= kSmallRows ? (seg & 1) * (kSmallRows * 128 >> 4) : 0);
+        opens |= 1u << bit;
+        if (!wait_or_fail(&B.q_full[X][seg & 1], (seg >> 1) & 1, fail)) return false;
+        tmem_fence_after();
+      }
+      issue_s(s_tmem + (i & 1) * 64, qd, kd, idesc_s);
+      umma_commit_elect(&B.s_full[X][i & 1]);
+      if (--left == 0) {
+        closes |= 1u << bit;
+        umma_commit_elect(&B.q_empty[X][seg & 1]);
+      }
+      return true;
     };
-    uint32_t idle = 0;
-    while (o_n[0] < total[0] || o_n[1] < total[1]) {
-      bool progress = false;
-#pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        const int32_t rbase = shared ? 0 : X * kLaneRing;
-        // ---- O_X(i) += P_X(i) V(i)
-        if (o_n[X] < s_n[X]) {
-          const int32_t i = o_n[X];
-          const bool opens = (first_bits[X] >> (i & 7)) & 1u;
-          uint64_t* vfull = &B.kv_full[rbase + vp[X].slot];
-          if (ready(&B.p_full[X][i & 1], (i >> 1) & 1) && ready(vfull, vp[X].use & 1) &&
-              (!opens || o_seg[X] < 0 || ready(&B.o_free[X], o_seg[X] & 1))) {
-            tmem_fence_after();
-            const uint64_t bd =
-                umma_desc_sw128(sbase + kOffRing + (rbase + vp[X].slot) * kSlot, kKvHalf, 1024);
-#pragma unroll
-            for (int kk = 0; kk < kStep / 16; ++kk)
-              umma_bf16_ts_elect(tmem + 256 + X * 128, tmem + X * 128 + (i & 1) * 64 + kk * 8,
-                                 bd + kk * (2048 >> 4), idesc_o, (!opens || kk > 0) ? 1u : 0u);
-            umma_commit_elect(&B.o_full[X][i & 1]);
-            o_n[X] = i + 1;
-            if (opens) ++o_seg[X];
-            if (!shared || o_n[1 - X] >= o_n[X]) umma_commit_elect(&B.kv_empty[rbase + vp[X].slot]);
-            vp[X].advance(i + 2 < total[X] ? 2 : 1, rlen);
-            progress = true;
-          }
-        }
-        // ---- S_X(i) = Q_X K(i)^T
-        if (s_n[X] < total[X] && s_n[X] < o_n[X] + 2) {
-          const int32_t i = s_n[X];
-          if (left[X] == 0) {
-            Seg s;
-            w[X].next(p, pl, s);
-            left[X] = s.n;
-            ++s_seg[X];
-            first_bits[X] |= 1u << (i & 7);
-          }
-          uint64_t* kfull = &B.kv_full[rbase + kp[X].slot];
-          if (ready(kfull, kp[X].use & 1) && ready(&B.q_full[X], s_seg[X] & 1)) {
-            tmem_fence_after();
-            const uint64_t qd = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
-            const uint64_t kd =
-                umma_desc_sw128(sbase + kOffRing + (rbase + kp[X].slot) * kSlot, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t qoff = (kk >> 2) * kQHalf + (kk & 3) * 32;
-              const uint32_t koff = (kk >> 2) * kKvHalf + (kk & 3) * 32;
-              umma_bf16_elect(tmem + X * 128 + (i & 1) * 64, qd + (qoff >> 4), kd + (koff >> 4),
-                              idesc_s, kk > 0);
-            }
-            umma_commit_elect(&B.s_full[X][i & 1]);
-            s_n[X] = i + 1;
-            first_bits[X] &= ~(1u << ((i + 1) & 7));
-            if (--left[X] == 0) umma_commit_elect(&B.q_empty[X]);
-            if (!shared || s_n[1 - X] >= s_n[X]) umma_commit_elect(&B.kv_empty[rbase + kp[X].slot]);
-            kp[X].advance(i == 0 ? 1 : 2, rlen);
-            progress = true;
-          }
-        }
+    RingPos r{0, 0};
+    if (total > 0) {
+      good = wait_or_fail(&B.kv_full[rbase], 0, fail);
+      tmem_fence_after();
+      good = good && issue_step_s(0, kd0, 0);
+      if (total > 1) good = good && issue_step_s(1, kd0 + (kKvTile >> 4), 1);
+      if (good) umma_commit_elect(&B.kv_empty[rbase]);
+      r.advance(rlen);
+    }
+    for (int32_t i = 0; good && i < total; ++i) {
+      uint64_t* full = &B.kv_full[rbase + r.slot];
+      const uint64_t off = r.slot * (kStage >> 4);
+      if (!(good = wait_or_fail(full, r.phase, fail))) break;
+      if (opens & 1u) {
+        if (o_seg > 0 && !(good = wait_or_fail(&B.o_free[X], (o_seg - 1) & 1, fail))) break;
       }
-      if (progress) {
-        idle = 0;
-      } else {
-        const int X = (o_n[0] < s_n[0]) ? 0 : 1;
-        if (o_n[X] < s_n[X]) mbar_try_wait_hint(&B.p_full[X][o_n[X] & 1], (o_n[X] >> 1) & 1, kIssuerNap);
-        else __nanosleep(32);
-        const bool failed = __any_sync(0xffffffffu, *fail != 0);
-        if (++idle > kWaitLimit || failed) {
-          if (!failed && lane == 0) msa_record_error(kErrTimeout);
-          *fail = 1;
-          // the MMAs in flight end before tensor memory is given back
-          umma_commit_elect(&B.drained);
-          mbar_wait(&B.drained, 0);
-          break;
-        }
+      if (!(good = wait_or_fail(&B.p_full[X][i & 1], (i >> 1) & 1, fail))) break;
+      tmem_fence_after();
+      issue_o(o_tmem, s_tmem + (i & 1) * 64, vd0 + off, idesc_o, (opens & 1u) ^ 1u);
+      if (closes & 1u) {
+        umma_commit_elect(&B.o_full[X]);
+        ++o_seg;
       }
+      if (i + 2 < total && !(good = issue_step_s(i, kd0 + off + (kKvTile >> 4), 2))) break;
+      umma_commit_elect(&B.kv_empty[rbase + r.slot]);
+      r.advance(rlen);
+      opens >>= 1;
+      closes >>= 1;
+    }
+    if (!good) {  // the MMAs in flight end before tensor memory is given back
+      __syncwarp();
+      umma_commit_elect(&B.drained[X]);
+      mbar_wait(&B.drained[X], 0);
     }
     __syncwarp();
   } else {
@@ -594,11 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_tmem = tmem + lane_addr + 256 + X * 128;
     Walker w;
     start(w, X);
-    const int32_t total = w.left;
     const int32_t worker = worker_of(X);
-    int32_t n = 0;
+    int32_t n = 0, segs = 0;
     Seg s;
-    while (!*fail && w.next(p, pl, s)) {
+    while (w.next(p, pl, s)) {
+      bool good = true;
       int32_t rows, lim = INT32_MAX, lim_min = INT32_MAX;  // valid rows; visible keys of this row
       if (s.kind == 2) {
         const int32_t t0 = s.u * p.tpt;
@@ -613,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_run = -INFINITY, l = 0.f;         // running max (log2 units) and sum
       int32_t kb = (s.kind == 2 ? pl.prefix : 0) + s.step0 * kStep;
       for (int32_t j = 0; j < s.n; ++j, ++n, kb += kStep) {
-        if (!wait_or_fail(&B.s_full[X][n & 1], (n >> 1) & 1, fail)) break;
+        if (!(good = wait_or_fail(&B.s_full[X][n & 1], (n >> 1) & 1, fail))) break;
         tmem_fence_after();
         const uint32_t sb = s_tmem + (n & 1) * 64;
         float factor = 1.f;
@@ -655,8 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
           tmem_st32(sb, pk);
           if (__any_sync(0xffffffffu, need)) {
-            // the max grew by more than 2^8: rescale O once O(n-1) has completed
-            if (!wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail)) break;
+            // the max grew by more than 2^8: rescale O once O(n-1) has completed, which the release
+            // of its stage says (stage n; the slot is not released again before O(n))
+            uint64_t* bar = &B.kv_empty[(shared ? 0 : X * kLaneRing) + n % rlen];
+            if (!(good = wait_or_fail(bar, (n / rlen) & 1, fail))) break;
             tmem_fence_after();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -675,10 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the cache cells behind the request's last token may hold anything, NaN included, and
           // 0 * NaN is NaN: their V rows become zero
           const int32_t z0 = s.seq - kb;
-          const int32_t q = seq_of_v(n, total);
-          const int32_t slot = X * kLaneRing + q % kLaneRing;
-          if (!wait_or_fail(&B.kv_full[slot], (q / kLaneRing) & 1, fail)) break;
-          uint8_t* vrow = smem + kOffRing + slot * kSlot;
+          const int32_t slot = X * kLaneRing + (n + 1) % kLaneRing;
+          if (!(good = wait_or_fail(&B.kv_full[slot], ((n + 1) / kLaneRing) & 1, fail))) break;
+          uint8_t* vrow = smem + kOffRing + slot * kStage;
           for (int32_t c = z0 * 16 + row; c < kStep * 16; c += 128)
             *reinterpret_cast<uint4*>(vrow + ((c >> 3) & 1) * kKvHalf + (c >> 4) * 128 + (c & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -688,10 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.p_full[X][n & 1]);
       }
-      if (*fail) break;
-      // ---------------- the segment's partial. S of the last step says that O(n-3) has completed,
-      // so a barrier per step parity is at most one phase behind and its parity is unambiguous
-      if (!wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail)) break;
+      // ---------------- the segment's partial
+      if (!good || !wait_or_fail(&B.o_full[X], segs & 1, fail)) break;
+      ++segs;
       tmem_fence_after();
       if (act) {
         float* po;
