@@ -51,6 +51,7 @@ constexpr int kSmallRows = 64;                   // request tiles up to this are
 constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPairCost = 1300.f, kPrivateCost = 1500.f;  // cycles of a CTA per step
 constexpr float kRescale = 8.0f;                 // log2 headroom before O is rescaled
 
 struct Bars {
@@ -58,6 +59,7 @@ struct Bars {
   uint64_t q_full[2][2], q_empty[2][2];  // [lane][segment & 1]
   uint64_t s_full[2][2], p_full[2][2];  // [lane][step & 1]
   uint64_t o_full[2], o_free[2];        // per segment: O complete, O read
+  uint64_t turn[2];                     // pair: the other lane's burst has been issued
   uint64_t drained[2];
   uint32_t tmem_base;
   int32_t fail;
@@ -70,7 +72,7 @@ static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // What the join needs of the plan, written by CTA 0 of the attention kernel.
 struct PlanOut {
-  int32_t prefix, w_s, w_p, ts, tp, tpl;
+  int32_t prefix, runs, w_p, tp, tpl;
 };
 
 struct KParams {
@@ -82,6 +84,7 @@ struct KParams {
   int32_t rows_g;     // B*N*G: query rows of a group
   int32_t tpt;        // tokens per tile: 128 / G
   int32_t pairs;      // pairs of prefix tiles per group
+  int32_t abreast;    // pairs that walk the prefix together
   int32_t odd;        // 1: a last unpaired prefix tile
   int32_t units;      // tiles of one request's rows
   int32_t rows_u;     // rows of a request tile (box height): G * min(N, tpt)
@@ -103,27 +106,30 @@ __device__ __forceinline__ int32_t seq_of(const KParams& p, int b) {
 __device__ __forceinline__ int32_t private_steps(int32_t seq, int32_t prefix) {
   return seq > prefix ? (seq - prefix + kStep - 1) / kStep : 0;
 }
-// First item of worker w when `total` items are cut into n equal runs, and the worker of item x.
-__device__ __forceinline__ int32_t run_start(int32_t total, int32_t w, int32_t n) {
-  return (int32_t)((int64_t)total * w / n);
+// `total` items cut into n runs, the first total % n of them one item longer: the first item of
+// run w, and the run of item x.
+__device__ __forceinline__ int32_t run_start(uint32_t total, uint32_t w, uint32_t n) {
+  return (int32_t)(w * (total / n) + min(w, total % n));
 }
-__device__ __forceinline__ int32_t run_of(int32_t total, int32_t x, int32_t n) {
-  return (int32_t)((((int64_t)x + 1) * n - 1) / total);
+__device__ __forceinline__ int32_t run_of(uint32_t total, uint32_t x, uint32_t n) {
+  const uint32_t q = total / n, r = total % n;
+  return (int32_t)(x < r * (q + 1) ? x / (q + 1) : (x - r) / q);
 }
 
 struct Plan {
   int32_t prefix;        // tokens of the prefix pass, a multiple of kStep
   int32_t first;         // an active request (its page table gives the prefix's pages)
   int32_t nst;           // prefix steps
-  int32_t ts, tp, tpl;   // steps: paired prefix tiles; private space; of it the odd tiles
+  int32_t ts;            // prefix steps of one pair: all groups
+  int32_t tp, tpl;       // private steps; of these the odd tiles'
   int32_t n_s, n_p;      // CTAs of either kind
-  int32_t w_s, w_p;      // workers of either kind, none of them without a step
+  int32_t runs, w_p;     // runs of the ts steps, private workers: none of them without a step
 };
 
 // A run of steps of one tile.
 struct Seg {
   int32_t kind;   // 0: pair of prefix tiles, 1: odd prefix tile, 2: one request
-  int32_t index;  // tile (pair) index within its kind
+  int32_t slot;   // of its partial, within its kind
   int32_t step0, n;
   int32_t b, u, g;
   int32_t seq;    // kind 2: the request's length
@@ -131,7 +137,8 @@ struct Seg {
 
 // Walks the segments of one worker's run of steps.
 struct Walker {
-  int32_t kind, left, index, step, b, u, g, seq, nst;
+  int32_t kind, left, worker, index, step, b, u, g, seq, nst;
+  int32_t round, x0, len;  // pairs: steps left in this pair's run, the run
 
   __device__ __forceinline__ void to_request(const KParams& p, const Plan& pl, int32_t from) {
     kind = 2;
@@ -146,22 +153,38 @@ struct Walker {
     }
     if (b >= p.B) left = 0;
   }
-  // Worker w of its kind; sb/srem: request and offset in it where the run starts, when it
-  // starts in a request.
-  __device__ __forceinline__ void init(const KParams& p, const Plan& pl, bool shared, int32_t w,
-                                       int32_t sb, int32_t srem) {
-    const int32_t n = shared ? pl.w_s : pl.w_p, total = shared ? pl.ts : pl.tp;
-    const int32_t x0 = w < n ? run_start(total, w, n) : 0;
-    left = w < n ? run_start(total, w + 1, n) - x0 : 0;
-    u = g = b = seq = 0;
-    if (shared || x0 < pl.tpl) {
-      kind = shared ? 0 : 1;
+  // A CTA of pairs: run cta / abreast of the prefix steps, for the pairs cta % abreast,
+  // + abreast, ... So the pairs abreast read the same keys at the same time and DRAM once.
+  __device__ __forceinline__ void init_pairs(const KParams& p, const Plan& pl, int32_t cta) {
+    kind = 0;
+    worker = cta / p.abreast;
+    u = cta % p.abreast;
+    nst = pl.nst;
+    x0 = len = left = 0;
+    if (worker < pl.runs && u < p.pairs) {
+      x0 = run_start(pl.ts, worker, pl.runs);
+      len = run_start(pl.ts, worker + 1, pl.runs) - x0;
+      left = len * ((p.pairs - 1 - u) / p.abreast + 1);
+      g = x0 / nst;
+      step = x0 % nst;
+    }
+    round = len;
+  }
+  // Private worker w; sb/srem: request and offset in it where its run starts, when it starts in
+  // a request.
+  __device__ __forceinline__ void init_private(const KParams& p, const Plan& pl, int32_t w, int32_t sb,
+                                               int32_t srem) {
+    worker = w;
+    const int32_t start = w < pl.w_p ? run_start(pl.tp, w, pl.w_p) : 0;
+    left = w < pl.w_p ? run_start(pl.tp, w + 1, pl.w_p) - start : 0;
+    u = g = b = seq = index = step = nst = 0;
+    if (start < pl.tpl) {
+      kind = 1;
       nst = pl.nst;
-      index = left > 0 ? x0 / nst : 0;
-      step = left > 0 ? x0 % nst : 0;
+      index = start / nst;
+      step = start % nst;
     } else {
       kind = 2;
-      index = step = nst = 0;
       if (left > 0) {
         b = sb;
         seq = seq_of(p, b);
@@ -177,29 +200,43 @@ struct Walker {
     if (left <= 0) return false;
     s.kind = kind;
     s.step0 = step;
-    s.n = min(left, nst - step);
-    left -= s.n;
-    if (kind != 2) {
-      s.index = index;
+    s.u = u;
+    s.g = g;
+    if (kind == 0) {
+      s.n = min(round, nst - step);
+      s.slot = (worker + g) * p.pairs + u;
       s.b = pl.first;
-      s.u = kind == 0 ? index % p.pairs : 0;
-      s.g = kind == 0 ? index / p.pairs : index;
       s.seq = 0;
-      ++index;
       step = 0;
-      if (kind == 1 && index == p.Hkv && left > 0) to_request(p, pl, 0);
+      ++g;
+      round -= s.n;
+      if (round == 0) {
+        u += p.abreast;
+        round = len;
+        g = x0 / nst;
+        step = x0 % nst;
+      }
+    } else if (kind == 1) {
+      s.n = min(left, nst - step);
+      s.slot = worker + index;
+      s.b = pl.first;
+      s.g = index;
+      s.seq = 0;
+      step = 0;
+      ++index;
+      if (index == p.Hkv && left > s.n) to_request(p, pl, 0);
     } else {
-      s.index = (b * p.units + u) * p.Hkv + g;
+      s.n = min(left, nst - step);
+      s.slot = worker + (b * p.units + u) * p.Hkv + g;
       s.b = b;
-      s.u = u;
-      s.g = g;
       s.seq = seq;
       step = 0;
       if (++g == p.Hkv) {
         g = 0;
-        if (++u == p.units && left > 0) to_request(p, pl, b + 1);
+        if (++u == p.units && left > s.n) to_request(p, pl, b + 1);
       }
     }
+    left -= s.n;
     return true;
   }
 };
@@ -230,28 +267,37 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, vol
   return false;
 }
 
-// S = Q K^T: eight K-16 products of 128-byte-swizzled tiles whose channel halves lie kQHalf and
-// kKvHalf apart, issued by one elected lane of the converged warp.
-__device__ __forceinline__ void issue_s(uint32_t d, uint64_t qd, uint64_t kd, uint32_t idesc) {
+// The same for three barriers at once: a part of the warp tests each.
+__device__ __forceinline__ bool wait_three_or_fail(uint32_t bar0, uint32_t par0, uint32_t bar1,
+                                                   uint32_t par1, uint32_t bar2, uint32_t par2,
+                                                   volatile int32_t* fail) {
+  const uint32_t part = (threadIdx.x >> 3) & 3;
+  const uint32_t bar = part == 0 ? bar0 : (part == 1 ? bar1 : bar2);
+  const uint32_t par = part == 0 ? par0 : (part == 1 ? par1 : par2);
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_addr(bar, par))) return true;
+    if (__any_sync(0xffffffffu, *fail != 0)) return false;
+  }
+  msa_record_error(kErrTimeout);
+  *fail = 1;
+  return false;
+}
+
+// Half of S = Q K^T: the four K-16 products of one channel half of 128-byte-swizzled tiles, issued
+// by one elected lane of the converged warp.
+__device__ __forceinline__ void issue_s(uint32_t d, uint64_t qd, uint64_t kd, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n"
-      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 t, 0, 1;\n setp.eq.b32 f, 0, 1;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 t, 0, 1;\n setp.ne.b32 f, %4, 0;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
       " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
       " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
       " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.s64 a, %1, %4;\n add.s64 b, %2, %5;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.s64 a, %1, %4 + 2;\n add.s64 b, %2, %5 + 2;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.s64 a, %1, %4 + 4;\n add.s64 b, %2, %5 + 4;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.s64 a, %1, %4 + 6;\n add.s64 b, %2, %5 + 6;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(d),
-      "l"(qd), "l"(kd), "r"(idesc), "n"(kQHalf >> 4), "n"(kKvHalf >> 4)
+      "l"(qd), "l"(kd), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // O (+)= P V: four K-16 products, P in tensor memory (8 columns per 16 keys), V rows 2 KB apart.
@@ -275,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap qmap_t,
                          const __grid_constant__ CUtensorMap qmap_u,
                          const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap, const KParams p) {
+                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ KParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -290,46 +336,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (tid == 0) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+    tma_prefetch_desc(&qmap_t);
+    tma_prefetch_desc(&qmap_u);
+  }
   // ------------------------------------------------------------------ plan
   Plan pl;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int pb0 = min(p.B, tid * per), pb1 = min(p.B, pb0 + per);
   {
+    const int32_t want = p.shared_len[0];
+    const int32_t seq0 = pb0 < pb1 ? seq_of(p, pb0) : 0;
+    auto seq_at = [&](int b) { return b == pb0 ? seq0 : seq_of(p, b); };
     int32_t vis = INT32_MAX, first = INT32_MAX;  // keys every active row sees; first active request
-    bool bad = false;
     for (int b = pb0; b < pb1; ++b) {
-      const int32_t s = seq_of(p, b);
-      bad |= s != p.seq_lens[b];
+      const int32_t s = seq_at(b);
       if (s > 0) {
         vis = min(vis, max(0, s - p.N + 1));
         first = min(first, b);
       }
     }
-    if (bad && blockIdx.x == 0) msa_record_error(kErrBadBlock);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      vis = min(vis, __shfl_xor_sync(0xffffffffu, vis, o));
-      first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-    }
+    vis = __reduce_min_sync(0xffffffffu, vis);
+    first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) {
       B.w_min[warp] = vis;
       B.w_first[warp] = first;
     }
     __syncthreads();
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       vis = min(vis, B.w_min[w]);
       first = min(first, B.w_first[w]);
     }
     const bool any = first != INT32_MAX;
     pl.first = any ? first : 0;
-    const int32_t want = p.shared_len[0];
     pl.prefix = any ? max(0, min(want, vis)) / kStep * kStep : 0;
     pl.nst = pl.prefix / kStep;
-    pl.ts = p.Hkv * p.pairs * pl.nst;
+    pl.ts = p.pairs > 0 ? p.Hkv * pl.nst : 0;
     pl.tpl = p.odd ? p.Hkv * pl.nst : 0;
+    const int32_t tiles = p.units * p.Hkv;
     int32_t sum = 0;
-    for (int b = pb0; b < pb1; ++b) sum += private_steps(seq_of(p, b), pl.prefix);
-    sum *= p.units * p.Hkv;
+    for (int b = pb0; b < pb1; ++b) sum += private_steps(seq_at(b), pl.prefix) * tiles;
     int32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -339,17 +388,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) B.w_sum[warp] = incl;
     __syncthreads();
     int32_t before = incl - sum, total = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += B.w_sum[w];
       total += B.w_sum[w];
     }
     pl.tp = pl.tpl + total;
+    // CTAs of either kind: the split whose slower side is faster. Weights are the measured times
+    // of one step of one CTA (cycles): a pair's step is bound by its MMAs, a private one by HBM.
     const int32_t C = gridDim.x;
-    if (pl.ts == 0) pl.n_p = C;
-    else if (pl.tp == 0) pl.n_p = 0;
-    else pl.n_p = min(C - 1, (int32_t)(((int64_t)C * pl.tp + pl.ts + pl.tp - 1) / ((int64_t)pl.ts + pl.tp)));
-    pl.n_s = C - pl.n_p;
-    pl.w_s = min(pl.n_s, pl.ts);
+    if (pl.ts == 0) {
+      pl.runs = 0;
+    } else {
+      const float cs = kPairCost * p.pairs * pl.ts, cp = kPrivateCost * pl.tp;
+      const int32_t most = max(1, (C - (pl.tp > 0 ? 1 : 0)) / p.abreast);
+      auto slower = [&](int32_t runs) {
+        const int32_t n = runs * p.abreast;
+        return fmaxf(cs / n, pl.tp > 0 ? cp / max(1, C - n) : 0.f);
+      };
+      const int32_t lo = max(1, min(most, (int32_t)(C * (cs / (cs + cp)) / p.abreast)));
+      const int32_t hi = min(most, lo + 1);
+      pl.runs = min(pl.ts, slower(lo) <= slower(hi) ? lo : hi);
+    }
+    pl.n_s = pl.runs * p.abreast;
+    pl.n_p = C - pl.n_s;
     pl.w_p = min(2 * pl.n_p, pl.tp);
     // where the two lanes of this CTA start, when they start in a request
     const bool priv = (int)blockIdx.x >= pl.n_s;
@@ -362,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int32_t rem = at - before;
         int b = pb0;
         for (; b < pb1; ++b) {
-          const int32_t c = private_steps(seq_of(p, b), pl.prefix) * p.units * p.Hkv;
+          const int32_t c = private_steps(seq_at(b), pl.prefix) * tiles;
           if (rem < c) break;
           rem -= c;
         }
@@ -372,13 +434,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (blockIdx.x == 0) {
       int32_t c = before;
+      bool bad = false;
       for (int b = pb0; b < pb1; ++b) {
         p.cum[b] = c;
-        c += private_steps(seq_of(p, b), pl.prefix) * p.units * p.Hkv;
+        c += private_steps(seq_at(b), pl.prefix) * tiles;
+        bad |= seq_at(b) != p.seq_lens[b];
       }
+      if (bad) msa_record_error(kErrBadBlock);
       if (tid == 0) {
         p.cum[p.B] = total;
-        *p.plan = {pl.prefix, pl.w_s, pl.w_p, pl.ts, pl.tp, pl.tpl};
+        *p.plan = {pl.prefix, pl.runs, pl.w_p, pl.tp, pl.tpl};
       }
     }
   }
@@ -386,11 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&B.kv_full[i], 1);
-      mbar_init(&B.kv_empty[i], shared ? 2 : 1);  // lanes that read the slot
+      mbar_init(&B.kv_empty[i], shared ? 2 : 1);  // lanes that read the stage
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&B.o_full[x], 1);
       mbar_init(&B.o_free[x], 4);
+      mbar_init(&B.turn[x], 1);
       mbar_init(&B.drained[x], 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&B.q_full[x][i], 1);
@@ -408,12 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = B.tmem_base;
   const uint32_t sbase = smem_u32(smem);
   const int32_t rlen = shared ? kRing : kLaneRing;
-  // worker of lane X: the first n_p workers are the CTAs' lanes 0, so few steps spread over all
-  auto worker_of = [&](int X) {
-    return shared ? (int32_t)blockIdx.x : X * pl.n_p + (int32_t)blockIdx.x - pl.n_s;
-  };
+  // the first n_p private workers are the CTAs' lanes 0, so few steps spread over all CTAs
   auto start = [&](Walker& w, int X) {
-    w.init(p, pl, shared, worker_of(X), B.start_b[X], B.start_rem[X]);
+    if (shared) w.init_pairs(p, pl, blockIdx.x);
+    else w.init_private(p, pl, X * pl.n_p + (int32_t)blockIdx.x - pl.n_s, B.start_b[X], B.start_rem[X]);
   };
 
   if (warp == 0 || warp == 2) {
@@ -421,10 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int X = warp >> 1;
     const int32_t rbase = shared ? 0 : X * kLaneRing;
     if (!(shared && X == 1)) {
-      if (lane == 0) {
-        tma_prefetch_desc(&kmap);
-        tma_prefetch_desc(&vmap);
-      }
       Walker w;
       start(w, X);
       const int32_t total = w.left;
@@ -561,8 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Lane X's order: S(0), S(1), then O(i), S(i+2): S(i+2) overwrites the tensor memory from
     // which O(i) reads P(i); the tensor pipe runs one thread's MMAs in issue order, and the
     // commit that signals S(i+2) covers O(i). The warp runs in lockstep, an elected lane issues.
-    // The pipe queues only a few MMAs, so the time between two groups is lost unless the other
-    // lane's group runs meanwhile: hence two issuers, and two waits and two commits per step.
+    // The pipe queues only a few MMAs, so an issuer's waits between two bursts idle it unless the
+    // other lane's burst runs meanwhile. The lanes of a pair therefore take turns, a whole burst
+    // each: left alone their MMAs interleave, both lanes' softmax start together and both issuers
+    // wait together (a two-lane step of 1250 cycles of MMAs took 1760; 2080 with one issuer).
     const int X = warp == 12;
     const int32_t rbase = shared ? 0 : X * kLaneRing;
     const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
@@ -580,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t o_seg = 0;
     bool good = true;
     // S of the step that bit `bit` of the flags stands for
-    auto issue_step_s = [&](int32_t i, uint64_t kd, int bit) {
+    auto issue_step_s = [&](int32_t i, uint64_t kd, int bit, bool pass_turn) {
       if (left == 0) {
         Seg s;
         w.next(p, pl, s);
@@ -591,8 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_or_fail(&B.q_full[X][seg & 1], (seg >> 1) & 1, fail)) return false;
         tmem_fence_after();
       }
-      issue_s(s_tmem + (i & 1) * 64, qd, kd, idesc_s);
+#ifndef PASS
+#define PASS 1
+#endif
+      if (PASS == 0) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
+      issue_s(s_tmem + (i & 1) * 64, qd, kd, idesc_s, 0);
+      if (PASS == 1) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
+      issue_s(s_tmem + (i & 1) * 64, qd + (kQHalf >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
+      if (PASS == 2) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
       umma_commit_elect(&B.s_full[X][i & 1]);
+      if (PASS == 3) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
       if (--left == 0) {
         closes |= 1u << bit;
         umma_commit_elect(&B.q_empty[X][seg & 1]);
@@ -602,31 +672,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     RingPos r{0, 0};
     if (total > 0) {
       good = wait_or_fail(&B.kv_full[rbase], 0, fail);
+      if (shared && X == 1) good = good && wait_or_fail(&B.turn[1], 0, fail);
       tmem_fence_after();
-      good = good && issue_step_s(0, kd0, 0);
-      if (total > 1) good = good && issue_step_s(1, kd0 + (kKvTile >> 4), 1);
+      good = good && issue_step_s(0, kd0, 0, shared && total == 1);
+      if (total > 1) good = good && issue_step_s(1, kd0 + (kKvTile >> 4), 1, shared);
       if (good) umma_commit_elect(&B.kv_empty[rbase]);
       r.advance(rlen);
     }
+    const uint32_t full0 = smem_u32(&B.kv_full[rbase]);
+    const uint32_t p0 = smem_u32(&B.p_full[X][0]), turn = smem_u32(&B.turn[X]);
     for (int32_t i = 0; good && i < total; ++i) {
-      uint64_t* full = &B.kv_full[rbase + r.slot];
       const uint64_t off = r.slot * (kStage >> 4);
-      if (!(good = wait_or_fail(full, r.phase, fail))) break;
-      if (opens & 1u) {
-        if (o_seg > 0 && !(good = wait_or_fail(&B.o_free[X], (o_seg - 1) & 1, fail))) break;
-      }
-      if (!(good = wait_or_fail(&B.p_full[X][i & 1], (i >> 1) & 1, fail))) break;
-      tmem_fence_after();
-      issue_o(o_tmem, s_tmem + (i & 1) * 64, vd0 + off, idesc_o, (opens & 1u) ^ 1u);
-      if (closes & 1u) {
-        umma_commit_elect(&B.o_full[X]);
-        ++o_seg;
-      }
-      if (i + 2 < total && !(good = issue_step_s(i, kd0 + off + (kKvTile >> 4), 2))) break;
-      umma_commit_elect(&B.kv_empty[rbase + r.slot]);
+      const uint32_t bar = full0 + r.slot * 8, phase = r.phase, buf = i & 1, par = (i >> 1) & 1;
+      const bool first = opens & 1u, close = closes & 1u;
+      uint64_t* empty = &B.kv_empty[rbase + r.slot];
       r.advance(rlen);
       opens >>= 1;
       closes >>= 1;
+      if (first && o_seg > 0 && !(good = wait_or_fail(&B.o_free[X], (o_seg - 1) & 1, fail))) break;
+      // lane 0's burst i + 1 follows lane 1's burst i, lane 1's burst i + 1 lane 0's
+      if (!(good = shared ? wait_three_or_fail(bar, phase, p0 + buf * 8, par, turn, (i + X) & 1, fail)
+                          : wait_three_or_fail(bar, phase, p0 + buf * 8, par, bar, phase, fail)))
+        break;
+      tmem_fence_after();
+      issue_o(o_tmem, s_tmem + buf * 64, vd0 + off, idesc_o, first ? 0u : 1u);
+      if (close) {
+        umma_commit_elect(&B.o_full[X]);
+        ++o_seg;
+      }
+      if (i + 2 < total) {
+        if (!(good = issue_step_s(i, kd0 + off + (kKvTile >> 4), 1, shared))) break;
+      } else if (shared) {
+        if (lane == 0) mbar_arrive(&B.turn[1 - X]);
+        __syncwarp();
+      }
+      umma_commit_elect(empty);
     }
     if (!good) {  // the MMAs in flight end before tensor memory is given back
       __syncwarp();
@@ -643,7 +723,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_tmem = tmem + lane_addr + 256 + X * 128;
     Walker w;
     start(w, X);
-    const int32_t worker = worker_of(X);
     int32_t n = 0, segs = 0;
     Seg s;
     while (w.next(p, pl, s)) {
@@ -747,15 +826,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2* ml;
         int32_t cap = 128;
         if (s.kind == 0) {
-          const int64_t slot = ((int64_t)worker + s.index) * 2 + X;
+          const int64_t slot = (int64_t)s.slot * 2 + X;
           po = p.po_s + slot * 128 * 128;
           ml = p.ml_s + slot * 128;
         } else if (s.kind == 1) {
-          const int64_t slot = (int64_t)worker + s.index;
+          const int64_t slot = s.slot;
           po = p.po_l + slot * 128 * 128;
           ml = p.ml_l + slot * 128;
         } else {
-          const int64_t slot = (int64_t)worker + s.index;
+          const int64_t slot = s.slot;
           cap = p.rows_u;
           po = p.po_u + slot * cap * 128;
           ml = p.ml_u + slot * cap;
@@ -791,8 +870,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------ join
 // A CTA joins eight consecutive query rows of a group; a thread owns four channels of one row,
-// so a warp reads whole 128-byte lines of the partials' [channel quad][row][4] layout.
+// so a warp reads whole 128-byte lines of the partials' [channel quad][row][4] layout. With
+// SPLIT > 1 the row's segments are dealt to SPLIT threads, four loads in flight each, and joined
+// through shared memory: few tiles over many CTAs leave a row tens of segments (8 requests on
+// 60K tokens: 38), which one thread after the other would wait for.
 constexpr int kJoinRows = 8;
+constexpr int kJoinSplit = 4;
 
 struct Parts {
   const float* o;
@@ -800,77 +883,125 @@ struct Parts {
   int64_t o_step, ml_step;  // to the next segment of the row
   int32_t n;
 };
+struct Joined {
+  float m, l;
+  float4 acc;
+};
 
-__device__ __forceinline__ void join_max(const Parts& s, float& m) {
-  for (int i = 0; i < s.n; ++i) m = fmaxf(m, s.ml[i * s.ml_step].x);
-}
-__device__ __forceinline__ void join_add(const Parts& s, float m, float& l, float4& acc) {
-#pragma unroll 4
-  for (int i = 0; i < s.n; ++i) {
-    const float2 ml = s.ml[i * s.ml_step];
-    const float4 o = *reinterpret_cast<const float4*>(s.o + i * s.o_step);
-    if (ml.x == -INFINITY && !(ml.y != ml.y)) continue;  // the row saw no key of this segment
-    const float w = ex2(ml.x - m);
-    l += w * ml.y;
-    acc.x += w * o.x;
-    acc.y += w * o.y;
-    acc.z += w * o.z;
-    acc.w += w * o.w;
+// Adds up to four parts (n of them valid) to j.
+__device__ __forceinline__ void join_four(Joined& j, const float2 (&ml)[4], const float4 (&o)[4], int n) {
+  float m = j.m;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < n) m = fmaxf(m, ml[u].x);
+  const float f = j.m == m ? 1.f : ex2(j.m - m);  // 2^(-inf) = 0 for the first parts
+  j.m = m;
+  j.l *= f;
+  j.acc.x *= f;
+  j.acc.y *= f;
+  j.acc.z *= f;
+  j.acc.w *= f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u >= n || (ml[u].x == -INFINITY && ml[u].y == 0.f)) continue;  // the row saw no key there
+    const float w = ex2(ml[u].x - m);
+    j.l += w * ml[u].y;
+    j.acc.x += w * o[u].x;
+    j.acc.y += w * o[u].y;
+    j.acc.z += w * o[u].z;
+    j.acc.w += w * o[u].w;
   }
 }
 
-__global__ void __launch_bounds__(kJoinRows * 32) shared_prefix_join_kernel(const KParams p) {
+template <int SPLIT>
+__global__ void __launch_bounds__(kJoinRows * 32 * SPLIT)
+    shared_prefix_join_kernel(const __grid_constant__ KParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t g = blockIdx.x % p.Hkv;
-  const int32_t pr = (int32_t)(blockIdx.x / p.Hkv) * kJoinRows + (threadIdx.x & (kJoinRows - 1));
-  const int32_t quad = threadIdx.x / kJoinRows;
-  if (pr >= p.rows_g) return;
-  const PlanOut pl = *p.plan;
-  const int32_t r = pr / p.G, e = pr % p.G, b = r / p.N, i = r % p.N;
-  const int32_t nst = pl.prefix / kStep;
-  Parts a{}, c{};
-  if (nst > 0 && p.seq_lens[b] > 0) {  // a padding request's rows sit in the prefix tiles too
-    const int32_t tile = pr >> 7, row = pr & 127;
-    if (tile < 2 * p.pairs) {
-      const int32_t index = g * p.pairs + (tile >> 1);
-      const int32_t w0 = run_of(pl.ts, index * nst, pl.w_s), w1 = run_of(pl.ts, index * nst + nst - 1, pl.w_s);
-      const int64_t slot = ((int64_t)w0 + index) * 2 + (tile & 1);
-      a = {p.po_s + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_s + slot * 128 + row,
-           2 * 128 * 128, 2 * 128, w1 - w0 + 1};
-    } else {
-      const int32_t w0 = run_of(pl.tp, g * nst, pl.w_p), w1 = run_of(pl.tp, g * nst + nst - 1, pl.w_p);
-      const int64_t slot = (int64_t)w0 + g;
-      a = {p.po_l + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_l + slot * 128 + row,
-           128 * 128, 128, w1 - w0 + 1};
+  const int t = threadIdx.x % (kJoinRows * 32), split = threadIdx.x / (kJoinRows * 32);
+  const int32_t pr = (int32_t)(blockIdx.x / p.Hkv) * kJoinRows + (t & (kJoinRows - 1));
+  const int32_t quad = t / kJoinRows;
+  const bool valid = pr < p.rows_g;
+  const int32_t r = valid ? pr / p.G : 0, e = pr % p.G, b = r / p.N, i = r % p.N;
+  Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (valid) {
+    const PlanOut pl = *p.plan;
+    const int32_t nst = pl.prefix / kStep;
+    const int32_t seq = p.seq_lens[b], c0 = p.cum[b], c1 = p.cum[b + 1];
+    Parts a{}, c{};
+    if (nst > 0 && seq > 0) {  // a padding request's rows sit in the prefix tiles too
+      const int32_t tile = pr >> 7, row = pr & 127;
+      if (tile < 2 * p.pairs) {
+        const int32_t ts = p.Hkv * nst;
+        const int32_t w0 = run_of(ts, g * nst, pl.runs), w1 = run_of(ts, g * nst + nst - 1, pl.runs);
+        const int64_t slot = ((int64_t)(w0 + g) * p.pairs + (tile >> 1)) * 2 + (tile & 1);
+        a = {p.po_s + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_s + slot * 128 + row,
+             (int64_t)p.pairs * 2 * 128 * 128, (int64_t)p.pairs * 2 * 128, w1 - w0 + 1};
+      } else {
+        const int32_t w0 = run_of(pl.tp, g * nst, pl.w_p), w1 = run_of(pl.tp, g * nst + nst - 1, pl.w_p);
+        const int64_t slot = (int64_t)w0 + g;
+        a = {p.po_l + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_l + slot * 128 + row,
+             128 * 128, 128, w1 - w0 + 1};
+      }
+    }
+    const int32_t per = (c1 - c0) / (p.units * p.Hkv);
+    if (per > 0) {
+      const int32_t u = i / p.tpt, row = (i - u * p.tpt) * p.G + e;
+      const int32_t x0 = pl.tpl + c0 + (u * p.Hkv + g) * per;
+      const int32_t w0 = run_of(pl.tp, x0, pl.w_p), w1 = run_of(pl.tp, x0 + per - 1, pl.w_p);
+      const int64_t slot = (int64_t)w0 + ((int64_t)b * p.units + u) * p.Hkv + g;
+      const int64_t cap = p.rows_u;
+      c = {p.po_u + ((slot * 32 + quad) * cap + row) * 4, p.ml_u + slot * cap + row, cap * 128, cap,
+           w1 - w0 + 1};
+    }
+    const int32_t n = a.n + c.n;
+    for (int32_t k = split; k < n; k += 4 * SPLIT) {
+      float2 ml[4];
+      float4 o[4];
+      int have = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int32_t x = k + u * SPLIT;
+        if (x < n) {
+          const bool pre = x < a.n;
+          const int64_t y = pre ? x : x - a.n;
+          ml[u] = __ldcs((pre ? a.ml : c.ml) + y * (pre ? a.ml_step : c.ml_step));
+          o[u] = __ldcs(reinterpret_cast<const float4*>((pre ? a.o : c.o) + y * (pre ? a.o_step : c.o_step)));
+          ++have;
+        }
+      }
+      join_four(j, ml, o, have);
     }
   }
-  const int32_t c0 = p.cum[b], per = (p.cum[b + 1] - c0) / (p.units * p.Hkv);
-  if (per > 0) {
-    const int32_t u = i / p.tpt, row = (i - u * p.tpt) * p.G + e;
-    const int32_t x0 = pl.tpl + c0 + (u * p.Hkv + g) * per;
-    const int32_t w0 = run_of(pl.tp, x0, pl.w_p), w1 = run_of(pl.tp, x0 + per - 1, pl.w_p);
-    const int64_t slot = (int64_t)w0 + ((int64_t)b * p.units + u) * p.Hkv + g;
-    const int64_t cap = p.rows_u;
-    c = {p.po_u + ((slot * 32 + quad) * cap + row) * 4, p.ml_u + slot * cap + row, cap * 128, cap,
-         w1 - w0 + 1};
+  if (SPLIT > 1) {
+    __shared__ float2 s_ml[SPLIT > 1 ? SPLIT : 1][kJoinRows * 32];
+    __shared__ float4 s_o[SPLIT > 1 ? SPLIT : 1][kJoinRows * 32];
+    s_ml[split][t] = make_float2(j.m, j.l);
+    s_o[split][t] = j.acc;
+    __syncthreads();
+    if (split > 0) return;
+    float2 ml[4];
+    float4 o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = u + 1 < SPLIT ? u + 1 : 0;
+      ml[u] = s_ml[x][t];
+      o[u] = s_o[x][t];
+    }
+    join_four(j, ml, o, SPLIT - 1);
   }
-  float m = -INFINITY, l = 0.f;
-  join_max(a, m);
-  join_max(c, m);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  join_add(a, m, l, acc);
-  join_add(c, m, l, acc);
-  const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: o = 0, lse = -inf
+  if (!valid) return;
+  const float inv = j.l == 0.f ? 0.f : 1.0f / j.l;  // a row that sees no key: o = 0, lse = -inf
   const int64_t out = (int64_t)r * p.Hq + g * p.G + e;
   uint2 u;
-  u.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-  u.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  u.x = pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
+  u.y = pack_bf16x2(j.acc.z * inv, j.acc.w * inv);
   *reinterpret_cast<uint2*>(p.o + out * 128 + quad * 4) = u;
-  if (quad == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (quad == 0 && p.lse) p.lse[out] = j.l == 0.f ? -INFINITY : (j.m + log2f(j.l)) * kLn2;
 }
 
 struct Layout {
-  int32_t rows_g, tpt, pairs, odd, units, rows_u;
+  int32_t rows_g, tpt, pairs, abreast, odd, units, rows_u;
   size_t po_s, po_l, po_u, ml_s, ml_l, ml_u, plan, cum, total;
 };
 
@@ -884,8 +1015,21 @@ Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
   y.odd = tiles & 1;
   y.units = (N + y.tpt - 1) / y.tpt;
   y.rows_u = G * (N < y.tpt ? N : y.tpt);
-  // a worker's segments of one kind have distinct worker + tile sums
-  const size_t n_s = y.pairs ? (size_t)ctas + (size_t)Hkv * y.pairs : 0;
+  // pairs that walk the prefix together: enough that DRAM feeds them (4 to 8 of the CTAs on one
+  // stream of keys), few enough that whole runs of them split the CTAs evenly, and without idle
+  // places in the last round
+  y.abreast = 1;
+  float best = 1e30f;
+  for (int32_t n = 1; n <= 16 && n <= y.pairs; ++n) {
+    const float rounds = (float)((y.pairs + n - 1) / n) * n / y.pairs;
+    const float cost = rounds * (1.f + 0.5f * n / ctas) + (n < 4 && n < y.pairs ? 0.3f * (4 - n) : 0.f);
+    if (cost < best) {
+      best = cost;
+      y.abreast = n;
+    }
+  }
+  // a worker's segments of one kind have distinct worker + tile (or worker + group) sums
+  const size_t n_s = y.pairs ? ((size_t)ctas / y.abreast + Hkv) * y.pairs : 0;
   const size_t n_l = y.odd ? (size_t)2 * ctas + Hkv : 0;
   const size_t n_u = (size_t)2 * ctas + (size_t)B * y.units * Hkv;
   size_t at = 0;
@@ -930,6 +1074,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.rows_g = y.rows_g;
   p.tpt = y.tpt;
   p.pairs = y.pairs;
+  p.abreast = y.abreast;
   p.odd = y.odd;
   p.units = y.units;
   p.rows_u = y.rows_u;
@@ -968,14 +1113,17 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.Hkv * (((int64_t)y.rows_g + kJoinRows - 1) / kJoinRows)));
-  cfg.blockDim = dim3(kJoinRows * 32);
+  // segments of a row when the prefix dominates: the workers over the tiles
+  const bool many = 2 * (int64_t)ctas > 8 * (int64_t)a.Hkv * (y.pairs + y.odd);
+  cfg.blockDim = dim3(kJoinRows * 32 * (many ? kJoinSplit : 1));
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel, p);
+  return many ? cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<kJoinSplit>, p)
+              : cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<1>, p);
 }
 
 }  // namespace msa
