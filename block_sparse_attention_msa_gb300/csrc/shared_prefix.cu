@@ -36,38 +36,65 @@ namespace msa {
 
 namespace {
 
-constexpr int kThreads = 416;                    // 4 control warps, 2 softmax warpgroups, 1 more issuer
+constexpr int kThreads = 512;                    // warpgroups: loads, softmax x 2, MMA issue
+constexpr int kLaunchRegs = 128;                 // registers per thread at launch, then split
+#ifndef RL
+#define RL 72
+#define RI 72
+#define RS 184
+#endif
+constexpr int kRegsLoad = RL;
+constexpr int kRegsIssue = RI;
+constexpr int kRegsSoftmax = RS;
 constexpr int kStep = 64;                        // keys per step
 constexpr uint32_t kQHalf = 128 * 128;           // 128 rows x 64 channels bf16
 constexpr uint32_t kQTile = 2 * kQHalf;
 constexpr uint32_t kKvHalf = kStep * 128;        // 64 keys x 64 channels bf16
 constexpr uint32_t kKvTile = 2 * kKvHalf;        // K or V of one step: 16 KB
 constexpr uint32_t kStage = 2 * kKvTile;         // one load stage: V(i) and K(i + 2)
-constexpr int kRing = 5;                         // stages of a pair of tiles
-constexpr int kLaneRing = 2;                     // stages of a private lane
-constexpr uint32_t kOffRing = 2 * kQTile;
-constexpr uint32_t kOffBar = kOffRing + kRing * kStage;
-constexpr int kSmallRows = 64;                   // request tiles up to this are double-buffered
+// shared memory: two query tiles and a ring of stages. A pair's tiles have 128 rows and leave 5
+// stages; private tiles of at most 64 rows leave 6, three per lane instead of two (a stage takes
+// 2500 cycles to arrive and a lane's step 1500).
+constexpr int kRing = 5;
+constexpr int kMaxStages = 6;
+constexpr uint32_t kOffBar = 2 * kQTile + kRing * kStage;
+static_assert(kOffBar == kQTile + kMaxStages * kStage, "the two layouts fill the same space");
 constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPairCost = 1300.f, kPrivateCost = 1500.f;  // cycles of a CTA per step
-constexpr float kRescale = 8.0f;                 // log2 headroom before O is rescaled
+constexpr float kRescale = 8.0f;                // log2 headroom before O is rescaled
+
+// A run of steps of one tile: what the roles of a lane need to know of it.
+struct __align__(16) Seg {
+  int32_t n;          // steps; 0: the lane has no more
+  int32_t key0;       // first key
+  int32_t b, g;       // page-table row, group
+  int32_t seq;        // keys the request holds (INT32_MAX in the prefix)
+  int32_t kind;       // 0: pair of prefix tiles, 1: odd prefix tile, 2: one request
+  int32_t slot;       // of the partial, within its kind
+  int32_t rows;       // valid rows of the tile
+  int32_t vis;        // keys that the tile's first row sees (INT32_MAX in the prefix)
+  int32_t total;      // steps of the whole lane
+  int32_t q_row, pad; // first query row
+};
+constexpr int kQueue = 4;  // segments a lane's feeder is ahead of the slowest reader
 
 struct Bars {
-  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[2][2], q_empty[2][2];  // [lane][segment & 1]
-  uint64_t s_full[2][2], p_full[2][2];  // [lane][step & 1]
-  uint64_t o_full[2], o_free[2];        // per segment: O complete, O read
-  uint64_t turn[2];                     // pair: the other lane's burst has been issued
-  uint64_t drained[2];
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][step & 1]
+  uint64_t o_free[2];                    // per segment: O read
+  uint64_t seg_full[2][kQueue], seg_free[2][kQueue];
+  uint64_t drained[4];
+  Seg seg[2][kQueue];
   uint32_t tmem_base;
   int32_t fail;
   // plan
   int32_t w_min[kThreads / 32], w_first[kThreads / 32], w_sum[kThreads / 32];
   int32_t start_b[2], start_rem[2];
 };
-constexpr size_t kSmemBytes = 1024 + kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
+constexpr size_t kSmemBytes = kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // What the join needs of the plan, written by CTA 0 of the attention kernel.
@@ -75,12 +102,19 @@ struct PlanOut {
   int32_t prefix, runs, w_p, tp, tpl;
 };
 
+// V maps with boxes of one channel half of 1, 2, 4, ..., 32 tokens.
+struct TailMaps {
+  CUtensorMap m[6];
+};
+__device__ uint4 g_zero_rows[kKvHalf / 16];  // never written
+
 struct KParams {
   const int32_t* page_table;
   const int32_t* seq_lens;
   const int32_t* shared_len;
   int32_t B, N, G, Hq, Hkv, max_blocks;
   int64_t num_pages;
+  int32_t gs, hs;     // log2 of G and Hkv
   int32_t rows_g;     // B*N*G: query rows of a group
   int32_t tpt;        // tokens per tile: 128 / G
   int32_t pairs;      // pairs of prefix tiles per group
@@ -88,6 +122,7 @@ struct KParams {
   int32_t odd;        // 1: a last unpaired prefix tile
   int32_t units;      // tiles of one request's rows
   int32_t rows_u;     // rows of a request tile (box height): G * min(N, tpt)
+  int32_t q_rows;     // rows of a private CTA's query areas: 64, or 128
   // partials: O as [32 channel quads][rows][4] fp32, then (m, l) per row
   float *po_s, *po_l, *po_u;
   float2 *ml_s, *ml_l, *ml_u;
@@ -126,15 +161,6 @@ struct Plan {
   int32_t runs, w_p;     // runs of the ts steps, private workers: none of them without a step
 };
 
-// A run of steps of one tile.
-struct Seg {
-  int32_t kind;   // 0: pair of prefix tiles, 1: odd prefix tile, 2: one request
-  int32_t slot;   // of its partial, within its kind
-  int32_t step0, n;
-  int32_t b, u, g;
-  int32_t seq;    // kind 2: the request's length
-};
-
 // Walks the segments of one worker's run of steps.
 struct Walker {
   int32_t kind, left, worker, index, step, b, u, g, seq, nst;
@@ -145,28 +171,29 @@ struct Walker {
     u = g = step = 0;
     b = from;
     nst = 0;
-    while (b < p.B) {
+#pragma unroll 1
+    for (; b < p.B; ++b) {
       seq = seq_of(p, b);
       nst = private_steps(seq, pl.prefix);
-      if (nst > 0) break;
-      ++b;
+      if (nst > 0) return;
     }
-    if (b >= p.B) left = 0;
+    left = 0;
   }
   // A CTA of pairs: run cta / abreast of the prefix steps, for the pairs cta % abreast,
   // + abreast, ... So the pairs abreast read the same keys at the same time and DRAM once.
   __device__ __forceinline__ void init_pairs(const KParams& p, const Plan& pl, int32_t cta) {
     kind = 0;
     worker = cta / p.abreast;
-    u = cta % p.abreast;
+    u = cta - worker * p.abreast;
     nst = pl.nst;
     x0 = len = left = 0;
     if (worker < pl.runs && u < p.pairs) {
       x0 = run_start(pl.ts, worker, pl.runs);
       len = run_start(pl.ts, worker + 1, pl.runs) - x0;
       left = len * ((p.pairs - 1 - u) / p.abreast + 1);
-      g = x0 / nst;
-      step = x0 % nst;
+      index = x0 / nst;  // the run's first group
+      g = index;
+      step = x0 -= index * nst;
     }
     round = len;
   }
@@ -178,65 +205,66 @@ struct Walker {
     const int32_t start = w < pl.w_p ? run_start(pl.tp, w, pl.w_p) : 0;
     left = w < pl.w_p ? run_start(pl.tp, w + 1, pl.w_p) - start : 0;
     u = g = b = seq = index = step = nst = 0;
-    if (start < pl.tpl) {
-      kind = 1;
+    kind = start < pl.tpl ? 1 : 2;
+    if (left > 0) {
+      int32_t rest = start;
       nst = pl.nst;
-      index = start / nst;
-      step = start % nst;
-    } else {
-      kind = 2;
-      if (left > 0) {
+      if (kind == 2) {
         b = sb;
         seq = seq_of(p, b);
         nst = private_steps(seq, pl.prefix);
-        const int32_t t = srem / nst;
-        step = srem % nst;
-        u = t / p.Hkv;
-        g = t % p.Hkv;
+        rest = srem;
       }
+      const int32_t t = rest / nst;
+      step = rest - t * nst;
+      index = t;
+      u = t >> p.hs;
+      g = t & (p.Hkv - 1);
     }
   }
-  __device__ __forceinline__ bool next(const KParams& p, const Plan& pl, Seg& s) {
+  // The next segment of lane X into s (n = 0: none is left).
+  __device__ __forceinline__ bool next(const KParams& p, const Plan& pl, int X, Seg& s) {
+    s.n = 0;
     if (left <= 0) return false;
     s.kind = kind;
-    s.step0 = step;
-    s.u = u;
+    s.n = min(kind == 0 ? round : left, nst - step);
+    left -= s.n;
+    s.key0 = step * kStep;
     s.g = g;
-    if (kind == 0) {
-      s.n = min(round, nst - step);
-      s.slot = (worker + g) * p.pairs + u;
-      s.b = pl.first;
-      s.seq = 0;
-      step = 0;
-      ++g;
-      round -= s.n;
-      if (round == 0) {
-        u += p.abreast;
-        round = len;
-        g = x0 / nst;
-        step = x0 % nst;
-      }
-    } else if (kind == 1) {
-      s.n = min(left, nst - step);
-      s.slot = worker + index;
-      s.b = pl.first;
-      s.g = index;
-      s.seq = 0;
-      step = 0;
-      ++index;
-      if (index == p.Hkv && left > s.n) to_request(p, pl, 0);
-    } else {
-      s.n = min(left, nst - step);
-      s.slot = worker + (b * p.units + u) * p.Hkv + g;
+    s.b = pl.first;
+    s.seq = s.vis = INT32_MAX;
+    step = 0;
+    if (kind == 2) {
+      const int32_t t0 = u * p.tpt;
+      s.key0 += pl.prefix;
+      s.slot = worker + (((b * p.units + u) << p.hs) | g);
       s.b = b;
       s.seq = seq;
-      step = 0;
+      s.vis = seq - p.N + t0 + 1;
+      s.rows = min(p.rows_u, (p.N - t0) << p.gs);
+      s.q_row = b * p.N + t0;
       if (++g == p.Hkv) {
         g = 0;
-        if (++u == p.units && left > s.n) to_request(p, pl, b + 1);
+        if (++u == p.units && left > 0) to_request(p, pl, b + 1);
+      }
+    } else {
+      const int32_t tile = kind == 0 ? 2 * u + X : 2 * p.pairs;
+      s.rows = min(128, p.rows_g - tile * 128);
+      s.q_row = tile * p.tpt;
+      s.slot = kind == 0 ? (worker + g) * p.pairs + u : worker + g;
+      ++g;
+      if (kind == 0) {
+        round -= s.n;
+        if (round == 0) {
+          u += p.abreast;
+          round = len;
+          g = index;
+          step = x0;
+        }
+      } else if (g == p.Hkv && left > 0) {
+        to_request(p, pl, 0);
       }
     }
-    left -= s.n;
     return true;
   }
 };
@@ -267,13 +295,16 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, vol
   return false;
 }
 
-// The same for three barriers at once: a part of the warp tests each.
-__device__ __forceinline__ bool wait_three_or_fail(uint32_t bar0, uint32_t par0, uint32_t bar1,
-                                                   uint32_t par1, uint32_t bar2, uint32_t par2,
-                                                   volatile int32_t* fail) {
-  const uint32_t part = (threadIdx.x >> 3) & 3;
-  const uint32_t bar = part == 0 ? bar0 : (part == 1 ? bar1 : bar2);
-  const uint32_t par = part == 0 ? par0 : (part == 1 ? par1 : par2);
+// A value that is the same in all threads of a converged warp, in a form that lets the compiler see
+// it: operands of tensor-core and bulk-copy instructions that it cannot prove uniform cost a loop
+// over the threads each (the issuers were 70 KB of code, and bound by it).
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// wait_or_fail for two barriers at once: half of the warp tests either.
+__device__ __forceinline__ bool wait_two_or_fail(uint32_t bar0, uint32_t par0, uint32_t bar1,
+                                                 uint32_t par1, volatile int32_t* fail) {
+  const bool lo = (threadIdx.x & 16) == 0;
+  const uint32_t bar = lo ? bar0 : bar1, par = lo ? par0 : par1;
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait_addr(bar, par))) return true;
     if (__any_sync(0xffffffffu, *fail != 0)) return false;
@@ -319,15 +350,20 @@ __device__ __forceinline__ void issue_o(uint32_t d, uint32_t p_tmem, uint64_t vd
 
 __global__ void __launch_bounds__(kThreads, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap qmap_t,
+                         const __grid_constant__ CUtensorMap qmap_o,
                          const __grid_constant__ CUtensorMap qmap_u,
                          const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ KParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+                         const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ TailMaps vtail, const __grid_constant__ KParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];  // 1024: the swizzle atoms
   Bars& B = *reinterpret_cast<Bars*>(smem + kOffBar);
   volatile int32_t* fail = &B.fail;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = uniform(tid >> 5);
+  if (smem_u32(smem) & 1023u) {  // not seen: the declared alignment is kept
+    msa_record_error(kErrTimeout);
+    return;
+  }
   // the join may be scheduled as CTAs of this kernel leave; it waits for all of their stores
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) {
@@ -341,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&vmap);
     tma_prefetch_desc(&qmap_t);
     tma_prefetch_desc(&qmap_u);
+    tma_prefetch_desc(&qmap_o);
   }
   // ------------------------------------------------------------------ plan
   Plan pl;
@@ -351,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t seq0 = pb0 < pb1 ? seq_of(p, pb0) : 0;
     auto seq_at = [&](int b) { return b == pb0 ? seq0 : seq_of(p, b); };
     int32_t vis = INT32_MAX, first = INT32_MAX;  // keys every active row sees; first active request
+#pragma unroll 1
     for (int b = pb0; b < pb1; ++b) {
       const int32_t s = seq_at(b);
       if (s > 0) {
@@ -378,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pl.tpl = p.odd ? p.Hkv * pl.nst : 0;
     const int32_t tiles = p.units * p.Hkv;
     int32_t sum = 0;
+#pragma unroll 1
     for (int b = pb0; b < pb1; ++b) sum += private_steps(seq_at(b), pl.prefix) * tiles;
     int32_t incl = sum;
 #pragma unroll
@@ -415,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pl.w_p = min(2 * pl.n_p, pl.tp);
     // where the two lanes of this CTA start, when they start in a request
     const bool priv = (int)blockIdx.x >= pl.n_s;
-#pragma unroll
+#pragma unroll 1
     for (int x = 0; x < 2; ++x) {
       const int32_t wk = x * pl.n_p + (int)blockIdx.x - pl.n_s;
       if (!priv || wk >= pl.w_p) break;
@@ -423,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (at >= before && at < before + sum) {
         int32_t rem = at - before;
         int b = pb0;
+#pragma unroll 1
         for (; b < pb1; ++b) {
           const int32_t c = private_steps(seq_at(b), pl.prefix) * tiles;
           if (rem < c) break;
@@ -435,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0) {
       int32_t c = before;
       bool bad = false;
+#pragma unroll 1
       for (int b = pb0; b < pb1; ++b) {
         p.cum[b] = c;
         c += private_steps(seq_at(b), pl.prefix) * tiles;
@@ -449,48 +490,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const bool shared = (int)blockIdx.x < pl.n_s;
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&B.kv_full[i], 1);
       mbar_init(&B.kv_empty[i], shared ? 2 : 1);  // lanes that read the stage
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&B.o_full[x], 1);
       mbar_init(&B.o_free[x], 4);
-      mbar_init(&B.turn[x], 1);
-      mbar_init(&B.drained[x], 1);
+      for (int i = 0; i < kQueue; ++i) {
+        mbar_init(&B.seg_full[x][i], 1);
+        // readers: four softmax warps, two issuers, a K/V producer (a pair has one, on lane 0)
+        mbar_init(&B.seg_free[x][i], shared && x == 1 ? 6 : 7);
+      }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&B.q_full[x][i], 1);
         mbar_init(&B.q_empty[x][i], 1);
         mbar_init(&B.s_full[x][i], 1);
+        mbar_init(&B.o_full[x][i], 1);
         mbar_init(&B.p_full[x][i], 4);
       }
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&B.drained[i], 1);
     B.fail = 0;
     mbar_fence_init();
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = B.tmem_base;
+  const uint32_t tmem = uniform((int32_t)B.tmem_base);
   const uint32_t sbase = smem_u32(smem);
-  const int32_t rlen = shared ? kRing : kLaneRing;
-  // the first n_p private workers are the CTAs' lanes 0, so few steps spread over all CTAs
-  auto start = [&](Walker& w, int X) {
-    if (shared) w.init_pairs(p, pl, blockIdx.x);
-    else w.init_private(p, pl, X * pl.n_p + (int32_t)blockIdx.x - pl.n_s, B.start_b[X], B.start_rem[X]);
+  const bool wide = shared || p.q_rows == 128;          // query areas of 128 rows
+  const uint32_t q_half = wide ? kQHalf : kQHalf / 2;   // a channel half of one
+  const uint32_t off_ring = 4 * q_half;
+  const int32_t lane_ring = wide ? 2 : 3;               // stages of a private lane
+  const int32_t rlen = shared ? kRing : lane_ring;
+  // request tiles that leave half of their area free are double-buffered
+  const bool twice = !shared && 2 * p.rows_u <= p.q_rows;
+  static_assert(128 * (kRegsLoad + kRegsIssue) + 256 * kRegsSoftmax == kThreads * kLaunchRegs,
+                "register split");
+  // The next segment of lane X (its k-th) for one of its readers.
+  auto take = [&](int X, int32_t& k, Seg& s) {
+    const int q = k & (kQueue - 1);
+    if (!wait_or_fail(&B.seg_full[X][q], (k / kQueue) & 1, fail)) return false;
+    const Seg& e = B.seg[X][q];
+    s = {uniform(e.n),    uniform(e.key0), uniform(e.b),   uniform(e.g),     uniform(e.seq),   uniform(e.kind),
+         uniform(e.slot), uniform(e.rows), uniform(e.vis), uniform(e.total), uniform(e.q_row), 0};
+    __syncwarp();
+    mbar_arrive_if(&B.seg_free[X][q], lane == 0);
+    ++k;
+    return true;
   };
-
-  if (warp == 0 || warp == 2) {
-    // ================================================================ K/V producers
-    const int X = warp >> 1;
-    const int32_t rbase = shared ? 0 : X * kLaneRing;
-    if (!(shared && X == 1)) {
-      Walker w;
-      start(w, X);
-      const int32_t total = w.left;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    const int X = warp & 1;
+    const int32_t rbase = shared ? 0 : X * lane_ring;
+    if (warp < 2 && !(shared && X == 1)) {
+      // ============================================================== K/V producers
+      // warp 0 for lane 0 or a pair, warp 1 for lane 1
       RingPos r{0, 0};
       int32_t used = 0;                                 // stages begun
-      int32_t tok1 = 0, g1 = 0, tok2 = 0, g2 = 0;       // steps i - 1 and i - 2
+      int32_t tok1 = 0, g1 = 0, z1 = 0, tok2 = 0, g2 = 0, z2 = 0;  // steps i - 1 and i - 2
       bool good = true;
       auto begin = [&](uint32_t bytes) {
         if (used >= rlen && !wait_or_fail(&B.kv_empty[rbase + r.slot], r.phase ^ 1u, fail)) return false;
@@ -501,245 +559,256 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto load = [&](const CUtensorMap* map, uint32_t off, int32_t tok, int32_t g) {
         if (lane == 0)
-          tma_load_4d(smem + kOffRing + (rbase + r.slot) * kStage + off, map,
+          tma_load_4d(smem + off_ring + (rbase + r.slot) * kStage + off, map,
                       &B.kv_full[rbase + r.slot], 0, tok, 0, g);
       };
-      Seg s;
-      int32_t i = 0;
-      while (good && w.next(p, pl, s)) {
-        const int32_t key0 = (s.kind == 2 ? pl.prefix : 0) + s.step0 * kStep;
-        const int32_t* table = p.page_table + (int64_t)s.b * p.max_blocks;
-        int32_t tok_l = 0;
-        for (int32_t j = 0; j < s.n; ++j, ++i) {
-          if ((j & 31) == 0) {  // the token rows of the next 32 steps, one per thread
-            const int32_t jj = j + lane;
-            bool bad = false;
-            if (jj < s.n) {
-              const int32_t key = key0 + jj * kStep;
-              int32_t page = table[key / MSA_BLOCK_TOKENS];
-              bad = page < 0 || page >= p.num_pages;
-              if (bad) page = 0;
-              tok_l = page * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+      // V of step i - 2, of which the first z2 rows are the request's. The cache cells behind its
+      // last token may hold anything, NaN included, and 0 * NaN is NaN, so those rows are not
+      // loaded: zeros come in their place, by the same engine.
+      auto load_v = [&]() {
+        if (z2 >= kStep) {
+          load(&vmap, 0, tok2, g2);
+          return;
+        }
+        if (lane < 2) {  // one channel half each
+          uint8_t* dst = smem + off_ring + (rbase + r.slot) * kStage + lane * kKvHalf;
+          uint64_t* full = &B.kv_full[rbase + r.slot];
+          int32_t at = 0;
+#pragma unroll 1
+          for (int b = 5; b >= 0; --b)
+            if (z2 >> b & 1) {
+              tma_load_4d(dst + at * 128, &vtail.m[b], full, 0, tok2 + at, lane, g2);
+              at += 1 << b;
             }
+          bulk_load(dst + at * 128, g_zero_rows, (kStep - at) * 128, full);
+        }
+        __syncwarp();
+      };
+      // the token rows of 32 steps from j on, one per thread
+      auto look_up = [&](const Seg& s, int32_t j) {
+        const int32_t jj = j + lane, key = s.key0 + jj * kStep;
+        return jj < s.n ? p.page_table[(int64_t)s.b * p.max_blocks + key / MSA_BLOCK_TOKENS] : 0;
+      };
+      int32_t k = 0, i = 0, total = 0;
+      Seg s, ahead;
+      good = take(X, k, s);
+      int32_t page = 0, page_ahead = 0;
+      if (good) {
+        total = s.total;
+        page = look_up(s, 0);
+      }
+#pragma unroll 1
+      while (good && s.n > 0) {
+        if (!(good = take(X, k, ahead))) break;
+        page_ahead = look_up(ahead, 0);  // arrives while this segment is loaded
+#pragma unroll 1
+        for (int32_t j = 0; j < s.n; ++j, ++i) {
+          if (j > 0 && (j & 31) == 0) page = look_up(s, j);
+          if ((j & 31) == 0) {
+            const bool bad = page < 0 || page >= p.num_pages;
+            if (bad) page = 0;
             if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
           }
-          const int32_t tok = __shfl_sync(0xffffffffu, tok_l, j & 31);
+          const int32_t key = s.key0 + j * kStep;
+          const int32_t tok = __shfl_sync(0xffffffffu, page, j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
           if (i == 0) {
             begin(total > 1 ? kStage : kKvTile);
             load(&kmap, 0, tok, s.g);
             if (total == 1) r.advance(rlen);
-          } else if (i == 1) {
-            load(&kmap, kKvTile, tok, s.g);
-            r.advance(rlen);
           } else {
-            if (!(good = begin(kStage))) break;
-            load(&vmap, 0, tok2, g2);
+            if (i > 1) {
+              if (!(good = begin(kStage))) break;
+              load_v();
+            }
             load(&kmap, kKvTile, tok, s.g);
             r.advance(rlen);
           }
           tok2 = tok1;
           g2 = g1;
+          z2 = z1;
           tok1 = tok;
           g1 = s.g;
+          z1 = s.seq - key;
         }
+        s = ahead;
+        page = page_ahead;
       }
-      if (good && total > 1 && (good = begin(kKvTile))) {
-        load(&vmap, 0, tok2, g2);
-        r.advance(rlen);
-      }
-      if (good && total > 0 && (good = begin(kKvTile))) {
-        load(&vmap, 0, tok1, g1);
-        r.advance(rlen);
-      }
-      if (!good) {  // let the copies in flight land before the CTA leaves
-        for (int32_t k = max(0, used - rlen); k < used; ++k)
-          mbar_wait(&B.kv_full[rbase + k % rlen], (k / rlen) & 1);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 3) {
-    // ================================================================ query tiles
-    // Tiles of at most 64 rows alternate between two halves of the lane's query area, so that the
-    // next request's rows are there before the current one's last S.
-    Walker w[2];
-    Seg s[2];
-    bool more[2];
-    int32_t done[2] = {0, 0};
-    bool alone[2] = {true, true};  // the last tile loaded fills the area
-#pragma unroll
-    for (int X = 0; X < 2; ++X) {
-      start(w[X], X);
-      more[X] = w[X].next(p, pl, s[X]);
-    }
-    uint32_t idle = 0;
-    while (more[0] || more[1]) {
-      bool progress = false;
-#pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        if (!more[X]) continue;
-        const bool req = s[X].kind == 2, small = req && p.rows_u <= kSmallRows;
-        // the segment whose S must have completed before this tile's rows may be overwritten
-        const int32_t after = done[X] - (small && !alone[X] ? 2 : 1);
-        if (after >= 0 &&
-            !__all_sync(0xffffffffu, mbar_test(&B.q_empty[X][after & 1], (after >> 1) & 1)))
-          continue;
-        uint64_t* full = &B.q_full[X][done[X] & 1];
-        if (lane == 0) {
-          uint8_t* dst = smem + X * kQTile + (small ? (done[X] & 1) * kSmallRows * 128 : 0);
-          const CUtensorMap* map = req ? &qmap_u : &qmap_t;
-          const int32_t tile = s[X].kind == 0 ? 2 * s[X].u + X : 2 * p.pairs;
-          const int32_t r0 = req ? s[X].b * p.N + s[X].u * p.tpt : tile * p.tpt;
-          mbar_expect_tx(full, (req ? p.rows_u : 128) * 256);
-          tma_load_5d(dst, map, full, 0, 0, r0, 0, s[X].g);
-          tma_load_5d(dst + kQHalf, map, full, 0, 0, r0, 1, s[X].g);
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) {  // the last two steps' V
+        if (good && total > 1 - e && (good = begin(kKvTile))) {
+          load_v();
+          r.advance(rlen);
         }
-        __syncwarp();
-        ++done[X];
-        alone[X] = !small;
-        more[X] = w[X].next(p, pl, s[X]);
-        progress = true;
+        tok2 = tok1;
+        g2 = g1;
+        z2 = z1;
       }
-      if (progress) {
-        idle = 0;
-      } else {
-        __nanosleep(64);
-        if (__any_sync(0xffffffffu, *fail != 0)) break;
-        if (++idle > kWaitLimit) {
-          if (lane == 0) msa_record_error(kErrTimeout);
-          *fail = 1;
-          break;
-        }
-      }
-    }
-    if (more[0] || more[1])  // gave up: let the copies in flight land before the CTA leaves
-      for (int X = 0; X < 2; ++X)
-        for (int32_t k = max(0, done[X] - 2); k < done[X]; ++k)
-          mbar_wait(&B.q_full[X][k & 1], (k >> 1) & 1);
-    __syncwarp();
-  } else if (warp == 1 || warp == 12) {
-    // ================================================================ MMA issuers, one per lane
-    // Lane X's order: S(0), S(1), then O(i), S(i+2): S(i+2) overwrites the tensor memory from
-    // which O(i) reads P(i); the tensor pipe runs one thread's MMAs in issue order, and the
-    // commit that signals S(i+2) covers O(i). The warp runs in lockstep, an elected lane issues.
-    // The pipe queues only a few MMAs, so an issuer's waits between two bursts idle it unless the
-    // other lane's burst runs meanwhile. The lanes of a pair therefore take turns, a whole burst
-    // each: left alone their MMAs interleave, both lanes' softmax start together and both issuers
-    // wait together (a two-lane step of 1250 cycles of MMAs took 1760; 2080 with one issuer).
-    const int X = warp == 12;
-    const int32_t rbase = shared ? 0 : X * kLaneRing;
-    const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
-    const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
-    const uint64_t qd0 = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
-    const uint64_t kd0 = umma_desc_sw128(sbase + kOffRing + rbase * kStage, 16, 1024);
-    const uint64_t vd0 = umma_desc_sw128(sbase + kOffRing + rbase * kStage, kKvHalf, 1024);
-    const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
-    Walker w;
-    start(w, X);
-    const int32_t total = w.left;
-    int32_t seg = -1, left = 0;      // segment of the next S and its steps left
-    uint64_t qd = qd0;
-    uint32_t opens = 0, closes = 0;  // bit k: step i + k opens / closes a segment
-    int32_t o_seg = 0;
-    bool good = true;
-    // S of the step that bit `bit` of the flags stands for
-    auto issue_step_s = [&](int32_t i, uint64_t kd, int bit, bool pass_turn) {
-      if (left == 0) {
+      if (!good)  // let the copies in flight land before the CTA leaves
+        for (int32_t q = max(0, used - rlen); q < used; ++q)
+          mbar_wait(&B.kv_full[rbase + q % rlen], (q / rlen) & 1);
+    } else if (warp >= 2) {
+      // ============================================================== segments and query tiles
+      // Walks the lane's segments for all of its roles (each walking them for itself made the
+      // kernel 217 KB of code, and every step waited for instructions) and loads their queries.
+      // Request tiles of at most half the lane's area alternate between its halves, so that the
+      // next request's rows are there before the current one's last S.
+      Walker w;
+      // the first n_p private workers are the CTAs' lanes 0, so few steps spread over all CTAs
+      if (shared) w.init_pairs(p, pl, blockIdx.x);
+      else w.init_private(p, pl, X * pl.n_p + (int32_t)blockIdx.x - pl.n_s, B.start_b[X], B.start_rem[X]);
+      const int32_t total = w.left;
+      int32_t k = 0, done = 0;  // segments published, query tiles loaded
+      bool good = true, alone = true;  // alone: the last tile fills the area
+      int32_t kind = -1, q_row = 0, g = 0;  // of segment k - 1
+#pragma unroll 1
+      for (bool more = true; more;) {
         Seg s;
-        w.next(p, pl, s);
-        left = s.n;
-        ++seg;
-        qd = qd0 + (s.kind == 2 && p.rows_u <= kSmallRows ? (seg & 1) * (kSmallRows * 128 >> 4) : 0);
-        opens |= 1u << bit;
-        if (!wait_or_fail(&B.q_full[X][seg & 1], (seg >> 1) & 1, fail)) return false;
-        tmem_fence_after();
-      }
-#ifndef PASS
-#define PASS 1
-#endif
-      if (PASS == 0) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
-      issue_s(s_tmem + (i & 1) * 64, qd, kd, idesc_s, 0);
-      if (PASS == 1) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
-      issue_s(s_tmem + (i & 1) * 64, qd + (kQHalf >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
-      if (PASS == 2) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
-      umma_commit_elect(&B.s_full[X][i & 1]);
-      if (PASS == 3) { if (pass_turn && lane == 0) mbar_arrive(&B.turn[1 - X]); __syncwarp(); }
-      if (--left == 0) {
-        closes |= 1u << bit;
-        umma_commit_elect(&B.q_empty[X][seg & 1]);
-      }
-      return true;
-    };
-    RingPos r{0, 0};
-    if (total > 0) {
-      good = wait_or_fail(&B.kv_full[rbase], 0, fail);
-      if (shared && X == 1) good = good && wait_or_fail(&B.turn[1], 0, fail);
-      tmem_fence_after();
-      good = good && issue_step_s(0, kd0, 0, shared && total == 1);
-      if (total > 1) good = good && issue_step_s(1, kd0 + (kKvTile >> 4), 1, shared);
-      if (good) umma_commit_elect(&B.kv_empty[rbase]);
-      r.advance(rlen);
-    }
-    const uint32_t full0 = smem_u32(&B.kv_full[rbase]);
-    const uint32_t p0 = smem_u32(&B.p_full[X][0]), turn = smem_u32(&B.turn[X]);
-    for (int32_t i = 0; good && i < total; ++i) {
-      const uint64_t off = r.slot * (kStage >> 4);
-      const uint32_t bar = full0 + r.slot * 8, phase = r.phase, buf = i & 1, par = (i >> 1) & 1;
-      const bool first = opens & 1u, close = closes & 1u;
-      uint64_t* empty = &B.kv_empty[rbase + r.slot];
-      r.advance(rlen);
-      opens >>= 1;
-      closes >>= 1;
-      if (first && o_seg > 0 && !(good = wait_or_fail(&B.o_free[X], (o_seg - 1) & 1, fail))) break;
-      // lane 0's burst i + 1 follows lane 1's burst i, lane 1's burst i + 1 lane 0's
-      if (!(good = shared ? wait_three_or_fail(bar, phase, p0 + buf * 8, par, turn, (i + X) & 1, fail)
-                          : wait_three_or_fail(bar, phase, p0 + buf * 8, par, bar, phase, fail)))
-        break;
-      tmem_fence_after();
-      issue_o(o_tmem, s_tmem + buf * 64, vd0 + off, idesc_o, first ? 0u : 1u);
-      if (close) {
-        umma_commit_elect(&B.o_full[X]);
-        ++o_seg;
-      }
-      if (i + 2 < total) {
-        if (!(good = issue_step_s(i, kd0 + off + (kKvTile >> 4), 1, shared))) break;
-      } else if (shared) {
-        if (lane == 0) mbar_arrive(&B.turn[1 - X]);
+        more = w.next(p, pl, X, s);
+        s.total = total;
+        const int q = k & (kQueue - 1);
+        if (k >= kQueue && !(good = wait_or_fail(&B.seg_free[X][q], (k / kQueue - 1) & 1, fail))) break;
+        if (lane == 0) {
+          B.seg[X][q] = s;
+          mbar_arrive(&B.seg_full[X][q]);
+        }
         __syncwarp();
+        if (k++ > 0) {  // the queries of the segment before
+          const bool small = kind == 2 && twice;
+          // the segment whose S must have completed before this tile's rows may be overwritten
+          const int32_t after = done - (small && !alone ? 2 : 1);
+          if (after >= 0 && !(good = wait_or_fail(&B.q_empty[X][after & 1], (after >> 1) & 1, fail))) break;
+          if (lane == 0) {
+            uint64_t* full = &B.q_full[X][done & 1];
+            uint8_t* dst = smem + X * 2 * q_half + (small ? (done & 1) * (q_half / 2) : 0);
+            const CUtensorMap* map = kind == 2 ? &qmap_u : (kind == 0 ? &qmap_t : &qmap_o);
+            mbar_expect_tx(full, (kind == 2 ? p.rows_u : (kind == 0 ? 128 : p.q_rows)) * 256);
+            tma_load_5d(dst, map, full, 0, 0, q_row, 0, g);
+            tma_load_5d(dst + q_half, map, full, 0, 0, q_row, 1, g);
+          }
+          __syncwarp();
+          ++done;
+          alone = !small;
+        }
+        kind = s.kind;
+        q_row = s.q_row;
+        g = s.g;
       }
-      umma_commit_elect(empty);
+      if (!good)  // let the copies in flight land before the CTA leaves
+        for (int32_t q = max(0, done - 2); q < done; ++q)
+          mbar_wait(&B.q_full[X][q & 1], (q >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    // ================================================================ MMA issuers
+    // One warp per lane and product. O(i) needs P(i) and V(i); S(i+2) needs K(i+2) and the
+    // completion of O(i), which reads P(i) from the tensor memory that S(i+2) overwrites. The
+    // tensor pipe queues only a few MMAs, and an issuer's waits and bookkeeping take as long as a
+    // group of MMAs, so it takes several issuers to keep the pipe fed.
+    const int X = (warp - 12) >> 1;
+    const bool scores = warp & 1;
+    const int32_t rbase = shared ? 0 : X * lane_ring;
+    const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
+    const uint32_t full0 = smem_u32(&B.kv_full[rbase]);
+    Seg s;
+    RingPos r{0, 0};
+    int32_t k = 0, left = 0;
+    bool good = take(X, k, s);
+    const int32_t total = good ? s.total : 0;
+    left = s.n;
+    if (scores) {
+      const uint32_t idesc = umma_idesc_bf16(128, kStep, 0, 0);
+      const uint64_t qd0 = umma_desc_sw128(sbase + X * 2 * q_half, 16, 1024);
+      const uint64_t kd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, 16, 1024);
+      const uint32_t o0 = smem_u32(&B.o_full[X][0]);
+      uint64_t qd = qd0;
+      bool opens = true;  // the next S is a segment's first
+      r.advance(rlen);
+      // S(i+2) for i = -2 ..., the first two of them from stage 0
+#pragma unroll 1
+      for (int32_t i = -2; good && i < total; ++i) {
+        const uint32_t buf = i & 1;
+        if (i + 2 < total) {
+          if (left == 0) {
+            if (!(good = take(X, k, s))) break;
+            left = s.n;
+            opens = true;
+          }
+          if (opens) {
+            const int32_t seg = k - 1;
+            qd = qd0 + (s.kind == 2 && twice ? (seg & 1) * (q_half / 2 >> 4) : 0);
+            if (!(good = wait_or_fail(&B.q_full[X][seg & 1], (seg >> 1) & 1, fail))) break;
+            opens = false;
+          }
+          uint64_t kd = kd0 + (i + 2) * (kKvTile >> 4);
+          if (i < 0) {
+            good = wait_or_fail(&B.kv_full[rbase], 0, fail);
+          } else {
+            good = wait_two_or_fail(full0 + r.slot * 8, r.phase, o0 + buf * 8, (i >> 1) & 1, fail);
+            kd = kd0 + r.slot * (kStage >> 4) + (kKvTile >> 4);
+          }
+          if (!good) break;
+          tmem_fence_after();
+          issue_s(s_tmem + buf * 64, qd, kd, idesc, 0);
+          issue_s(s_tmem + buf * 64, qd + (q_half >> 4), kd + (kKvHalf >> 4), idesc, 1);
+          umma_commit_elect(&B.s_full[X][buf]);
+          if (--left == 0) umma_commit_elect(&B.q_empty[X][(k - 1) & 1]);
+          // stage 0 is free after its last S, stage i + 1 after O(i) and S(i+2)
+          if (i >= 0) umma_commit_elect(&B.kv_empty[rbase + r.slot]);
+          else if (i == -1 || total == 1) umma_commit_elect(&B.kv_empty[rbase]);
+        } else if (i >= 0) {
+          if (!(good = wait_or_fail(&B.o_full[X][buf], (i >> 1) & 1, fail))) break;
+          mbar_arrive_if(&B.kv_empty[rbase + r.slot], lane == 0);
+        }
+        if (i >= 0) r.advance(rlen);
+      }
+    } else {
+      const uint32_t idesc = umma_idesc_bf16(128, 128, 0, 1);
+      const uint64_t vd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, kKvHalf, 1024);
+      const uint32_t p0 = smem_u32(&B.p_full[X][0]);
+      uint32_t accumulate = 0;
+      r.advance(rlen);
+#pragma unroll 1
+      for (int32_t i = 0; good && i < total; ++i) {
+        const uint32_t buf = i & 1;
+        if (left == 0) {
+          if (!(good = take(X, k, s) && wait_or_fail(&B.o_free[X], k & 1, fail))) break;
+          left = s.n;
+          accumulate = 0;
+        }
+        if (!(good = wait_two_or_fail(full0 + r.slot * 8, r.phase, p0 + buf * 8, (i >> 1) & 1, fail))) break;
+        tmem_fence_after();
+        issue_o(o_tmem, s_tmem + buf * 64, vd0 + r.slot * (kStage >> 4), idesc, accumulate);
+        umma_commit_elect(&B.o_full[X][buf]);
+        accumulate = 1;
+        r.advance(rlen);
+        --left;
+      }
     }
     if (!good) {  // the MMAs in flight end before tensor memory is given back
-      __syncwarp();
-      umma_commit_elect(&B.drained[X]);
-      mbar_wait(&B.drained[X], 0);
+      umma_commit_elect(&B.drained[warp - 12]);
+      mbar_wait(&B.drained[warp - 12], 0);
     }
     __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ================================================================ softmax + partials
     const int X = (warp - 4) >> 2;
     const int row = (tid - 128) & 127;  // tile row = tensor memory lane
     const uint32_t lane_addr = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_tmem = tmem + lane_addr + X * 128;
     const uint32_t o_tmem = tmem + lane_addr + 256 + X * 128;
-    Walker w;
-    start(w, X);
-    int32_t n = 0, segs = 0;
+    const int32_t token = row >> p.gs;
+    int32_t n = 0, k = 0;
     Seg s;
-    while (w.next(p, pl, s)) {
-      bool good = true;
-      int32_t rows, lim = INT32_MAX, lim_min = INT32_MAX;  // valid rows; visible keys of this row
-      if (s.kind == 2) {
-        const int32_t t0 = s.u * p.tpt;
-        rows = min(p.rows_u, p.N * p.G - t0 * p.G);
-        lim_min = s.seq - p.N + t0 + 1;
-        lim = lim_min + row / p.G;
-      } else {
-        const int32_t tile = s.kind == 0 ? 2 * s.u + X : 2 * p.pairs;
-        rows = min(128, p.rows_g - tile * 128);
-      }
-      const bool act = 32 * (warp & 3) < rows;  // a warp of padding rows only keeps the barriers
-      float m_run = -INFINITY, l = 0.f;         // running max (log2 units) and sum
-      int32_t kb = (s.kind == 2 ? pl.prefix : 0) + s.step0 * kStep;
+    bool good = true;
+#pragma unroll 1
+    while (good && take(X, k, s) && s.n > 0) {
+      const bool act = 32 * (warp & 3) < s.rows;  // a warp of padding rows only keeps the barriers
+      const bool mine = row < s.rows;  // the rows behind hold whatever the query area held before
+      float m_run = -INFINITY, l = 0.f;  // running max (log2 units) and sum
+      int32_t kb = s.key0;
+#pragma unroll 1
       for (int32_t j = 0; j < s.n; ++j, ++n, kb += kStep) {
         if (!(good = wait_or_fail(&B.s_full[X][n & 1], (n >> 1) & 1, fail))) break;
         tmem_fence_after();
@@ -751,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(sb, v);
           tmem_ld32(sb + 32, v + 32);
           tmem_wait_ld();
-          if (kb + kStep > lim_min) {  // uniform: the step holds a key some row does not see
-            const int32_t vis = lim - kb;
+          if (s.vis - kb < kStep) {  // uniform: the step holds a key some row does not see
+            const int32_t vis = s.vis + token - kb;
 #pragma unroll
             for (int x = 0; x < kStep; ++x)
               if (x >= vis) v[x] = -INFINITY;
@@ -763,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m2 = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * kLog2e;
           if (m_run == -INFINITY) {
             m_run = m2;  // nothing in O yet
-          } else if (m2 > m_run + kRescale) {
+          } else if (mine && m2 > m_run + kRescale) {
             factor = ex2(m_run - m2);
             need = true;
             m_run = m2;
@@ -783,79 +852,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
           tmem_st32(sb, pk);
           if (__any_sync(0xffffffffu, need)) {
-            // the max grew by more than 2^8: rescale O once O(n-1) has completed, which the release
-            // of its stage says (stage n; the slot is not released again before O(n))
-            uint64_t* bar = &B.kv_empty[(shared ? 0 : X * kLaneRing) + n % rlen];
-            if (!(good = wait_or_fail(bar, (n / rlen) & 1, fail))) break;
+            // the max grew by more than 2^8: rescale O once O(n-1) has completed (S(n) says that
+            // O(n-2) has, so the barrier's parity is unambiguous)
+            if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
             tmem_fence_after();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float o[32];
-              tmem_ld32(o_tmem + c * 32, o);
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o_tmem + c * 16, o);
               tmem_wait_ld();
-              uint32_t ob[32];
 #pragma unroll
-              for (int x = 0; x < 32; ++x) ob[x] = __float_as_uint(o[x] * factor);
-              tmem_st32(o_tmem + c * 32, ob);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * factor);
+              tmem_st16(o_tmem + c * 16, o);
             }
           }
           tmem_wait_st();
         }
-        if (s.kind == 2 && kb + kStep > s.seq) {
-          // the cache cells behind the request's last token may hold anything, NaN included, and
-          // 0 * NaN is NaN: their V rows become zero
-          const int32_t z0 = s.seq - kb;
-          const int32_t slot = X * kLaneRing + (n + 1) % kLaneRing;
-          if (!(good = wait_or_fail(&B.kv_full[slot], ((n + 1) / kLaneRing) & 1, fail))) break;
-          uint8_t* vrow = smem + kOffRing + slot * kStage;
-          for (int32_t c = z0 * 16 + row; c < kStep * 16; c += 128)
-            *reinterpret_cast<uint4*>(vrow + ((c >> 3) & 1) * kKvHalf + (c >> 4) * 128 + (c & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.p_full[X][n & 1]);
+        mbar_arrive_if(&B.p_full[X][n & 1], lane == 0);
       }
+      if (!good) break;
       // ---------------- the segment's partial
-      if (!good || !wait_or_fail(&B.o_full[X], segs & 1, fail)) break;
-      ++segs;
-      tmem_fence_after();
-      if (act) {
-        float* po;
+      float4* po = nullptr;
+      int32_t cap = 128;
+      if (mine) {
         float2* ml;
-        int32_t cap = 128;
         if (s.kind == 0) {
           const int64_t slot = (int64_t)s.slot * 2 + X;
-          po = p.po_s + slot * 128 * 128;
+          po = reinterpret_cast<float4*>(p.po_s + slot * 128 * 128);
           ml = p.ml_s + slot * 128;
         } else if (s.kind == 1) {
-          const int64_t slot = s.slot;
-          po = p.po_l + slot * 128 * 128;
-          ml = p.ml_l + slot * 128;
+          po = reinterpret_cast<float4*>(p.po_l + (int64_t)s.slot * 128 * 128);
+          ml = p.ml_l + (int64_t)s.slot * 128;
         } else {
-          const int64_t slot = s.slot;
           cap = p.rows_u;
-          po = p.po_u + slot * cap * 128;
-          ml = p.ml_u + slot * cap;
+          po = reinterpret_cast<float4*>(p.po_u + (int64_t)s.slot * cap * 128);
+          ml = p.ml_u + (int64_t)s.slot * cap;
         }
-        const bool mine = row < rows;
-        if (mine) ml[row] = make_float2(m_run, l);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(o_tmem + c * 32, v);
-          tmem_wait_ld();
-          if (mine)
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<float4*>(po + ((int64_t)(c * 8 + x) * cap + row) * 4) =
-                  make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-        }
+        ml[row] = make_float2(m_run, l);
+        po += row;
       }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.o_free[X]);
+      if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
+      tmem_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float o[64];
+        if (act) {
+          tmem_ld32(o_tmem + c * 64, o);
+          tmem_ld32(o_tmem + c * 64 + 32, o + 32);
+          tmem_wait_ld();
+        }
+        if (c == 1) {  // all of O is read: the next segment may overwrite it
+          tmem_fence_before();
+          __syncwarp();
+          mbar_arrive_if(&B.o_free[X], lane == 0);
+        }
+        if (mine)
+#pragma unroll
+          for (int x = 0; x < 16; ++x, po += cap)
+            *po = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+      }
     }
   }
   // ------------------------------------------------------------------ teardown
@@ -1001,7 +1058,7 @@ __global__ void __launch_bounds__(kJoinRows * 32 * SPLIT)
 }
 
 struct Layout {
-  int32_t rows_g, tpt, pairs, abreast, odd, units, rows_u;
+  int32_t rows_g, tpt, pairs, abreast, odd, units, rows_u, q_rows;
   size_t po_s, po_l, po_u, ml_s, ml_l, ml_u, plan, cum, total;
 };
 
@@ -1015,6 +1072,7 @@ Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
   y.odd = tiles & 1;
   y.units = (N + y.tpt - 1) / y.tpt;
   y.rows_u = G * (N < y.tpt ? N : y.tpt);
+  y.q_rows = y.rows_u <= 64 && y.rows_g - 256 * y.pairs <= 64 ? 64 : 128;
   // pairs that walk the prefix together: enough that DRAM feeds them (4 to 8 of the CTAs on one
   // stream of keys), few enough that whole runs of them split the CTAs evenly, and without idle
   // places in the last round
@@ -1069,6 +1127,8 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.G = G;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
+  while ((1 << p.gs) < G) ++p.gs;
+  while ((1 << p.hs) < a.Hkv) ++p.hs;
   p.max_blocks = a.max_blocks;
   p.num_pages = a.num_pages;
   p.rows_g = y.rows_g;
@@ -1078,6 +1138,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.odd = y.odd;
   p.units = y.units;
   p.rows_u = y.rows_u;
+  p.q_rows = y.q_rows;
   uint8_t* w = a.workspace;
   p.plan = reinterpret_cast<PlanOut*>(w + y.plan);
   p.cum = reinterpret_cast<int32_t*>(w + y.cum);
@@ -1091,24 +1152,31 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.lse = a.lse;
   // query rows as (channel half, head of the group, row, half, group): a box is G heads of
   // consecutive rows, one 128-byte line each
-  CUtensorMap qt, qu, km, vm;
+  CUtensorMap qt, qo, qu, km, vm;
+  TailMaps vt;
   const uint64_t qd[5] = {64, (uint64_t)G, (uint64_t)a.B * a.N, 2, (uint64_t)a.Hkv};
   const uint64_t qs[4] = {256, (uint64_t)a.Hq * 256, 128, (uint64_t)G * 256};
   const uint32_t bt[5] = {64, (uint32_t)G, (uint32_t)y.tpt, 1, 1};
+  const uint32_t bo[5] = {64, (uint32_t)G, (uint32_t)(y.q_rows / G), 1, 1};
   const uint32_t bu[5] = {64, (uint32_t)G, (uint32_t)(y.rows_u / G), 1, 1};
   // cache cells as (channel half, token, half, group): a box is both halves of 64 tokens
   const uint64_t kd[4] = {64, (uint64_t)a.num_pages * 128, 2, (uint64_t)a.Hkv};
   const uint64_t ks[3] = {(uint64_t)a.Hkv * 256, 128, 256};
   const uint32_t bk[4] = {64, kStep, 2, 1};
   if (!encode_bf16_map(&qt, a.q, 5, qd, qs, bt, true) ||
+      !encode_bf16_map(&qo, a.q, 5, qd, qs, bo, true) ||
       !encode_bf16_map(&qu, a.q, 5, qd, qs, bu, true) ||
       !encode_bf16_map(&km, a.k_cache, 4, kd, ks, bk, true) ||
       !encode_bf16_map(&vm, a.v_cache, 4, kd, ks, bk, true))
     return cudaErrorInvalidValue;
+  for (int b = 0; b < 6; ++b) {
+    const uint32_t box[4] = {64, 1u << b, 1, 1};
+    if (!encode_bf16_map(&vt.m[b], a.v_cache, 4, kd, ks, box, true)) return cudaErrorInvalidValue;
+  }
   cudaError_t e = cudaFuncSetAttribute(shared_prefix_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  shared_prefix_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(qt, qu, km, vm, p);
+  shared_prefix_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(qt, qo, qu, km, vm, vt, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
