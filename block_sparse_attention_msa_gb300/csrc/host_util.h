@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 namespace msa {
@@ -56,6 +57,27 @@ inline int sm_count() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
     return 148;
   return n;
+}
+
+// Raises a kernel's dynamic shared memory limit on the current device, once per device and size
+// (the call takes several microseconds; `raised` is the kernel's own, zero-initialised).
+constexpr int kMaxDevices = 64;
+template <class K>
+inline cudaError_t raise_smem_limit(K kernel, size_t bytes, std::atomic<size_t> (&raised)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && raised[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < kMaxDevices) raised[dev].store(bytes, std::memory_order_relaxed);
+  return e;
+}
+// After a launch that failed: whether raising the limit again may mend it (a device reset unloads
+// the kernel and its limit).
+inline bool forget_smem_limit(cudaError_t e, std::atomic<size_t> (&raised)[kMaxDevices]) {
+  int dev = 0;
+  if (e != cudaErrorInvalidValue || cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return false;
+  return raised[dev].exchange(0) != 0;
 }
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

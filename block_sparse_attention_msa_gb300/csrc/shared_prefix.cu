@@ -62,7 +62,12 @@ static_assert(kOffBar == kQTile + kMaxStages * kStage, "the two layouts fill the
 constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kPairCost = 1300.f, kPrivateCost = 1500.f;  // cycles of a CTA per step
+// Relative time of one step of one CTA, of a pair and of private lanes, and the steps' time that each
+// request tile takes besides, all with everything running. (Pair costs of 1500, 1700, 1900 and 2100
+// gave 158, 153, 150 and 148 us for 64 requests on 64K tokens, 292, 283, 277 and 277 us for 256 on
+// 32K; tile costs of 0, 1, 2 and 3 gave 145, 111, 112 and 114 us for 64 requests of one private token
+// on 64K.)
+constexpr float kPairCost = 2200.f, kPrivateCost = 1500.f, kTileCost = 1.f;
 constexpr float kRescale = 8.0f;                // log2 headroom before O is rescaled
 
 // A run of steps of one tile: what the roles of a lane need to know of it.
@@ -91,16 +96,11 @@ struct Bars {
   uint32_t tmem_base;
   int32_t fail;
   // plan
-  int32_t w_min[kThreads / 32], w_first[kThreads / 32], w_sum[kThreads / 32];
+  int32_t w_min[kThreads / 32], w_first[kThreads / 32], w_sum[kThreads / 32], w_req[kThreads / 32];
   int32_t start_b[2], start_rem[2];
 };
 constexpr size_t kSmemBytes = kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
-
-// What the join needs of the plan, written by CTA 0 of the attention kernel.
-struct PlanOut {
-  int32_t prefix, runs, w_p, tp, tpl;
-};
 
 // V maps with boxes of one channel half of 1, 2, 4, ..., 32 tokens.
 struct TailMaps {
@@ -115,6 +115,7 @@ struct KParams {
   int32_t B, N, G, Hq, Hkv, max_blocks;
   int64_t num_pages;
   int32_t gs, hs;     // log2 of G and Hkv
+  int32_t ctas;
   int32_t rows_g;     // B*N*G: query rows of a group
   int32_t tpt;        // tokens per tile: 128 / G
   int32_t pairs;      // pairs of prefix tiles per group
@@ -126,8 +127,10 @@ struct KParams {
   // partials: O as [32 channel quads][rows][4] fp32, then (m, l) per row
   float *po_s, *po_l, *po_u;
   float2 *ml_s, *ml_l, *ml_u;
-  PlanOut* plan;
-  int32_t* cum;       // [B + 1] private steps before request b
+  // what the join needs to know: the prefix pass's tokens, and the first and last worker of each
+  // tile's segments
+  int32_t* prefix;
+  int2 *range_s, *range_l, *range_u;  // [Hkv, pairs], [Hkv], [B, units, Hkv]
   uint16_t* o;
   float* lse;
 };
@@ -141,15 +144,8 @@ __device__ __forceinline__ int32_t seq_of(const KParams& p, int b) {
 __device__ __forceinline__ int32_t private_steps(int32_t seq, int32_t prefix) {
   return seq > prefix ? (seq - prefix + kStep - 1) / kStep : 0;
 }
-// `total` items cut into n runs, the first total % n of them one item longer: the first item of
-// run w, and the run of item x.
-__device__ __forceinline__ int32_t run_start(uint32_t total, uint32_t w, uint32_t n) {
-  return (int32_t)(w * (total / n) + min(w, total % n));
-}
-__device__ __forceinline__ int32_t run_of(uint32_t total, uint32_t x, uint32_t n) {
-  const uint32_t q = total / n, r = total % n;
-  return (int32_t)(x < r * (q + 1) ? x / (q + 1) : (x - r) / q);
-}
+// Items cut into runs of q, the first r of them one item longer: the first item of run w.
+__device__ __forceinline__ int32_t run_start(int32_t q, int32_t r, int32_t w) { return w * q + min(w, r); }
 
 struct Plan {
   int32_t prefix;        // tokens of the prefix pass, a multiple of kStep
@@ -159,6 +155,7 @@ struct Plan {
   int32_t tp, tpl;       // private steps; of these the odd tiles'
   int32_t n_s, n_p;      // CTAs of either kind
   int32_t runs, w_p;     // runs of the ts steps, private workers: none of them without a step
+  int32_t qs, rs, qp, rp;  // ts / runs, ts % runs, tp / w_p, tp % w_p
 };
 
 // Walks the segments of one worker's run of steps.
@@ -188,8 +185,8 @@ struct Walker {
     nst = pl.nst;
     x0 = len = left = 0;
     if (worker < pl.runs && u < p.pairs) {
-      x0 = run_start(pl.ts, worker, pl.runs);
-      len = run_start(pl.ts, worker + 1, pl.runs) - x0;
+      x0 = run_start(pl.qs, pl.rs, worker);
+      len = pl.qs + (worker < pl.rs ? 1 : 0);
       left = len * ((p.pairs - 1 - u) / p.abreast + 1);
       index = x0 / nst;  // the run's first group
       g = index;
@@ -202,8 +199,8 @@ struct Walker {
   __device__ __forceinline__ void init_private(const KParams& p, const Plan& pl, int32_t w, int32_t sb,
                                                int32_t srem) {
     worker = w;
-    const int32_t start = w < pl.w_p ? run_start(pl.tp, w, pl.w_p) : 0;
-    left = w < pl.w_p ? run_start(pl.tp, w + 1, pl.w_p) - start : 0;
+    const int32_t start = w < pl.w_p ? run_start(pl.qp, pl.rp, w) : 0;
+    left = w < pl.w_p ? pl.qp + (w < pl.rp ? 1 : 0) : 0;
     u = g = b = seq = index = step = nst = 0;
     kind = start < pl.tpl ? 1 : 2;
     if (left > 0) {
@@ -229,6 +226,8 @@ struct Walker {
     s.kind = kind;
     s.n = min(kind == 0 ? round : left, nst - step);
     left -= s.n;
+    const bool begins = step == 0, ends = step + s.n == nst;
+    int2* range;
     s.key0 = step * kStep;
     s.g = g;
     s.b = pl.first;
@@ -243,6 +242,7 @@ struct Walker {
       s.vis = seq - p.N + t0 + 1;
       s.rows = min(p.rows_u, (p.N - t0) << p.gs);
       s.q_row = b * p.N + t0;
+      range = p.range_u + (((b * p.units + u) << p.hs) | g);
       if (++g == p.Hkv) {
         g = 0;
         if (++u == p.units && left > 0) to_request(p, pl, b + 1);
@@ -252,6 +252,7 @@ struct Walker {
       s.rows = min(128, p.rows_g - tile * 128);
       s.q_row = tile * p.tpt;
       s.slot = kind == 0 ? (worker + g) * p.pairs + u : worker + g;
+      range = kind == 0 ? p.range_s + g * p.pairs + u : p.range_l + g;
       ++g;
       if (kind == 0) {
         round -= s.n;
@@ -264,6 +265,10 @@ struct Walker {
       } else if (g == p.Hkv && left > 0) {
         to_request(p, pl, 0);
       }
+    }
+    if ((threadIdx.x & 31) == 0) {
+      if (begins) range->x = worker;
+      if (ends) range->y = worker;
     }
     return true;
   }
@@ -415,31 +420,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     pl.ts = p.pairs > 0 ? p.Hkv * pl.nst : 0;
     pl.tpl = p.odd ? p.Hkv * pl.nst : 0;
     const int32_t tiles = p.units * p.Hkv;
-    int32_t sum = 0;
+    int32_t sum = 0, reqs = 0;  // private steps, requests that have any
 #pragma unroll 1
-    for (int b = pb0; b < pb1; ++b) sum += private_steps(seq_at(b), pl.prefix) * tiles;
+    for (int b = pb0; b < pb1; ++b) {
+      const int32_t steps = private_steps(seq_at(b), pl.prefix);
+      sum += steps * tiles;
+      reqs += steps > 0;
+    }
+    reqs = __reduce_add_sync(0xffffffffu, reqs);
     int32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) B.w_sum[warp] = incl;
+    if (lane == 31) {
+      B.w_sum[warp] = incl;
+      B.w_req[warp] = reqs;
+    }
     __syncthreads();
     int32_t before = incl - sum, total = 0;
+    reqs = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += B.w_sum[w];
       total += B.w_sum[w];
+      reqs += B.w_req[w];
     }
     pl.tp = pl.tpl + total;
-    // CTAs of either kind: the split whose slower side is faster. Weights are the measured times
-    // of one step of one CTA (cycles): a pair's step is bound by its MMAs, a private one by HBM.
+    // CTAs of either kind: the split whose slower side is faster
     const int32_t C = gridDim.x;
     if (pl.ts == 0) {
       pl.runs = 0;
     } else {
-      const float cs = kPairCost * p.pairs * pl.ts, cp = kPrivateCost * pl.tp;
+      const float cs = kPairCost * p.pairs * pl.ts, cp = kPrivateCost * (pl.tp + kTileCost * reqs * tiles);
       const int32_t most = max(1, (C - (pl.tp > 0 ? 1 : 0)) / p.abreast);
       auto slower = [&](int32_t runs) {
         const int32_t n = runs * p.abreast;
@@ -452,13 +466,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     pl.n_s = pl.runs * p.abreast;
     pl.n_p = C - pl.n_s;
     pl.w_p = min(2 * pl.n_p, pl.tp);
+    const uint32_t runs = max(1, pl.runs), w_p = max(1, pl.w_p);
+    pl.qs = (uint32_t)pl.ts / runs;
+    pl.rs = pl.ts - pl.qs * runs;
+    pl.qp = (uint32_t)pl.tp / w_p;
+    pl.rp = pl.tp - pl.qp * w_p;
     // where the two lanes of this CTA start, when they start in a request
     const bool priv = (int)blockIdx.x >= pl.n_s;
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
       const int32_t wk = x * pl.n_p + (int)blockIdx.x - pl.n_s;
       if (!priv || wk >= pl.w_p) break;
-      const int32_t at = run_start(pl.tp, wk, pl.w_p) - pl.tpl;
+      const int32_t at = run_start(pl.qp, pl.rp, wk) - pl.tpl;
       if (at >= before && at < before + sum) {
         int32_t rem = at - before;
         int b = pb0;
@@ -473,19 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (blockIdx.x == 0) {
-      int32_t c = before;
       bool bad = false;
 #pragma unroll 1
-      for (int b = pb0; b < pb1; ++b) {
-        p.cum[b] = c;
-        c += private_steps(seq_at(b), pl.prefix) * tiles;
-        bad |= seq_at(b) != p.seq_lens[b];
-      }
+      for (int b = pb0; b < pb1; ++b) bad |= seq_at(b) != p.seq_lens[b];
       if (bad) msa_record_error(kErrBadBlock);
-      if (tid == 0) {
-        p.cum[p.B] = total;
-        *p.plan = {pl.prefix, pl.runs, pl.w_p, pl.tp, pl.tpl};
-      }
+      if (tid == 0) *p.prefix = pl.prefix;
     }
   }
   const bool shared = (int)blockIdx.x < pl.n_s;
@@ -558,9 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       auto load = [&](const CUtensorMap* map, uint32_t off, int32_t tok, int32_t g) {
+        const int32_t ut = uniform(tok), ug = uniform(g), us = uniform(r.slot);
         if (lane == 0)
-          tma_load_4d(smem + off_ring + (rbase + r.slot) * kStage + off, map,
-                      &B.kv_full[rbase + r.slot], 0, tok, 0, g);
+          tma_load_4d(smem + off_ring + (rbase + us) * kStage + off, map, &B.kv_full[rbase + us], 0, ut,
+                      0, ug);
       };
       // V of step i - 2, of which the first z2 rows are the request's. The cache cells behind its
       // last token may hold anything, NaN included, and 0 * NaN is NaN, so those rows are not
@@ -940,6 +952,12 @@ struct Parts {
   int64_t o_step, ml_step;  // to the next segment of the row
   int32_t n;
 };
+// First worker and number of workers of a tile, within the slots there are (after a timeout the
+// attention kernel may not have written them).
+__device__ __forceinline__ int2 worker_range(int2 r, int32_t workers) {
+  const int32_t x = max(0, min(r.x, workers - 1));
+  return make_int2(x, max(0, min(r.y - x + 1, workers - x)));
+}
 struct Joined {
   float m, l;
   float4 acc;
@@ -979,37 +997,35 @@ __global__ void __launch_bounds__(kJoinRows * 32 * SPLIT)
   const int32_t pr = (int32_t)(blockIdx.x / p.Hkv) * kJoinRows + (t & (kJoinRows - 1));
   const int32_t quad = t / kJoinRows;
   const bool valid = pr < p.rows_g;
-  const int32_t r = valid ? pr / p.G : 0, e = pr % p.G, b = r / p.N, i = r % p.N;
+  const int32_t r = valid ? pr >> p.gs : 0, e = pr & (p.G - 1), b = r / p.N, i = r - b * p.N;
   Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   if (valid) {
-    const PlanOut pl = *p.plan;
-    const int32_t nst = pl.prefix / kStep;
-    const int32_t seq = p.seq_lens[b], c0 = p.cum[b], c1 = p.cum[b + 1];
+    // requested together: where the row's segments are, whether there are any
+    const int32_t tile = pr >> 7, u = i >> (7 - p.gs);
+    const bool paired = tile < 2 * p.pairs;
+    const int64_t unit = ((int64_t)b * p.units + u) * p.Hkv + g;
+    const int32_t prefix = *p.prefix, seq = seq_of(p, b);
+    const int2 ra = worker_range(paired ? p.range_s[g * p.pairs + (tile >> 1)] : p.range_l[g],
+                                 paired ? p.ctas / p.abreast : 2 * p.ctas);
+    const int2 rc = worker_range(p.range_u[unit], 2 * p.ctas);
     Parts a{}, c{};
-    if (nst > 0 && seq > 0) {  // a padding request's rows sit in the prefix tiles too
-      const int32_t tile = pr >> 7, row = pr & 127;
-      if (tile < 2 * p.pairs) {
-        const int32_t ts = p.Hkv * nst;
-        const int32_t w0 = run_of(ts, g * nst, pl.runs), w1 = run_of(ts, g * nst + nst - 1, pl.runs);
-        const int64_t slot = ((int64_t)(w0 + g) * p.pairs + (tile >> 1)) * 2 + (tile & 1);
+    if (prefix > 0 && seq > 0) {  // a padding request's rows sit in the prefix tiles too
+      const int32_t row = pr & 127;
+      if (paired) {
+        const int64_t slot = ((int64_t)(ra.x + g) * p.pairs + (tile >> 1)) * 2 + (tile & 1);
         a = {p.po_s + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_s + slot * 128 + row,
-             (int64_t)p.pairs * 2 * 128 * 128, (int64_t)p.pairs * 2 * 128, w1 - w0 + 1};
+             (int64_t)p.pairs * 2 * 128 * 128, (int64_t)p.pairs * 2 * 128, ra.y};
       } else {
-        const int32_t w0 = run_of(pl.tp, g * nst, pl.w_p), w1 = run_of(pl.tp, g * nst + nst - 1, pl.w_p);
-        const int64_t slot = (int64_t)w0 + g;
+        const int64_t slot = (int64_t)ra.x + g;
         a = {p.po_l + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_l + slot * 128 + row,
-             128 * 128, 128, w1 - w0 + 1};
+             128 * 128, 128, ra.y};
       }
     }
-    const int32_t per = (c1 - c0) / (p.units * p.Hkv);
-    if (per > 0) {
-      const int32_t u = i / p.tpt, row = (i - u * p.tpt) * p.G + e;
-      const int32_t x0 = pl.tpl + c0 + (u * p.Hkv + g) * per;
-      const int32_t w0 = run_of(pl.tp, x0, pl.w_p), w1 = run_of(pl.tp, x0 + per - 1, pl.w_p);
-      const int64_t slot = (int64_t)w0 + ((int64_t)b * p.units + u) * p.Hkv + g;
-      const int64_t cap = p.rows_u;
+    if (seq > prefix) {
+      const int32_t row = (i - u * p.tpt) * p.G + e;
+      const int64_t slot = rc.x + unit, cap = p.rows_u;
       c = {p.po_u + ((slot * 32 + quad) * cap + row) * 4, p.ml_u + slot * cap + row, cap * 128, cap,
-           w1 - w0 + 1};
+           rc.y};
     }
     const int32_t n = a.n + c.n;
     for (int32_t k = split; k < n; k += 4 * SPLIT) {
@@ -1059,7 +1075,7 @@ __global__ void __launch_bounds__(kJoinRows * 32 * SPLIT)
 
 struct Layout {
   int32_t rows_g, tpt, pairs, abreast, odd, units, rows_u, q_rows;
-  size_t po_s, po_l, po_u, ml_s, ml_l, ml_u, plan, cum, total;
+  size_t po_s, po_l, po_u, ml_s, ml_l, ml_u, prefix, range_s, range_l, range_u, total;
 };
 
 Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
@@ -1096,8 +1112,10 @@ Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
     at += align_up(bytes, 256);
     return here;
   };
-  y.plan = take(sizeof(PlanOut));
-  y.cum = take(((size_t)B + 1) * sizeof(int32_t));
+  y.prefix = take(sizeof(int32_t));
+  y.range_s = take((size_t)Hkv * y.pairs * sizeof(int2));
+  y.range_l = take((size_t)Hkv * sizeof(int2));
+  y.range_u = take((size_t)B * y.units * Hkv * sizeof(int2));
   y.ml_s = take(n_s * 256 * sizeof(float2));
   y.ml_l = take(n_l * 128 * sizeof(float2));
   y.ml_u = take(n_u * y.rows_u * sizeof(float2));
@@ -1131,6 +1149,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   while ((1 << p.hs) < a.Hkv) ++p.hs;
   p.max_blocks = a.max_blocks;
   p.num_pages = a.num_pages;
+  p.ctas = ctas;
   p.rows_g = y.rows_g;
   p.tpt = y.tpt;
   p.pairs = y.pairs;
@@ -1140,8 +1159,10 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.rows_u = y.rows_u;
   p.q_rows = y.q_rows;
   uint8_t* w = a.workspace;
-  p.plan = reinterpret_cast<PlanOut*>(w + y.plan);
-  p.cum = reinterpret_cast<int32_t*>(w + y.cum);
+  p.prefix = reinterpret_cast<int32_t*>(w + y.prefix);
+  p.range_s = reinterpret_cast<int2*>(w + y.range_s);
+  p.range_l = reinterpret_cast<int2*>(w + y.range_l);
+  p.range_u = reinterpret_cast<int2*>(w + y.range_u);
   p.ml_s = reinterpret_cast<float2*>(w + y.ml_s);
   p.ml_l = reinterpret_cast<float2*>(w + y.ml_l);
   p.ml_u = reinterpret_cast<float2*>(w + y.ml_u);
@@ -1173,11 +1194,20 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
     const uint32_t box[4] = {64, 1u << b, 1, 1};
     if (!encode_bf16_map(&vt.m[b], a.v_cache, 4, kd, ks, box, true)) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(shared_prefix_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  static std::atomic<size_t> raised[kMaxDevices];
+  cudaError_t e = raise_smem_limit(shared_prefix_kernel, kSmemBytes, raised);
   if (e != cudaSuccess) return e;
+  static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, shared_prefix_kernel);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
   shared_prefix_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(qt, qo, qu, km, vm, vt, p);
   e = cudaGetLastError();
+  if (forget_smem_limit(e, raised)) return launch_shared_prefix_decode(a, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.Hkv * (((int64_t)y.rows_g + kJoinRows - 1) / kJoinRows)));
