@@ -20,8 +20,7 @@
 //    prefix pass needs no mask, and shared_len is a hint about sharing, never about visibility.
 //
 // Per lane: S = Q K^T (128 x 64 x 128) and O += P V run on tcgen05 with S, P and O in tensor
-// memory; one softmax warpgroup per lane keeps the running max and sum (O rescaled only when the
-// max grows by more than 2^8) in fp32. P is rounded to bf16 for its product, as tensor cores
+// memory; one softmax warpgroup per lane keeps the running reference and sum in fp32. P is rounded to bf16 for its product, as tensor cores
 // take it; its sum l is taken before that rounding. A step is 64 keys because then S has two
 // buffers per lane next to O (2 lanes x (2 x 64 + 128) = 512 columns): S(i+1) is ready when the
 // softmax of step i ends, and the chain S -> softmax -> O of one step no longer bounds the rate.
@@ -38,14 +37,7 @@ namespace {
 
 constexpr int kThreads = 512;                    // warpgroups: loads, softmax x 2, MMA issue
 constexpr int kLaunchRegs = 128;                 // registers per thread at launch, then split
-#ifndef RL
-#define RL 72
-#define RI 72
-#define RS 184
-#endif
-constexpr int kRegsLoad = RL;
-constexpr int kRegsIssue = RI;
-constexpr int kRegsSoftmax = RS;
+constexpr int kRegsLoad = 56, kRegsIssue = 56, kRegsSoftmax = 200;
 constexpr int kStep = 64;                        // keys per step
 constexpr uint32_t kQHalf = 128 * 128;           // 128 rows x 64 channels bf16
 constexpr uint32_t kQTile = 2 * kQHalf;
@@ -68,7 +60,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 32K; tile costs of 0, 1, 2 and 3 gave 145, 111, 112 and 114 us for 64 requests of one private token
 // on 64K.)
 constexpr float kPairCost = 2200.f, kPrivateCost = 1500.f, kTileCost = 1.f;
-constexpr float kRescale = 8.0f;                // log2 headroom before O is rescaled
+constexpr float kFarSum = 16384.f;               // of a step's P: beyond it the reference moves
 
 // A run of steps of one tile: what the roles of a lane need to know of it.
 struct __align__(16) Seg {
@@ -91,7 +83,7 @@ struct Bars {
   uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][step & 1]
   uint64_t o_free[2];                    // per segment: O read
   uint64_t seg_full[2][kQueue], seg_free[2][kQueue];
-  uint64_t drained[4];
+  uint64_t drained[2];
   Seg seg[2][kQueue];
   uint32_t tmem_base;
   int32_t fail;
@@ -369,8 +361,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     msa_record_error(kErrTimeout);
     return;
   }
-  // the join may be scheduled as CTAs of this kernel leave; it waits for all of their stores
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 64) {
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&B.kv_full[i], 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&B.o_free[x], 4);
+      mbar_init(&B.drained[x], 1);
+      for (int i = 0; i < kQueue; ++i) {
+        mbar_init(&B.seg_full[x][i], 1);
+        mbar_init(&B.seg_free[x][i], 6);  // readers: four softmax warps, an issuer, a K/V producer
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&B.q_full[x][i], 1);
+        mbar_init(&B.q_empty[x][i], 1);
+        mbar_init(&B.s_full[x][i], 1);
+        mbar_init(&B.o_full[x][i], 1);
+        mbar_init(&B.p_full[x][i], 4);
+      }
+    }
+    B.fail = 0;
+    mbar_fence_init();
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&B.tmem_base)), "n"(kTmemCols)
@@ -384,6 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&qmap_u);
     tma_prefetch_desc(&qmap_o);
   }
+  // What precedes this kernel in the stream ends here: lengths, queries and caches are its output,
+  // the workspace was its join's input. The join in turn may be scheduled as CTAs of this kernel
+  // leave; it waits for all of their stores.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ------------------------------------------------------------------ plan
   Plan pl;
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -500,28 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const bool shared = (int)blockIdx.x < pl.n_s;
-  if (tid == 0) {
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&B.kv_full[i], 1);
-      mbar_init(&B.kv_empty[i], shared ? 2 : 1);  // lanes that read the stage
-    }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&B.o_free[x], 4);
-      for (int i = 0; i < kQueue; ++i) {
-        mbar_init(&B.seg_full[x][i], 1);
-        // readers: four softmax warps, two issuers, a K/V producer (a pair has one, on lane 0)
-        mbar_init(&B.seg_free[x][i], shared && x == 1 ? 6 : 7);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&B.q_full[x][i], 1);
-        mbar_init(&B.q_empty[x][i], 1);
-        mbar_init(&B.s_full[x][i], 1);
-        mbar_init(&B.o_full[x][i], 1);
-        mbar_init(&B.p_full[x][i], 4);
-      }
-    }
-    for (int i = 0; i < 4; ++i) mbar_init(&B.drained[i], 1);
-    B.fail = 0;
+  if (tid == 64) {
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&B.kv_empty[i], shared ? 2 : 1);  // lanes that read it
     mbar_fence_init();
   }
   tmem_fence_before();
@@ -554,7 +549,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
     const int X = warp & 1;
     const int32_t rbase = shared ? 0 : X * lane_ring;
-    if (warp < 2 && !(shared && X == 1)) {
+    if (shared && warp == 1) {
+      // a pair has one K/V producer, on lane 0: nothing to load here, but lane 1's feeder counts on
+      // a reader
+      int32_t k = 0;
+      Seg s;
+      while (take(1, k, s) && s.n > 0) {
+      }
+    } else if (warp < 2) {
       // ============================================================== K/V producers
       // warp 0 for lane 0 or a pair, warp 1 for lane 1
       RingPos r{0, 0};
@@ -712,94 +714,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    // ================================================================ MMA issuers
-    // One warp per lane and product. O(i) needs P(i) and V(i); S(i+2) needs K(i+2) and the
-    // completion of O(i), which reads P(i) from the tensor memory that S(i+2) overwrites. The
-    // tensor pipe queues only a few MMAs, and an issuer's waits and bookkeeping take as long as a
-    // group of MMAs, so it takes several issuers to keep the pipe fed.
-    const int X = (warp - 12) >> 1;
-    const bool scores = warp & 1;
+    // ================================================================ MMA issuers, one per lane
+    // Warps 12 and 13 (the other two of the warpgroup idle). In order S(0), S(1), then O(i), S(i+2):
+    // O(i) needs P(i) and V(i); S(i+2) needs K(i+2) and overwrites the tensor memory from which
+    // O(i) reads P(i), which it may as the tensor pipe runs one thread's MMAs in issue order; the
+    // commit that signals S(i+2) covers O(i). The warp runs in lockstep, an elected lane issues.
+    if (warp < 14) {
+    const int X = warp - 12;
     const int32_t rbase = shared ? 0 : X * lane_ring;
     const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
-    const uint32_t full0 = smem_u32(&B.kv_full[rbase]);
+    const uint32_t full0 = smem_u32(&B.kv_full[rbase]), p0 = smem_u32(&B.p_full[X][0]);
+    const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
+    const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
+    const uint64_t qd0 = umma_desc_sw128(sbase + X * 2 * q_half, 16, 1024);
+    const uint64_t kd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, 16, 1024);
+    const uint64_t vd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, kKvHalf, 1024);
     Seg s;
     RingPos r{0, 0};
-    int32_t k = 0, left = 0;
+    int32_t k = 0, o_seg = 0;
     bool good = take(X, k, s);
     const int32_t total = good ? s.total : 0;
-    left = s.n;
-    if (scores) {
-      const uint32_t idesc = umma_idesc_bf16(128, kStep, 0, 0);
-      const uint64_t qd0 = umma_desc_sw128(sbase + X * 2 * q_half, 16, 1024);
-      const uint64_t kd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, 16, 1024);
-      const uint32_t o0 = smem_u32(&B.o_full[X][0]);
-      uint64_t qd = qd0;
-      bool opens = true;  // the next S is a segment's first
-      r.advance(rlen);
-      // S(i+2) for i = -2 ..., the first two of them from stage 0
+    int32_t left = s.n;
+    uint32_t opens = 4;  // bit j: step i + j is a segment's first
+    uint64_t qd = qd0;
+    r.advance(rlen);
+    if (total > 0) good = wait_or_fail(&B.kv_full[rbase], 0, fail);
 #pragma unroll 1
-      for (int32_t i = -2; good && i < total; ++i) {
-        const uint32_t buf = i & 1;
-        if (i + 2 < total) {
-          if (left == 0) {
-            if (!(good = take(X, k, s))) break;
-            left = s.n;
-            opens = true;
-          }
-          if (opens) {
-            const int32_t seg = k - 1;
-            qd = qd0 + (s.kind == 2 && twice ? (seg & 1) * (q_half / 2 >> 4) : 0);
-            if (!(good = wait_or_fail(&B.q_full[X][seg & 1], (seg >> 1) & 1, fail))) break;
-            opens = false;
-          }
-          uint64_t kd = kd0 + (i + 2) * (kKvTile >> 4);
-          if (i < 0) {
-            good = wait_or_fail(&B.kv_full[rbase], 0, fail);
-          } else {
-            good = wait_two_or_fail(full0 + r.slot * 8, r.phase, o0 + buf * 8, (i >> 1) & 1, fail);
-            kd = kd0 + r.slot * (kStage >> 4) + (kKvTile >> 4);
-          }
-          if (!good) break;
-          tmem_fence_after();
-          issue_s(s_tmem + buf * 64, qd, kd, idesc, 0);
-          issue_s(s_tmem + buf * 64, qd + (q_half >> 4), kd + (kKvHalf >> 4), idesc, 1);
-          umma_commit_elect(&B.s_full[X][buf]);
-          if (--left == 0) umma_commit_elect(&B.q_empty[X][(k - 1) & 1]);
-          // stage 0 is free after its last S, stage i + 1 after O(i) and S(i+2)
-          if (i >= 0) umma_commit_elect(&B.kv_empty[rbase + r.slot]);
-          else if (i == -1 || total == 1) umma_commit_elect(&B.kv_empty[rbase]);
-        } else if (i >= 0) {
-          if (!(good = wait_or_fail(&B.o_full[X][buf], (i >> 1) & 1, fail))) break;
-          mbar_arrive_if(&B.kv_empty[rbase + r.slot], lane == 0);
-        }
-        if (i >= 0) r.advance(rlen);
-      }
-    } else {
-      const uint32_t idesc = umma_idesc_bf16(128, 128, 0, 1);
-      const uint64_t vd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, kKvHalf, 1024);
-      const uint32_t p0 = smem_u32(&B.p_full[X][0]);
-      uint32_t accumulate = 0;
-      r.advance(rlen);
-#pragma unroll 1
-      for (int32_t i = 0; good && i < total; ++i) {
-        const uint32_t buf = i & 1;
-        if (left == 0) {
-          if (!(good = take(X, k, s) && wait_or_fail(&B.o_free[X], k & 1, fail))) break;
-          left = s.n;
-          accumulate = 0;
-        }
+    for (int32_t i = -2; good && i < total; ++i) {
+      const uint32_t buf = i & 1;
+      if (i >= 0) {
+        if ((opens & 1u) && o_seg++ > 0 && !(good = wait_or_fail(&B.o_free[X], o_seg & 1, fail))) break;
         if (!(good = wait_two_or_fail(full0 + r.slot * 8, r.phase, p0 + buf * 8, (i >> 1) & 1, fail))) break;
         tmem_fence_after();
-        issue_o(o_tmem, s_tmem + buf * 64, vd0 + r.slot * (kStage >> 4), idesc, accumulate);
+        issue_o(o_tmem, s_tmem + buf * 64, vd0 + r.slot * (kStage >> 4), idesc_o, (opens & 1u) ^ 1u);
         umma_commit_elect(&B.o_full[X][buf]);
-        accumulate = 1;
-        r.advance(rlen);
-        --left;
       }
+      if (i + 2 < total) {
+        if (left == 0) {
+          if (!(good = take(X, k, s))) break;
+          left = s.n;
+          opens |= 4u;
+        }
+        if (opens & 4u) {
+          qd = qd0 + (s.kind == 2 && twice ? ((k - 1) & 1) * (q_half / 2 >> 4) : 0);
+          if (!(good = wait_or_fail(&B.q_full[X][(k - 1) & 1], ((k - 1) >> 1) & 1, fail))) break;
+          tmem_fence_after();
+        }
+        // K(0) and K(1) are stage 0, K(i+2) is the second half of stage i + 1
+        const uint64_t kd = kd0 + (i < 0 ? (i + 2) * (kKvTile >> 4) : r.slot * (kStage >> 4) + (kKvTile >> 4));
+        issue_s(s_tmem + buf * 64, qd, kd, idesc_s, 0);
+        issue_s(s_tmem + buf * 64, qd + (q_half >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
+        umma_commit_elect(&B.s_full[X][buf]);
+        if (--left == 0) umma_commit_elect(&B.q_empty[X][(k - 1) & 1]);
+      }
+      // stage 0 is free after its last S, stage i + 1 after O(i) and S(i+2)
+      if (i >= 0) {
+        umma_commit_elect(&B.kv_empty[rbase + r.slot]);
+        r.advance(rlen);
+      } else if (i == -1) {
+        umma_commit_elect(&B.kv_empty[rbase]);
+      }
+      opens >>= 1;
     }
     if (!good) {  // the MMAs in flight end before tensor memory is given back
-      umma_commit_elect(&B.drained[warp - 12]);
-      mbar_wait(&B.drained[warp - 12], 0);
+      umma_commit_elect(&B.drained[X]);
+      mbar_wait(&B.drained[X], 0);
+    }
     }
     __syncwarp();
   } else {
@@ -825,59 +805,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(good = wait_or_fail(&B.s_full[X][n & 1], (n >> 1) & 1, fail))) break;
         tmem_fence_after();
         const uint32_t sb = s_tmem + (n & 1) * 64;
-        float factor = 1.f;
-        bool need = false;
         if (act) {
-          float v[kStep];
-          tmem_ld32(sb, v);
-          tmem_ld32(sb + 32, v + 32);
-          tmem_wait_ld();
-          if (s.vis - kb < kStep) {  // uniform: the step holds a key some row does not see
-            const int32_t vis = s.vis + token - kb;
-#pragma unroll
-            for (int x = 0; x < kStep; ++x)
-              if (x >= vis) v[x] = -INFINITY;
-          }
-          float m4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int x = 4; x < kStep; x += 2) m4[(x >> 1) & 3] = max3(m4[(x >> 1) & 3], v[x], v[x + 1]);
-          const float m2 = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * kLog2e;
-          if (m_run == -INFINITY) {
-            m_run = m2;  // nothing in O yet
-          } else if (mine && m2 > m_run + kRescale) {
-            factor = ex2(m_run - m2);
-            need = true;
-            m_run = m2;
-            l *= factor;
-          }
-          const float off = m_run == -INFINITY ? 0.f : -m_run;
-          float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          float l4[4];
           uint32_t pk[32];
-#pragma unroll
-          for (int x = 0; x < kStep; x += 2) {
-            fma2(v[x], v[x + 1], v[x], v[x + 1], kLog2e, kLog2e, off, off);
-            v[x] = ex2(v[x]);
-            v[x + 1] = ex2(v[x + 1]);
-            add2(l8[(x >> 1) & 3], l8[4 + ((x >> 1) & 3)], v[x], v[x + 1]);
-            pk[x >> 1] = pack_bf16x2(v[x], v[x + 1]);
-          }
-          l += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
-          tmem_st32(sb, pk);
-          if (__any_sync(0xffffffffu, need)) {
-            // the max grew by more than 2^8: rescale O once O(n-1) has completed (S(n) says that
-            // O(n-2) has, so the barrier's parity is unambiguous)
-            if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
-            tmem_fence_after();
+          // Any reference near the row's maximum serves for m: P and its sums keep their relative
+          // precision as long as nothing overflows. So P is taken against the reference there is,
+          // and its sum, needed anyway, tells whether a score lies far above it; only then, and on
+          // a segment's first step, a second pass takes the maximum.
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t o[16];
-              tmem_ld16(o_tmem + c * 16, o);
-              tmem_wait_ld();
+          for (bool exact = j == 0;; exact = true) {
+            float v[kStep];
+            tmem_ld32(sb, v);
+            tmem_ld32(sb + 32, v + 32);
+            tmem_wait_ld();
+            if (s.vis - kb < kStep) {  // uniform: the step holds a key some row does not see
+              const int32_t vis = s.vis + token - kb;
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * factor);
-              tmem_st16(o_tmem + c * 16, o);
+              for (int x = 0; x < kStep; ++x)
+                if (x >= vis) v[x] = -INFINITY;
             }
+            if (exact) {
+              float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+              for (int x = 4; x < kStep; x += 2) m4[(x >> 1) & 3] = max3(m4[(x >> 1) & 3], v[x], v[x + 1]);
+              const float m2 = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * kLog2e;
+              float factor = 1.f;
+              if (m_run == -INFINITY) {
+                m_run = m2;  // nothing in O yet
+              } else if (mine && m2 > m_run) {
+                factor = ex2(m_run - m2);
+                m_run = m2;
+                l *= factor;
+              }
+              if (__any_sync(0xffffffffu, factor != 1.f)) {
+                // rescale O once O(n-1) has completed (S(n) says that O(n-2) has, so the barrier's
+                // parity is unambiguous)
+                if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
+                tmem_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(o_tmem + c * 16, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * factor);
+                  tmem_st16(o_tmem + c * 16, o);
+                }
+              }
+            }
+            const float off = m_run == -INFINITY ? 0.f : -m_run;
+            l4[0] = l4[1] = l4[2] = l4[3] = 0.f;
+#pragma unroll
+            for (int x = 0; x < kStep; x += 2) {
+              fma2(v[x], v[x + 1], v[x], v[x + 1], kLog2e, kLog2e, off, off);
+              v[x] = ex2(v[x]);
+              v[x + 1] = ex2(v[x + 1]);
+              add2(l4[x & 2], l4[(x & 2) + 1], v[x], v[x + 1]);
+              pk[x >> 1] = pack_bf16x2(v[x], v[x + 1]);
+            }
+            l4[0] = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            if (exact || !__any_sync(0xffffffffu, mine && (l4[0] > kFarSum || m_run == -INFINITY))) break;
           }
+          if (!good) break;
+          l += l4[0];
+          tmem_st32(sb, pk);
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -992,6 +983,7 @@ template <int SPLIT>
 __global__ void __launch_bounds__(kJoinRows * 32 * SPLIT)
     shared_prefix_join_kernel(const __grid_constant__ KParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int32_t g = blockIdx.x % p.Hkv;
   const int t = threadIdx.x % (kJoinRows * 32), split = threadIdx.x / (kJoinRows * 32);
   const int32_t pr = (int32_t)(blockIdx.x / p.Hkv) * kJoinRows + (t & (kJoinRows - 1));
@@ -1205,21 +1197,25 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  shared_prefix_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(qt, qo, qu, km, vm, vt, p);
-  e = cudaGetLastError();
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, shared_prefix_kernel, qt, qo, qu, km, vm, vt, p);
   if (forget_smem_limit(e, raised)) return launch_shared_prefix_decode(a, stream);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.Hkv * (((int64_t)y.rows_g + kJoinRows - 1) / kJoinRows)));
+  cfg.dynamicSmemBytes = 0;
   // segments of a row when the prefix dominates: the workers over the tiles
   const bool many = 2 * (int64_t)ctas > 8 * (int64_t)a.Hkv * (y.pairs + y.odd);
   cfg.blockDim = dim3(kJoinRows * 32 * (many ? kJoinSplit : 1));
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   return many ? cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<kJoinSplit>, p)
               : cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<1>, p);
 }

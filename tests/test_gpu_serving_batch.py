@@ -35,6 +35,12 @@ def built():
     assert msa.device_error() == 0
 
 
+@pytest.fixture(autouse=True)
+def no_error_left():
+    yield
+    assert msa.device_error() == 0  # a wait that ran out shows in its own test
+
+
 def i32(x):
     return torch.from_numpy(np.array(x, dtype=np.int32))
 
