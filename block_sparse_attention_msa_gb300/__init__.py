@@ -402,7 +402,7 @@ def build_page_tables(prev_lens, new_lens, page_table, free_pages, pages_used, T
         raise ValueError("build_page_tables: inconsistent shapes")
     sizes = (B, B + 1, T, T, 1)
     if out is None:
-        out = torch.empty(2 * B + 2 * T + 2, dtype=i32, device=dev).split_with_sizes(sizes)
+        out = [torch.empty(n, dtype=i32, device=dev) for n in sizes]
     else:
         for name, t, n in zip(("seq_lens", "cu_tokens", "slot_map", "positions", "pages_used"), out,
                               sizes, strict=True):

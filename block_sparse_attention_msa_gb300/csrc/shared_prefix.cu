@@ -932,8 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A CTA joins eight consecutive query rows of a group; a thread owns four channels of one row,
 // so a warp reads whole 128-byte lines of the partials' [channel quad][row][4] layout. With
 // SPLIT > 1 the row's segments are dealt to SPLIT threads, four loads in flight each, and joined
-// through shared memory: few tiles over many CTAs leave a row tens of segments (8 requests on
-// 60K tokens: 38), which one thread after the other would wait for.
+// through shared memory: few rows leave SMs idle and have many segments each (8 requests on 60K
+// tokens: 38), which one thread would wait for four by four.
 constexpr int kJoinRows = 8;
 constexpr int kJoinSplit = 4;
 
@@ -1212,8 +1212,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(a.Hkv * (((int64_t)y.rows_g + kJoinRows - 1) / kJoinRows)));
   cfg.dynamicSmemBytes = 0;
-  // segments of a row when the prefix dominates: the workers over the tiles
-  const bool many = 2 * (int64_t)ctas > 8 * (int64_t)a.Hkv * (y.pairs + y.odd);
+  const bool many = (int64_t)cfg.gridDim.x <= ctas;  // a CTA of 1024 threads fills an SM
   cfg.blockDim = dim3(kJoinRows * 32 * (many ? kJoinSplit : 1));
   cfg.stream = stream;
   return many ? cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<kJoinSplit>, p)
