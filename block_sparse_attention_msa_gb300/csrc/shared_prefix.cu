@@ -116,6 +116,7 @@ struct KParams {
   int32_t units;      // tiles of one request's rows
   int32_t rows_u;     // rows of a request tile (box height): G * min(N, tpt)
   int32_t q_rows;     // rows of a private CTA's query areas: 64, or 128
+  int32_t rows_l;     // rows kept of an odd prefix tile's partial: a multiple of 8
   // partials: O as [32 channel quads][rows][4] fp32, then (m, l) per row
   float *po_s, *po_l, *po_u;
   float2 *ml_s, *ml_l, *ml_u;
@@ -886,8 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           po = reinterpret_cast<float4*>(p.po_s + slot * 128 * 128);
           ml = p.ml_s + slot * 128;
         } else if (s.kind == 1) {
-          po = reinterpret_cast<float4*>(p.po_l + (int64_t)s.slot * 128 * 128);
-          ml = p.ml_l + (int64_t)s.slot * 128;
+          cap = p.rows_l;
+          po = reinterpret_cast<float4*>(p.po_l + (int64_t)s.slot * cap * 128);
+          ml = p.ml_l + (int64_t)s.slot * cap;
         } else {
           cap = p.rows_u;
           po = reinterpret_cast<float4*>(p.po_u + (int64_t)s.slot * cap * 128);
@@ -1009,8 +1011,9 @@ __global__ void __launch_bounds__(kJoinRows * 32 * SPLIT)
              (int64_t)p.pairs * 2 * 128 * 128, (int64_t)p.pairs * 2 * 128, ra.y};
       } else {
         const int64_t slot = (int64_t)ra.x + g;
-        a = {p.po_l + (slot * 128 * 32 + (int64_t)quad * 128 + row) * 4, p.ml_l + slot * 128 + row,
-             128 * 128, 128, ra.y};
+        const int64_t cap = p.rows_l;
+        a = {p.po_l + ((slot * 32 + quad) * cap + row) * 4, p.ml_l + slot * cap + row, cap * 128, cap,
+             ra.y};
       }
     }
     if (seq > prefix) {
@@ -1066,7 +1069,7 @@ __global__ void __launch_bounds__(kJoinRows * 32 * SPLIT)
 }
 
 struct Layout {
-  int32_t rows_g, tpt, pairs, abreast, odd, units, rows_u, q_rows;
+  int32_t rows_g, tpt, pairs, abreast, odd, units, rows_u, q_rows, rows_l;
   size_t po_s, po_l, po_u, ml_s, ml_l, ml_u, prefix, range_s, range_l, range_u, total;
 };
 
@@ -1081,6 +1084,7 @@ Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
   y.units = (N + y.tpt - 1) / y.tpt;
   y.rows_u = G * (N < y.tpt ? N : y.tpt);
   y.q_rows = y.rows_u <= 64 && y.rows_g - 256 * y.pairs <= 64 ? 64 : 128;
+  y.rows_l = (y.rows_g - 256 * y.pairs + 7) / 8 * 8;
   // pairs that walk the prefix together: enough that DRAM feeds them (4 to 8 of the CTAs on one
   // stream of keys), few enough that whole runs of them split the CTAs evenly, and without idle
   // places in the last round
@@ -1109,10 +1113,10 @@ Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
   y.range_l = take((size_t)Hkv * sizeof(int2));
   y.range_u = take((size_t)B * y.units * Hkv * sizeof(int2));
   y.ml_s = take(n_s * 256 * sizeof(float2));
-  y.ml_l = take(n_l * 128 * sizeof(float2));
+  y.ml_l = take(n_l * y.rows_l * sizeof(float2));
   y.ml_u = take(n_u * y.rows_u * sizeof(float2));
   y.po_s = take(n_s * 256 * 128 * sizeof(float));
-  y.po_l = take(n_l * 128 * 128 * sizeof(float));
+  y.po_l = take(n_l * y.rows_l * 128 * sizeof(float));
   y.po_u = take(n_u * y.rows_u * 128 * sizeof(float));
   y.total = at;
   return y;
@@ -1150,6 +1154,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.units = y.units;
   p.rows_u = y.rows_u;
   p.q_rows = y.q_rows;
+  p.rows_l = y.rows_l;
   uint8_t* w = a.workspace;
   p.prefix = reinterpret_cast<int32_t*>(w + y.prefix);
   p.range_s = reinterpret_cast<int2*>(w + y.range_s);
