@@ -394,11 +394,12 @@ int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache, const u
     return fail(MSA_ERR_UNSUPPORTED, "%s: Hq=%d Hkv=%d", name, Hq, Hkv);
   if (num_pages * 128 > kInt32Max || (int64_t)max_blocks * 128 > kInt32Max - 128)
     return fail(MSA_ERR_UNSUPPORTED, "%s: num_pages*128 or max_blocks*128 exceeds int32", name);
-  // key steps of the whole call, counted in int32 on the device: two per block and tile
+  // key steps of the whole call, counted in int32 on the device: two per block and tile, and a few
+  // per tile
   const int64_t tiles = (int64_t)B * ((N * (Hq / Hkv) + 127) / 128) + 1;
   const int64_t ptiles = ((int64_t)B * N * (Hq / Hkv) + 127) / 128;
   if ((int64_t)B * N * Hq > kInt32Max || (tiles > ptiles ? tiles : ptiles) > kInt32Max / 64 ||
-      (tiles > ptiles ? tiles : ptiles) * Hkv * 2 * max_blocks > kInt32Max)
+      (tiles > ptiles ? tiles : ptiles) * Hkv * (2 * (int64_t)max_blocks + 8) > kInt32Max)
     return fail(MSA_ERR_UNSUPPORTED, "%s: B=%d N=%d Hkv=%d max_blocks=%d: too many key blocks", name,
                 B, N, Hkv, max_blocks);
   const uintptr_t bits = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) |

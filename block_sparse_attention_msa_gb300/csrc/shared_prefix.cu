@@ -54,12 +54,13 @@ static_assert(kOffBar == kQTile + kMaxStages * kStage, "the two layouts fill the
 constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Relative time of one step of one CTA, of a pair and of private lanes, and the steps' time that each
-// request tile takes besides, all with everything running. (Pair costs of 1500, 1700, 1900 and 2100
-// gave 158, 153, 150 and 148 us for 64 requests on 64K tokens, 292, 283, 277 and 277 us for 256 on
-// 32K; tile costs of 0, 1, 2 and 3 gave 145, 111, 112 and 114 us for 64 requests of one private token
-// on 64K.)
-constexpr float kPairCost = 2200.f, kPrivateCost = 1500.f, kTileCost = 1.f;
+// Relative time of one step of one CTA, of a pair and of private lanes with everything running, and
+// the steps' time that a private tile's end and beginning take. (Pair costs of 2200, 2600, 3000 and
+// 3400: 132, 129, 126 and 137 us for 64 requests on 64K tokens, 267, 266, 267 and 277 us for 256 on
+// 32K. Tile costs of 0, 1, 2, 3 and 5: 145, 104, 106, 106 and 110 us for 64 requests of one private
+// token on 64K, 79, 65, 65, 66 and 66 us for 256 requests of 1 to 512 tokens.)
+constexpr float kPairCost = 2800.f, kPrivateCost = 1500.f;
+constexpr int kTileCost = 1;
 constexpr float kFarSum = 16384.f;               // of a step's P: beyond it the reference moves
 
 // A run of steps of one tile: what the roles of a lane need to know of it.
@@ -72,7 +73,7 @@ struct __align__(16) Seg {
   int32_t slot;       // of the partial, within its kind
   int32_t rows;       // valid rows of the tile
   int32_t vis;        // keys that the tile's first row sees (INT32_MAX in the prefix)
-  int32_t total;      // steps of the whole lane
+  int32_t last;       // 1: the lane's last
   int32_t q_row, pad; // first query row
 };
 constexpr int kQueue = 4;  // segments a lane's feeder is ahead of the slowest reader
@@ -88,7 +89,7 @@ struct Bars {
   uint32_t tmem_base;
   int32_t fail;
   // plan
-  int32_t w_min[kThreads / 32], w_first[kThreads / 32], w_sum[kThreads / 32], w_req[kThreads / 32];
+  int32_t w_min[kThreads / 32], w_first[kThreads / 32], w_sum[kThreads / 32];
   int32_t start_b[2], start_rem[2];
 };
 constexpr size_t kSmemBytes = kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
@@ -137,6 +138,8 @@ __device__ __forceinline__ int32_t seq_of(const KParams& p, int b) {
 __device__ __forceinline__ int32_t private_steps(int32_t seq, int32_t prefix) {
   return seq > prefix ? (seq - prefix + kStep - 1) / kStep : 0;
 }
+// The same in units of work: what ends and begins a tile counts as kTileCost steps behind its own.
+__device__ __forceinline__ int32_t tile_units(int32_t steps) { return steps > 0 ? steps + kTileCost : 0; }
 // Items cut into runs of q, the first r of them one item longer: the first item of run w.
 __device__ __forceinline__ int32_t run_start(int32_t q, int32_t r, int32_t w) { return w * q + min(w, r); }
 
@@ -145,7 +148,7 @@ struct Plan {
   int32_t first;         // an active request (its page table gives the prefix's pages)
   int32_t nst;           // prefix steps
   int32_t ts;            // prefix steps of one pair: all groups
-  int32_t tp, tpl;       // private steps; of these the odd tiles'
+  int32_t tp, tpl;       // private units (steps, and kTileCost per tile); of these the odd tiles'
   int32_t n_s, n_p;      // CTAs of either kind
   int32_t runs, w_p;     // runs of the ts steps, private workers: none of them without a step
   int32_t qs, rs, qp, rp;  // ts / runs, ts % runs, tp / w_p, tp % w_p
@@ -187,6 +190,15 @@ struct Walker {
     }
     round = len;
   }
+  // To the private tile behind the current one.
+  __device__ __forceinline__ void next_tile(const KParams& p, const Plan& pl) {
+    step = 0;
+    ++g;
+    if (g < p.Hkv || left <= 0) return;
+    g = 0;
+    if (kind == 1) to_request(p, pl, 0);
+    else if (++u == p.units) to_request(p, pl, b + 1);
+  }
   // Private worker w; sb/srem: request and offset in it where its run starts, when it starts in
   // a request.
   __device__ __forceinline__ void init_private(const KParams& p, const Plan& pl, int32_t w, int32_t sb,
@@ -205,11 +217,14 @@ struct Walker {
         nst = private_steps(seq, pl.prefix);
         rest = srem;
       }
-      const int32_t t = rest / nst;
-      step = rest - t * nst;
-      index = t;
+      const int32_t units = tile_units(nst), t = rest / units;
+      step = rest - t * units;
       u = t >> p.hs;
       g = t & (p.Hkv - 1);
+      if (step >= nst) {  // behind the tile's steps
+        left -= units - step;
+        next_tile(p, pl);
+      }
     }
   }
   // The next segment of lane X into s (n = 0: none is left).
@@ -225,40 +240,39 @@ struct Walker {
     s.g = g;
     s.b = pl.first;
     s.seq = s.vis = INT32_MAX;
-    step = 0;
     if (kind == 2) {
       const int32_t t0 = u * p.tpt;
+      const int32_t unit = ((b * p.units + u) << p.hs) | g;
       s.key0 += pl.prefix;
-      s.slot = worker + (((b * p.units + u) << p.hs) | g);
+      s.slot = worker + unit;
       s.b = b;
       s.seq = seq;
       s.vis = seq - p.N + t0 + 1;
       s.rows = min(p.rows_u, (p.N - t0) << p.gs);
       s.q_row = b * p.N + t0;
-      range = p.range_u + (((b * p.units + u) << p.hs) | g);
-      if (++g == p.Hkv) {
-        g = 0;
-        if (++u == p.units && left > 0) to_request(p, pl, b + 1);
-      }
+      range = p.range_u + unit;
     } else {
       const int32_t tile = kind == 0 ? 2 * u + X : 2 * p.pairs;
       s.rows = min(128, p.rows_g - tile * 128);
       s.q_row = tile * p.tpt;
       s.slot = kind == 0 ? (worker + g) * p.pairs + u : worker + g;
       range = kind == 0 ? p.range_s + g * p.pairs + u : p.range_l + g;
-      ++g;
-      if (kind == 0) {
-        round -= s.n;
-        if (round == 0) {
-          u += p.abreast;
-          round = len;
-          g = index;
-          step = x0;
-        }
-      } else if (g == p.Hkv && left > 0) {
-        to_request(p, pl, 0);
-      }
     }
+    if (kind == 0) {
+      step = 0;
+      ++g;
+      round -= s.n;
+      if (round == 0) {
+        u += p.abreast;
+        round = len;
+        g = index;
+        step = x0;
+      }
+    } else if (ends) {
+      left -= kTileCost;
+      next_tile(p, pl);
+    }
+    s.last = left <= 0;
     if ((threadIdx.x & 31) == 0) {
       if (begins) range->x = worker;
       if (ends) range->y = worker;
@@ -434,34 +448,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     pl.prefix = any ? max(0, min(want, vis)) / kStep * kStep : 0;
     pl.nst = pl.prefix / kStep;
     pl.ts = p.pairs > 0 ? p.Hkv * pl.nst : 0;
-    pl.tpl = p.odd ? p.Hkv * pl.nst : 0;
+    pl.tpl = p.odd ? p.Hkv * tile_units(pl.nst) : 0;
     const int32_t tiles = p.units * p.Hkv;
-    int32_t sum = 0, reqs = 0;  // private steps, requests that have any
+    int32_t sum = 0;  // units of the requests
 #pragma unroll 1
     for (int b = pb0; b < pb1; ++b) {
-      const int32_t steps = private_steps(seq_at(b), pl.prefix);
-      sum += steps * tiles;
-      reqs += steps > 0;
+      sum += tile_units(private_steps(seq_at(b), pl.prefix)) * tiles;
     }
-    reqs = __reduce_add_sync(0xffffffffu, reqs);
     int32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) {
-      B.w_sum[warp] = incl;
-      B.w_req[warp] = reqs;
-    }
+    if (lane == 31) B.w_sum[warp] = incl;
     __syncthreads();
     int32_t before = incl - sum, total = 0;
-    reqs = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += B.w_sum[w];
       total += B.w_sum[w];
-      reqs += B.w_req[w];
     }
     pl.tp = pl.tpl + total;
     // CTAs of either kind: the split whose slower side is faster
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (pl.ts == 0) {
       pl.runs = 0;
     } else {
-      const float cs = kPairCost * p.pairs * pl.ts, cp = kPrivateCost * (pl.tp + kTileCost * reqs * tiles);
+      const float cs = kPairCost * p.pairs * pl.ts, cp = kPrivateCost * pl.tp;
       const int32_t most = max(1, (C - (pl.tp > 0 ? 1 : 0)) / p.abreast);
       auto slower = [&](int32_t runs) {
         const int32_t n = runs * p.abreast;
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int b = pb0;
 #pragma unroll 1
         for (; b < pb1; ++b) {
-          const int32_t c = private_steps(seq_at(b), pl.prefix) * tiles;
+          const int32_t c = tile_units(private_steps(seq_at(b), pl.prefix)) * tiles;
           if (rem < c) break;
           rem -= c;
         }
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!wait_or_fail(&B.seg_full[X][q], (k / kQueue) & 1, fail)) return false;
     const Seg& e = B.seg[X][q];
     s = {uniform(e.n),    uniform(e.key0), uniform(e.b),   uniform(e.g),     uniform(e.seq),   uniform(e.kind),
-         uniform(e.slot), uniform(e.rows), uniform(e.vis), uniform(e.total), uniform(e.q_row), 0};
+         uniform(e.slot), uniform(e.rows), uniform(e.vis), uniform(e.last),  uniform(e.q_row), 0};
     __syncwarp();
     mbar_arrive_if(&B.seg_free[X][q], lane == 0);
     ++k;
@@ -604,14 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t jj = j + lane, key = s.key0 + jj * kStep;
         return jj < s.n ? p.page_table[(int64_t)s.b * p.max_blocks + key / MSA_BLOCK_TOKENS] : 0;
       };
-      int32_t k = 0, i = 0, total = 0;
+      int32_t k = 0, i = 0;
       Seg s, ahead;
       good = take(X, k, s);
       int32_t page = 0, page_ahead = 0;
-      if (good) {
-        total = s.total;
-        page = look_up(s, 0);
-      }
+      if (good) page = look_up(s, 0);
+      const bool single = s.n == 1 && s.last;  // one step in all
 #pragma unroll 1
       while (good && s.n > 0) {
         if (!(good = take(X, k, ahead))) break;
@@ -627,9 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t key = s.key0 + j * kStep;
           const int32_t tok = __shfl_sync(0xffffffffu, page, j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
           if (i == 0) {
-            begin(total > 1 ? kStage : kKvTile);
+            begin(single ? kKvTile : kStage);
             load(&kmap, 0, tok, s.g);
-            if (total == 1) r.advance(rlen);
+            if (single) r.advance(rlen);
           } else {
             if (i > 1) {
               if (!(good = begin(kStage))) break;
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll 1
       for (int e = 0; e < 2; ++e) {  // the last two steps' V
-        if (good && total > 1 - e && (good = begin(kKvTile))) {
+        if (good && i > 1 - e && (good = begin(kKvTile))) {
           load_v();
           r.advance(rlen);
         }
@@ -671,7 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the first n_p private workers are the CTAs' lanes 0, so few steps spread over all CTAs
       if (shared) w.init_pairs(p, pl, blockIdx.x);
       else w.init_private(p, pl, X * pl.n_p + (int32_t)blockIdx.x - pl.n_s, B.start_b[X], B.start_rem[X]);
-      const int32_t total = w.left;
       int32_t k = 0, done = 0;  // segments published, query tiles loaded
       bool good = true, alone = true;  // alone: the last tile fills the area
       int32_t kind = -1, q_row = 0, g = 0;  // of segment k - 1
@@ -679,7 +682,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool more = true; more;) {
         Seg s;
         more = w.next(p, pl, X, s);
-        s.total = total;
         const int q = k & (kQueue - 1);
         if (k >= kQueue && !(good = wait_or_fail(&B.seg_free[X][q], (k / kQueue - 1) & 1, fail))) break;
         if (lane == 0) {
@@ -734,14 +736,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     RingPos r{0, 0};
     int32_t k = 0, o_seg = 0;
     bool good = take(X, k, s);
-    const int32_t total = good ? s.total : 0;
-    int32_t left = s.n;
+    int32_t left = good ? s.n : 0;  // steps of the segment still to come
+    bool more = left > 0;           // S(i+2) exists
+    int32_t end = INT32_MAX;        // steps, once known
     uint32_t opens = 4;  // bit j: step i + j is a segment's first
     uint64_t qd = qd0;
     r.advance(rlen);
-    if (total > 0) good = wait_or_fail(&B.kv_full[rbase], 0, fail);
+    if (more) good = wait_or_fail(&B.kv_full[rbase], 0, fail);
+    else end = 0;
 #pragma unroll 1
-    for (int32_t i = -2; good && i < total; ++i) {
+    for (int32_t i = -2; good && i < end; ++i) {
       const uint32_t buf = i & 1;
       if (i >= 0) {
         if ((opens & 1u) && o_seg++ > 0 && !(good = wait_or_fail(&B.o_free[X], o_seg & 1, fail))) break;
@@ -750,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_o(o_tmem, s_tmem + buf * 64, vd0 + r.slot * (kStage >> 4), idesc_o, (opens & 1u) ^ 1u);
         umma_commit_elect(&B.o_full[X][buf]);
       }
-      if (i + 2 < total) {
+      if (more) {
         if (left == 0) {
           if (!(good = take(X, k, s))) break;
           left = s.n;
@@ -766,7 +770,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_s(s_tmem + buf * 64, qd, kd, idesc_s, 0);
         issue_s(s_tmem + buf * 64, qd + (q_half >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
         umma_commit_elect(&B.s_full[X][buf]);
-        if (--left == 0) umma_commit_elect(&B.q_empty[X][(k - 1) & 1]);
+        if (--left == 0) {
+          umma_commit_elect(&B.q_empty[X][(k - 1) & 1]);
+          if (s.last) {
+            more = false;
+            end = i + 3;
+          }
+        }
       }
       // stage 0 is free after its last S, stage i + 1 after O(i) and S(i+2)
       if (i >= 0) {
