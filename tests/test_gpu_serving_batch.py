@@ -4,7 +4,8 @@ and a run of the three together with the sparse path on the same caches.
 
 Attention tolerance, per output element, from the roundings the kernel makes. With w the exact
 softmax weights, A = sum_n w_n |v_n| and ref the exact output:
-  * P = 2^(s - m) is rounded to bf16 for its product: at most 2^-8 of each term, 2^-8 A in all;
+  * P = 2^(s - m) is rounded to bf16 for its product: at most 2^-8 of each term, 2^-8 A in all
+    (m a reference near the row's maximum);
   * o is rounded to bf16 once: 2^-8 of the value;
   * a score is an fp32 sum of 128 exact products of bf16 numbers, at most 2^-23 of sum |q_d k_d| per
     addition (truncating adds counted), then scaled to log2 units: ds = 2^-23 * 128 * max_n
@@ -261,14 +262,14 @@ def make_decode(seq, shared, N, Hq, Hkv, seed, scale=1.0):
     return dict(q=q, kc=kc, vc=vc, table=table, seq=i32(seq), N=N, shared=shared)
 
 
-def ref_decode(w):
+def ref_decode(w, device="cpu"):
     """o, lse, and per element / row the tolerances of the module docstring, in 64 bits."""
     q, N = w["q"].double(), w["N"]
     R, Hq, _ = q.shape
     Hkv = w["kc"].shape[2]
     G = Hq // Hkv
-    o = torch.zeros((R, Hq, D), dtype=torch.float64)
-    lse = torch.full((R, Hq), float("-inf"), dtype=torch.float64)
+    o = torch.zeros((R, Hq, D), dtype=torch.float64, device=device)
+    lse = torch.full((R, Hq), float("-inf"), dtype=torch.float64, device=device)
     to, tl = torch.zeros_like(o), torch.zeros_like(lse)
     for b, n in enumerate(w["seq"].tolist()):
         pages = w["table"][b, :(n + PAGE - 1) // PAGE].long()
@@ -333,6 +334,14 @@ CASES = [
     ([9000], 8960, 1, 64, 8),                        # a long prefix cut over every CTA
     ([130 + (i * 37) % 200 for i in range(300)], 128, 1, 8, 2),   # many requests
     ([0, 0, 0], 128, 2, 8, 2),                       # nobody is active
+    ([400, 333, 512], 192, 5, 64, 8),                # 40 rows per request: one area, one buffer
+    ([400, 333, 512, 300, 311], 256, 16, 8, 1),      # 128 rows per request, wide query areas
+    ([210, 340, 199], 128, 16, 16, 1),               # two tiles per request behind a pair
+    ([200 + i % 50 for i in range(144)], 192, 1, 16, 1),  # nine pairs in rounds
+    ([100 + i % 150 for i in range(150)], 64, 1, 32, 2),  # four pairs and an odd tile with 96 rows
+    ([1 + (i * 53) % 90 for i in range(700)], 0, 1, 4, 1),    # more requests than threads, all short
+    ([65 + i % 3 for i in range(600)], 64, 1, 1, 1),      # ... with a prefix of one step
+    ([64 * k + d for k in (1, 2, 5) for d in (-1, 0, 1)], 0, 2, 16, 4),  # lengths around the steps
 ]
 
 
@@ -342,6 +351,34 @@ def test_shared_prefix_decode(case):
     w = make_decode(seq, shared if min([n for n in seq if n] or [0]) >= shared else 0, N, Hq, Hkv,
                     seed=case)
     check_decode(run_decode(w, shared=shared), ref_decode(w))
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,shared,own", [
+    (1, 1, 16, 16, 0, 45000),      # a lane walks more than 32 steps of one request
+    (64, 1, 32, 2, 40000, 100),    # ... and of the prefix, four pairs abreast
+    (3, 1, 8, 1, 70001, 333),      # ... and of an odd tile
+])
+def test_long_runs(B, N, Hq, Hkv, shared, own):
+    """Sizes for which the 64-bit reference runs on the GPU too."""
+    g = torch.Generator(device=DEV).manual_seed(B)
+    seq = torch.randint(max(1, own // 2), own + 1, (B,), generator=g, device=DEV) + shared
+    seq[0] = shared + own
+    mb = (shared + own + PAGE - 1) // PAGE
+    whole = shared // PAGE
+    pages = whole + B * (mb - whole)
+    perm = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+    table = torch.empty((B, mb), dtype=torch.int32, device=DEV)
+    table[:, :whole] = perm[:whole]
+    table[:, whole:] = perm[whole:].view(B, mb - whole)
+    kc, vc = (torch.randn((pages, PAGE, Hkv, D), generator=g, device=DEV).to(torch.bfloat16)
+              for _ in range(2))
+    if shared % PAGE:
+        for c in (kc, vc):
+            c[table[:, whole].long(), :shared % PAGE] = c[table[0, whole].long(), :shared % PAGE].clone()
+    q = (torch.randn((B * N, Hq, D), generator=g, device=DEV) * D ** -0.5).to(torch.bfloat16)
+    w = dict(q=q, kc=kc, vc=vc, table=table, seq=seq.to(torch.int32), N=N, shared=shared)
+    ref = [x.cpu() for x in ref_decode(w, DEV)]
+    check_decode(run_decode(w), ref)
 
 
 @pytest.mark.parametrize("shared", [-3, 0, 63, 64, 100, 511, 512, 1 << 30])
