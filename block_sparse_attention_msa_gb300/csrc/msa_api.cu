@@ -281,7 +281,6 @@ int msa_build_page_tables(const int32_t* prev_lens, const int32_t* new_lens, int
                           int32_t T, int32_t* seq_lens, int32_t* cu_tokens, int32_t* slot_map,
                           int32_t* positions, int32_t* pages_used_out, void* stream) {
   const char* name = "msa_build_page_tables";
-  if (B == 0 && T == 0) return ok();
   if (B <= 0 || T < 0 || max_blocks <= 0 || num_free < 0 || num_shared < 0 || num_pages <= 0)
     return fail(MSA_ERR_ARG, "%s: B=%d T=%d max_blocks=%d num_free=%d num_shared=%d num_pages=%lld",
                 name, B, T, max_blocks, num_free, num_shared, (long long)num_pages);

@@ -377,7 +377,7 @@ MSA_API int msa_index_score_topk_noalloc(const uint16_t* q_idx, const uint16_t* 
  *   prev_lens, new_lens [B] int32; page_table [B, max_blocks] int32 (in/out);
  *   free_pages [num_free] int32; pages_used [1] int32; shared_pages [num_shared] int32 or NULL
  *   seq_lens [B], cu_tokens [B+1], slot_map [T], positions [T], pages_used_out [1] int32 (out)
- * No output may be (or overlap) an input. B <= 16384; num_pages*128, max_blocks*128 and
+ * No output may be (or overlap) an input. 1 <= B <= 16384; num_pages*128, max_blocks*128 and
  * B*max_blocks < 2^31.
  * Device-side checks: a negative length or one past max_blocks*128 is clamped, token rows past T
  * are dropped, pages_used is clamped to [0, num_free] (all bit 1); a page outside
@@ -462,8 +462,9 @@ MSA_API const char* msa_last_error(void);
 
 /* Synchronises the current device, returns the device error word recorded by the kernels
  * (0 = none; bit 0 = out-of-range page id, bit 1 = out-of-range block id or length, bit 2 = a
- * bounded wait timed out, bit 3 = the free page list ran out) in *word (host pointer) and clears it. Returns MSA_OK, or MSA_ERR_DEVICE
- * when the word was non-zero, or MSA_ERR_CUDA. Not for the hot path. */
+ * bounded wait timed out, bit 3 = the free page list ran out) in *word (host pointer) and clears
+ * it. Returns MSA_OK, or MSA_ERR_DEVICE when the word was non-zero, or MSA_ERR_CUDA. Not for the
+ * hot path. */
 MSA_API int msa_device_error(uint32_t* word);
 
 /* Library version as "major.minor.patch" (host string, static storage). */
