@@ -67,15 +67,6 @@ __device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool pred) {
       "r"((uint32_t)pred)
       : "memory");
 }
-// The same without release order: for hand-overs of tensor memory (whose accesses have completed:
-// tcgen05.wait) by a warp that has global stores in flight, which a release would wait for.
-__device__ __forceinline__ void mbar_arrive_relaxed_if(uint64_t* bar, bool pred) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n"
-      " @p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n}" ::"r"(smem_u32(bar)),
-      "r"((uint32_t)pred)
-      : "memory");
-}
 __device__ __forceinline__ bool mbar_try_wait_addr(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(

@@ -11,19 +11,30 @@
 //    Two tiles share each K/V step a CTA loads; an odd last tile is handled like private work.
 //  * Private keys. A tile is one request's N*G rows (padded to M): the MMAs run far below their
 //    rate, but a step's 32 KB take longer to arrive than the padded MMAs take.
-//  * Both kinds are dealt as one line of equal steps: CTAs [0, n_s) cut the prefix steps of all
-//    tile pairs into equal runs, each of the other CTAs' two "lanes" an equal run of the
-//    private steps, and n_s follows from the two totals. No length is read on the host, so the
-//    call can be captured once and replayed with other lengths.
+//  * CTAs [0, n_s) cut the prefix steps of all tile pairs into equal runs; the other CTAs' two
+//    "lanes" cut the private work, steps and what a tile costs besides, into equal runs; n_s
+//    follows from the two totals. The plan is made on the GPU from the lengths, so the call can be
+//    captured once and replayed with other lengths.
 //  * Only whole 64-key steps below every active request's first visible row go to the prefix;
 //    its remainder is read through each request's own page table, where it also stands. So the
 //    prefix pass needs no mask, and shared_len is a hint about sharing, never about visibility.
 //
-// Per lane: S = Q K^T (128 x 64 x 128) and O += P V run on tcgen05 with S, P and O in tensor
-// memory; one softmax warpgroup per lane keeps the running reference and sum in fp32. P is rounded to bf16 for its product, as tensor cores
-// take it; its sum l is taken before that rounding. A step is 64 keys because then S has two
-// buffers per lane next to O (2 lanes x (2 x 64 + 128) = 512 columns): S(i+1) is ready when the
-// softmax of step i ends, and the chain S -> softmax -> O of one step no longer bounds the rate.
+// Per lane S = Q K^T (128 x 64 x 128) and O += P V run on tcgen05 with S, P and O in tensor
+// memory; one softmax warpgroup per lane keeps the running reference and sum in fp32. P is rounded
+// to bf16 for its product, as tensor cores take it; its sum l is taken before that rounding. A step
+// is 64 keys because then S has two buffers per lane next to O (2 lanes x (2 x 64 + 128) = 512
+// columns): S(i+1) is ready when the softmax of step i ends, and the chain S -> softmax -> O of one
+// step does not bound the rate.
+//
+// Measured (64 query heads on 8 KV heads, N = 1, one call replayed from a graph): 256 requests on
+// 32K shared tokens with 1 to 1024 private ones 256 us (1090 TFLOP/s); 64 on 64K with 1 to 2048
+// 128 us (4.2 TB/s); 64 with 1 to 8192 behind 2000 176 us (6.2 TB/s); 8 on 60K with 1 to 512 53 us
+// (4.8 TB/s). The pairs alone (256 requests, 32K shared tokens, one private) run at 1330 TFLOP/s,
+// 70% of what a dense bf16 product reaches: what is left is the handover between each
+// step's softmax and MMAs, and the power limit (1360 W in a loop, the SM clock at 1.72 to 1.95 GHz).
+// Private work alone (64 requests of 8K tokens) reads 6.6 TB/s, 97% of a copy.
+// What was slower: one issuer for both lanes (207 -> 260 us), the lanes' softmax taking turns
+// (207 -> 292 us), two warpgroups per lane on half of the keys each, four issuers (equal).
 #include "common.cuh"
 #include "host_util.h"
 #include "kernels.h"
@@ -44,9 +55,9 @@ constexpr uint32_t kQTile = 2 * kQHalf;
 constexpr uint32_t kKvHalf = kStep * 128;        // 64 keys x 64 channels bf16
 constexpr uint32_t kKvTile = 2 * kKvHalf;        // K or V of one step: 16 KB
 constexpr uint32_t kStage = 2 * kKvTile;         // one load stage: V(i) and K(i + 2)
-// shared memory: two query tiles and a ring of stages. A pair's tiles have 128 rows and leave 5
+// Shared memory: two query tiles and a ring of stages. A pair's tiles have 128 rows and leave 5
 // stages; private tiles of at most 64 rows leave 6, three per lane instead of two (a stage takes
-// 2500 cycles to arrive and a lane's step 1500).
+// about 2500 cycles to arrive and a lane's step 1500).
 constexpr int kRing = 5;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kOffBar = 2 * kQTile + kRing * kStage;
@@ -61,7 +72,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // token on 64K, 79, 65, 65, 66 and 66 us for 256 requests of 1 to 512 tokens.)
 constexpr float kPairCost = 2800.f, kPrivateCost = 1500.f;
 constexpr int kTileCost = 1;
-constexpr float kFarSum = 16384.f;               // of a step's P: beyond it the reference moves
+constexpr float kFarSum = 16384.f;  // of a step's P: beyond it the softmax's reference moves
 
 // A run of steps of one tile: what the roles of a lane need to know of it.
 struct __align__(16) Seg {
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 2) {
       // ============================================================== segments and query tiles
       // Walks the lane's segments for all of its roles (each walking them for itself made the
-      // kernel 217 KB of code, and every step waited for instructions) and loads their queries.
+      // kernel 1.7 times its code, and every step waited for instructions) and loads their queries.
       // Request tiles of at most half the lane's area alternate between its halves, so that the
       // next request's rows are there before the current one's last S.
       Walker w;
@@ -723,74 +734,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     // O(i) reads P(i), which it may as the tensor pipe runs one thread's MMAs in issue order; the
     // commit that signals S(i+2) covers O(i). The warp runs in lockstep, an elected lane issues.
     if (warp < 14) {
-    const int X = warp - 12;
-    const int32_t rbase = shared ? 0 : X * lane_ring;
-    const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
-    const uint32_t full0 = smem_u32(&B.kv_full[rbase]), p0 = smem_u32(&B.p_full[X][0]);
-    const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
-    const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
-    const uint64_t qd0 = umma_desc_sw128(sbase + X * 2 * q_half, 16, 1024);
-    const uint64_t kd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, 16, 1024);
-    const uint64_t vd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, kKvHalf, 1024);
-    Seg s;
-    RingPos r{0, 0};
-    int32_t k = 0, o_seg = 0;
-    bool good = take(X, k, s);
-    int32_t left = good ? s.n : 0;  // steps of the segment still to come
-    bool more = left > 0;           // S(i+2) exists
-    int32_t end = INT32_MAX;        // steps, once known
-    uint32_t opens = 4;  // bit j: step i + j is a segment's first
-    uint64_t qd = qd0;
-    r.advance(rlen);
-    if (more) good = wait_or_fail(&B.kv_full[rbase], 0, fail);
-    else end = 0;
-#pragma unroll 1
-    for (int32_t i = -2; good && i < end; ++i) {
-      const uint32_t buf = i & 1;
-      if (i >= 0) {
-        if ((opens & 1u) && o_seg++ > 0 && !(good = wait_or_fail(&B.o_free[X], o_seg & 1, fail))) break;
-        if (!(good = wait_two_or_fail(full0 + r.slot * 8, r.phase, p0 + buf * 8, (i >> 1) & 1, fail))) break;
-        tmem_fence_after();
-        issue_o(o_tmem, s_tmem + buf * 64, vd0 + r.slot * (kStage >> 4), idesc_o, (opens & 1u) ^ 1u);
-        umma_commit_elect(&B.o_full[X][buf]);
-      }
-      if (more) {
-        if (left == 0) {
-          if (!(good = take(X, k, s))) break;
-          left = s.n;
-          opens |= 4u;
-        }
-        if (opens & 4u) {
-          qd = qd0 + (s.kind == 2 && twice ? ((k - 1) & 1) * (q_half / 2 >> 4) : 0);
-          if (!(good = wait_or_fail(&B.q_full[X][(k - 1) & 1], ((k - 1) >> 1) & 1, fail))) break;
+      const int X = warp - 12;
+      const int32_t rbase = shared ? 0 : X * lane_ring;
+      const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
+      const uint32_t full0 = smem_u32(&B.kv_full[rbase]), p0 = smem_u32(&B.p_full[X][0]);
+      const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
+      const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
+      const uint64_t qd0 = umma_desc_sw128(sbase + X * 2 * q_half, 16, 1024);
+      const uint64_t kd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, 16, 1024);
+      const uint64_t vd0 = umma_desc_sw128(sbase + off_ring + rbase * kStage, kKvHalf, 1024);
+      Seg s;
+      RingPos r{0, 0};
+      int32_t k = 0, o_seg = 0;
+      bool good = take(X, k, s);
+      int32_t left = good ? s.n : 0;  // steps of the segment still to come
+      bool more = left > 0;           // S(i+2) exists
+      int32_t end = INT32_MAX;        // steps, once known
+      uint32_t opens = 4;  // bit j: step i + j is a segment's first
+      uint64_t qd = qd0;
+      r.advance(rlen);
+      if (more) good = wait_or_fail(&B.kv_full[rbase], 0, fail);
+      else end = 0;
+  #pragma unroll 1
+      for (int32_t i = -2; good && i < end; ++i) {
+        const uint32_t buf = i & 1;
+        if (i >= 0) {
+          if ((opens & 1u) && o_seg++ > 0 && !(good = wait_or_fail(&B.o_free[X], o_seg & 1, fail))) break;
+          if (!(good = wait_two_or_fail(full0 + r.slot * 8, r.phase, p0 + buf * 8, (i >> 1) & 1, fail))) break;
           tmem_fence_after();
+          issue_o(o_tmem, s_tmem + buf * 64, vd0 + r.slot * (kStage >> 4), idesc_o, (opens & 1u) ^ 1u);
+          umma_commit_elect(&B.o_full[X][buf]);
         }
-        // K(0) and K(1) are stage 0, K(i+2) is the second half of stage i + 1
-        const uint64_t kd = kd0 + (i < 0 ? (i + 2) * (kKvTile >> 4) : r.slot * (kStage >> 4) + (kKvTile >> 4));
-        issue_s(s_tmem + buf * 64, qd, kd, idesc_s, 0);
-        issue_s(s_tmem + buf * 64, qd + (q_half >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
-        umma_commit_elect(&B.s_full[X][buf]);
-        if (--left == 0) {
-          umma_commit_elect(&B.q_empty[X][(k - 1) & 1]);
-          if (s.last) {
-            more = false;
-            end = i + 3;
+        if (more) {
+          if (left == 0) {
+            if (!(good = take(X, k, s))) break;
+            left = s.n;
+            opens |= 4u;
+          }
+          if (opens & 4u) {
+            qd = qd0 + (s.kind == 2 && twice ? ((k - 1) & 1) * (q_half / 2 >> 4) : 0);
+            if (!(good = wait_or_fail(&B.q_full[X][(k - 1) & 1], ((k - 1) >> 1) & 1, fail))) break;
+            tmem_fence_after();
+          }
+          // K(0) and K(1) are stage 0, K(i+2) is the second half of stage i + 1
+          const uint64_t kd = kd0 + (i < 0 ? (i + 2) * (kKvTile >> 4) : r.slot * (kStage >> 4) + (kKvTile >> 4));
+          issue_s(s_tmem + buf * 64, qd, kd, idesc_s, 0);
+          issue_s(s_tmem + buf * 64, qd + (q_half >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
+          umma_commit_elect(&B.s_full[X][buf]);
+          if (--left == 0) {
+            umma_commit_elect(&B.q_empty[X][(k - 1) & 1]);
+            if (s.last) {
+              more = false;
+              end = i + 3;
+            }
           }
         }
+        // stage 0 is free after its last S, stage i + 1 after O(i) and S(i+2)
+        if (i >= 0) {
+          umma_commit_elect(&B.kv_empty[rbase + r.slot]);
+          r.advance(rlen);
+        } else if (i == -1) {
+          umma_commit_elect(&B.kv_empty[rbase]);
+        }
+        opens >>= 1;
       }
-      // stage 0 is free after its last S, stage i + 1 after O(i) and S(i+2)
-      if (i >= 0) {
-        umma_commit_elect(&B.kv_empty[rbase + r.slot]);
-        r.advance(rlen);
-      } else if (i == -1) {
-        umma_commit_elect(&B.kv_empty[rbase]);
+      if (!good) {  // the MMAs in flight end before tensor memory is given back
+        umma_commit_elect(&B.drained[X]);
+        mbar_wait(&B.drained[X], 0);
       }
-      opens >>= 1;
-    }
-    if (!good) {  // the MMAs in flight end before tensor memory is given back
-      umma_commit_elect(&B.drained[X]);
-      mbar_wait(&B.drained[X], 0);
-    }
     }
     __syncwarp();
   } else {
