@@ -553,3 +553,56 @@ def test_steps_of_a_batch_behind_a_cached_prompt():
             check = [r[:4] for r in ref]
             assert (lse.double().cpu() - check[1]).abs().max() <= 1e-3
             assert (o.double().cpu() - check[0]).abs().max() <= 2e-2
+
+
+def test_a_whole_step_captured_with_copies_around_it_equals_the_eager_step():
+    """Copies, tables, append, decode and copies in one graph, replayed over several steps: each
+    kernel waits for what precedes it, copies included, and leaves what the eager step leaves."""
+    Hq, Hkv, Di, B, P, mb, T, n = 32, 4, 64, 6, 96, 12, 64, 640
+    g = torch.Generator(device=DEV).manual_seed(4)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV).to(torch.bfloat16)
+    prompt = rnd(P, PAGE, Hkv, D), rnd(P, PAGE, Hkv, D)
+    free = torch.randperm(P, generator=g, device=DEV).to(torch.int32)
+    zeros = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)
+
+    def state():
+        d = dict(lens=zeros(B), used=zeros(1), table=zeros(B, mb), new=zeros(B), sl=zeros(1),
+                 kc=prompt[0].clone(), vc=prompt[1].clone(),
+                 xc=torch.zeros((P, PAGE, Hkv, Di), dtype=torch.bfloat16, device=DEV))
+        d["table"][:, :n // PAGE] = free[:n // PAGE]
+        d["lens"].fill_(n)
+        d["used"].fill_(n // PAGE)
+        d["sl"].fill_(n)
+        for k, s in (("k", (T, Hkv, D)), ("v", (T, Hkv, D)), ("x", (T, Hkv, Di)), ("q", (B, Hq, D))):
+            d[k] = torch.zeros(s, dtype=torch.bfloat16, device=DEV)
+        return d
+
+    given = {k: torch.zeros_like(x) for k, x in state().items() if k in ("new", "k", "v", "x", "q")}
+
+    def step(d):
+        for k, x in given.items():
+            d[k].copy_(x)
+        seq, _, slots, _, used = msa.build_page_tables(d["lens"], d["new"], d["table"], free, d["used"], T=T,
+                                                       num_pages=P)
+        msa.append_kv(d["k"], d["v"], d["x"], slots, d["kc"], d["vc"], d["xc"])
+        o, lse = msa.shared_prefix_decode(d["q"], d["kc"], d["vc"], d["table"], seq, d["sl"])
+        d["lens"].copy_(seq)
+        d["used"].copy_(used)
+        again, _ = msa.shared_prefix_decode(d["q"], d["kc"], d["vc"], d["table"], seq, d["sl"])
+        return o, lse, again
+
+    eager, captured = state(), state()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(captured)
+    for new in ([1, 2, 3, 4, 5, 0], [10] * 6, [1] * 6, [0, 60, 0, 0, 0, 1]):
+        given["new"].copy_(i32(new))
+        for k in ("k", "v", "x", "q"):
+            given[k].copy_(rnd(*given[k].shape) * (0.1 if k == "q" else 1.0))
+        graph.replay()
+        want = step(eager)
+        torch.cuda.synchronize()
+        for a, b in zip((*out, *captured.values()), (*want, *eager.values()), strict=True):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        assert torch.equal(out[0], out[2])
+        assert torch.isfinite(out[1]).all() and captured["lens"].tolist() == eager["lens"].tolist()
