@@ -401,6 +401,21 @@ def test_large_scores_rescale_the_output():
     check_decode(run_decode(w), ref_decode(w))
 
 
+def test_rounded_weights_and_output_are_the_only_errors_that_show():
+    """RMS of the error of o over RMS of o, on random values. A rounding to bf16 is off by d, uniform in
+    [-2^-8, 2^-8] relative to the lower end of its binade at worst: RMS(d) <= 2^-8 / sqrt(3). With
+    independent V of mean 0, o = sum w_n v_n and the weights' share sum w_n d_n v_n have variances
+    sum w_n^2 and sum w_n^2 d_n^2 times V's, so their ratio is at most 2^-8 / sqrt(3) too; the two
+    roundings add as variances: 2^-8 * sqrt(2/3) = 3.19e-3, with 10 % for the samples' spread (rows
+    share V, so 4 * 128 channels count as independent: 1 / sqrt(2 * 512) = 3 %, three times). fp32
+    sums are below 1e-5."""
+    w = make_decode([1700, 1600, 1555], 1500, 1, 32, 4, seed=31)
+    o = run_decode(w)[0].double().cpu()
+    ref = ref_decode(w)[0]
+    rms = ((o - ref).square().mean() / ref.square().mean()).sqrt()
+    assert rms <= 2.0 ** -8 * (2 / 3) ** 0.5 * 1.1, float(rms)
+
+
 def test_runs_agree_bit_for_bit_and_inputs_stay():
     w = make_decode([900 + 13 * i for i in range(40)], 800, 1, 64, 4, seed=8)
     d = {k: x.to(DEV) for k, x in w.items() if isinstance(x, torch.Tensor)}
