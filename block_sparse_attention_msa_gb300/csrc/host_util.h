@@ -59,8 +59,9 @@ inline int sm_count() {
   return n;
 }
 
-// Raises a kernel's dynamic shared memory limit on the current device, once per device and size
-// (the call takes several microseconds; `raised` is the kernel's own, zero-initialised).
+// Raises a kernel's dynamic shared memory limit on the current device, once per device (the call
+// takes several microseconds; `raised` is the kernel's own, zero-initialised, and `bytes` the same
+// in every call for it).
 constexpr int kMaxDevices = 64;
 template <class K>
 inline cudaError_t raise_smem_limit(K kernel, size_t bytes, std::atomic<size_t> (&raised)[kMaxDevices]) {
@@ -72,12 +73,24 @@ inline cudaError_t raise_smem_limit(K kernel, size_t bytes, std::atomic<size_t> 
   if (e == cudaSuccess && dev < kMaxDevices) raised[dev].store(bytes, std::memory_order_relaxed);
   return e;
 }
-// After a launch that failed: whether raising the limit again may mend it (a device reset unloads
-// the kernel and its limit).
-inline bool forget_smem_limit(cudaError_t e, std::atomic<size_t> (&raised)[kMaxDevices]) {
-  int dev = 0;
-  if (e != cudaErrorInvalidValue || cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return false;
-  return raised[dev].exchange(0) != 0;
+// Launches a kernel that takes up to `bytes` of dynamic shared memory: `launch` returns the launch's own
+// status. A device reset unloads the kernel and its limit, which the record of it outlives; so a
+// launch that fails with cudaErrorInvalidValue is made once more with the limit raised again, and
+// only once: whatever it then returns is the answer. The error of a failed launch is taken off the
+// thread, since the caller gets it as a status.
+template <class K, class L>
+inline cudaError_t launch_with_smem(K kernel, size_t bytes, std::atomic<size_t> (&raised)[kMaxDevices],
+                                    L launch) {
+  for (int attempt = 0;; ++attempt) {
+    cudaError_t e = raise_smem_limit(kernel, bytes, raised);
+    if (e == cudaSuccess) e = launch();
+    if (e == cudaSuccess) return e;
+    cudaGetLastError();
+    int dev = 0;
+    if (e != cudaErrorInvalidValue || attempt > 0 || cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices)
+      return e;
+    raised[dev].store(0, std::memory_order_relaxed);
+  }
 }
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

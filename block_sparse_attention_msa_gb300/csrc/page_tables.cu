@@ -201,20 +201,22 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageTablesA
 }  // namespace
 
 cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream) {
-  const size_t smem = (size_t)2 * (a.B + 1) * sizeof(int32_t);
-  static std::atomic<size_t> raised[kMaxDevices];
-  if (smem > 48 * 1024) {
-    const cudaError_t e = raise_smem_limit(page_tables_kernel, smem, raised);
-    if (e != cudaSuccess) return e;
-  }
   // about four token rows or sixteen shared entries per thread, at most two CTAs per SM
   const int64_t rows = (int64_t)a.T / 4 + (int64_t)a.B * a.num_shared / 16;
   int64_t grid = (rows + kThreads - 1) / kThreads;
   const int64_t cap = 2 * (int64_t)sm_count();
   grid = grid < 1 ? 1 : (grid > cap ? cap : grid);
-  page_tables_kernel<<<(unsigned)grid, kThreads, smem, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return forget_smem_limit(e, raised) ? launch_page_tables(a, stream) : e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)2 * (a.B + 1) * sizeof(int32_t);
+  cfg.stream = stream;
+  // the limit of the largest batch for all of them: were it the call's own, one thread could lower it
+  // between another's raise and launch
+  constexpr size_t kMaxSmem = (size_t)2 * (kMaxRequests + 1) * sizeof(int32_t);
+  static std::atomic<size_t> raised[kMaxDevices];
+  return launch_with_smem(page_tables_kernel, kMaxSmem, raised,
+                          [&] { return cudaLaunchKernelEx(&cfg, page_tables_kernel, a); });
 }
 
 }  // namespace msa

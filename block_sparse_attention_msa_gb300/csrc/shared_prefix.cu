@@ -1214,9 +1214,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
     const uint32_t box[4] = {64, 1u << b, 1, 1};
     if (!encode_bf16_map(&vt.m[b], a.v_cache, 4, kd, ks, box, true)) return cudaErrorInvalidValue;
   }
-  static std::atomic<size_t> raised[kMaxDevices];
-  cudaError_t e = raise_smem_limit(shared_prefix_kernel, kSmemBytes, raised);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes fa;
@@ -1235,16 +1233,20 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, shared_prefix_kernel, qt, qo, qu, km, vm, vt, p);
-  if (forget_smem_limit(e, raised)) return launch_shared_prefix_decode(a, stream);
+  static std::atomic<size_t> raised[kMaxDevices];
+  e = launch_with_smem(shared_prefix_kernel, kSmemBytes, raised, [&] {
+    return cudaLaunchKernelEx(&cfg, shared_prefix_kernel, qt, qo, qu, km, vm, vt, p);
+  });
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(a.Hkv * (((int64_t)y.rows_g + kJoinRows - 1) / kJoinRows)));
   cfg.dynamicSmemBytes = 0;
   const bool many = (int64_t)cfg.gridDim.x <= ctas;  // a CTA of 1024 threads fills an SM
   cfg.blockDim = dim3(kJoinRows * 32 * (many ? kJoinSplit : 1));
   cfg.stream = stream;
-  return many ? cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<kJoinSplit>, p)
-              : cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<1>, p);
+  e = many ? cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<kJoinSplit>, p)
+           : cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<1>, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 }  // namespace msa
