@@ -86,8 +86,14 @@ cudaError_t launch_append_kv(const AppendArgs& a, cudaStream_t stream) {
   p.cells = a.num_pages * MSA_BLOCK_TOKENS;
   const int64_t pieces = (int64_t)a.T << widest;
   const int64_t grid = (pieces + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  append_kv_kernel<<<dim3((unsigned)grid, (unsigned)n), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)n);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  // the launch's own status: the thread's last error may be an older call's
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, append_kv_kernel, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 }  // namespace msa

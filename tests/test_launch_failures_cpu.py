@@ -22,6 +22,7 @@ void fake_on_limit(void (*f)(void)) { on_limit = f; }
 /* the next n launches fail with cudaErrorInvalidValue, and one that wants more dynamic shared
    memory than the kernel's limit always does */
 void fake_reset(int n) { launches = refused = 0; last = cudaSuccess; failing = n; }
+void fake_leave_error(int e) { last = e; }
 
 cudaError_t cudaGetDevice(int* d) { *d = 0; return cudaSuccess; }
 cudaError_t cudaDeviceGetAttribute(int* v, enum cudaDeviceAttr a, int d) { *v = 152; return cudaSuccess; }
@@ -134,3 +135,9 @@ def test_two_batch_sizes_at_once_do_not_lower_each_others_limit(run):
         "fake.fake_on_limit(cb)\n"
         "assert tables(16384) == 0 and inner == [0]\n"
         "assert fake.fake_refused() == 0 and fake.fake_launches() == 2")
+
+
+@pytest.mark.parametrize("call", ["tables(4)", "append()", "decode()"])
+def test_an_older_error_of_the_thread_is_not_the_calls(run, call):
+    # 1: cudaErrorInvalidValue of some earlier call, not yet read; it stays for whoever reads it
+    run(f"fake.fake_reset(0)\nfake.fake_leave_error(1)\nassert {call} == 0 and fake.fake_last() == 1")
