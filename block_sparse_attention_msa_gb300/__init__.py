@@ -366,6 +366,12 @@ def _check(name: str, t, dtype, ndim: int, dev):
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
 
 
+def _sizes(name: str, *sizes: int):
+    """Sizes become int32 arguments, which would wrap around without an error."""
+    if max(sizes) > 2 ** 31 - 1:
+        raise ValueError(f"{name}: a size of {max(sizes)} exceeds int32")
+
+
 def _call(dev, fn, *args):
     """fn(*args, current stream of `dev`) with `dev` current."""
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
@@ -387,6 +393,7 @@ def build_page_tables(prev_lens, new_lens, page_table, free_pages, pages_used, T
     ``out`` when given (no output may be an input).
     """
     i32 = torch.int32
+    _sizes("build_page_tables", T, num_pages)
     _need(page_table, "page_table", i32, 2)
     dev = page_table.device
     _check("prev_lens", prev_lens, i32, 1, dev)
@@ -400,6 +407,7 @@ def build_page_tables(prev_lens, new_lens, page_table, free_pages, pages_used, T
         shared, num_shared = shared_pages.data_ptr(), shared_pages.numel()
     if prev_lens.numel() != B or new_lens.numel() != B or pages_used.numel() != 1 or T < 0:
         raise ValueError("build_page_tables: inconsistent shapes")
+    _sizes("build_page_tables", B, max_blocks, free_pages.numel(), num_shared)
     sizes = (B, B + 1, T, T, 1)
     if out is None:
         out = [torch.empty(n, dtype=i32, device=dev) for n in sizes]
@@ -449,6 +457,7 @@ def append_kv(k, v, k_idx, slot_map, k_cache, v_cache, k_idx_pages):
     _need(slot_map, "slot_map", torch.int32, 1)
     dev = slot_map.device
     T = slot_map.numel()
+    _sizes("append_kv", T)
     kp = vp = xp = kc = vc = xc = None
     ks = vs = xs = 0
     D = Di = BLOCK
@@ -503,6 +512,7 @@ def shared_prefix_decode(q, k_cache, v_cache, page_table, seq_lens, shared_len, 
     if R != B * N or v_cache.shape != k_cache.shape or Dk != D or page != BLOCK \
             or seq_lens.numel() != B or shared_len.numel() != 1:
         raise ValueError("shared_prefix_decode: inconsistent shapes")
+    _sizes("shared_prefix_decode", B, N, Hq, max_blocks)
     if out is None:
         o = torch.empty((R, Hq, D), dtype=bf16, device=dev)
         lse = torch.empty((R, Hq), dtype=torch.float32, device=dev) if with_lse else None

@@ -111,3 +111,20 @@ def test_binding_refuses_cpu_tensors_and_shapes(lib):
         msa.append_kv(b, b, None, i, c, c, None)
     with pytest.raises(ValueError, match="CUDA"):
         msa.shared_prefix_decode(b, c, c, torch.zeros((2, 1), dtype=torch.int32), i, i[:1])
+
+
+@pytest.mark.parametrize("sizes", [dict(T=2 ** 32 + 2), dict(T=2 ** 31), dict(T=2, num_pages=2 ** 64 + 4)])
+def test_binding_refuses_sizes_past_int32(lib, sizes):
+    # the C arguments would wrap around: 2^32 + 2 rows would be a call for 2
+    i = torch.zeros(2, dtype=torch.int32)
+    a = dict(num_pages=4)
+    a.update(sizes)
+    with pytest.raises(ValueError, match="int32"):
+        msa.build_page_tables(i, i, torch.zeros((2, 4), dtype=torch.int32), i, i[:1], **a)
+
+
+def test_sizes_of_tensors_past_int32():
+    from block_sparse_attention_msa_gb300 import _sizes
+    _sizes("name", 0, 5, 2 ** 31 - 1)
+    with pytest.raises(ValueError, match="name.*int32"):
+        _sizes("name", 3, 2 ** 31, 7)
