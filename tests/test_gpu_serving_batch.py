@@ -126,6 +126,20 @@ def test_page_tables_ragged(B, hi, mb):
     check_tables(prev, new, mb, free, 2, int(new.sum()) + 11, seed=B)
 
 
+@pytest.mark.parametrize("B,hi,mb,shared", [
+    (6143, 3, 5, 0), (6144, 2, 5, 0),    # the scans around 48 KB of shared memory
+    (16384, 2, 4, 2), (16384, 130, 4, 0),    # the largest batch
+])
+def test_page_tables_large_batches(B, hi, mb, shared):
+    rng = np.random.default_rng(B + hi)
+    prev = rng.integers(0, (mb - 2) * PAGE + 1, B)
+    prev[::3] = (mb - 2) * PAGE    # at a page border: holds the shared pages, opens one
+    new = rng.integers(0, hi + 1, B)
+    free = rng.permutation(1 << 16)[:2 * B + 5]
+    check_tables(prev, new, mb, free, 3, int(new.sum()) + 77, seed=B,
+                 shared=rng.integers(0, 1 << 16, shared) if shared else None)
+
+
 def test_page_tables_shared_prefix():
     shared = np.array([9, 3, 77, 5])
     prev = [512, 512, 600, 511, 0, 512]   # requests 3 and 4 do not hold the whole prefix
