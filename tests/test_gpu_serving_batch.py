@@ -17,6 +17,7 @@ import numpy as np
 import pytest
 import torch
 
+import _long_runs as lr
 import block_sparse_attention_msa_gb300 as msa
 
 pytestmark = pytest.mark.gpu
@@ -393,6 +394,34 @@ def test_long_runs(B, N, Hq, Hkv, shared, own):
     w = dict(q=q, kc=kc, vc=vc, table=table, seq=seq.to(torch.int32), N=N, shared=shared)
     ref = [x.cpu() for x in ref_decode(w, DEV)]
     check_decode(run_decode(w), ref)
+
+
+LONG = [(1, 1, 16, 16, 0, 45000, [0]),           # B, N, Hq, Hkv, shared, own, claims of shared_len
+        (64, 1, 32, 2, 40000, 100, [40000, 0]),  # pairs abreast, and the same keys as private ones
+        (3, 1, 8, 1, 70001, 333, [70001, 35000, 0]),   # an odd tile
+        (16, 4, 32, 4, 20011, 300, [20011]),     # several rows per request: two pairs
+        (9, 1, 64, 4, 10007, 5000, [10007])]     # a pair and an odd tile, long private parts
+LONG = [(*c[:6], claim) for c in LONG for claim in c[6]]
+
+
+def long_call(w, q, claim):
+    dev = w["kc"].device
+    return msa.shared_prefix_decode(q, w["kc"], w["vc"], w["table"], i32(w["lens"]).to(dev),
+                                    i32([claim]).to(dev), N=w["N"])
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_runs_count_every_key_once(case):
+    w = lr.counting(*case[:6], DEV)
+    lr.check_counting(w, *long_call(w, w["q"], case[6]))
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_runs_read_every_step_where_it_stands(case):
+    w = lr.pointing(*case[:6], DEV)
+    for turn in range(lr.turns(w)):
+        q, pos = lr.point_at(w, turn, DEV)
+        lr.check_pointing(w, pos, *long_call(w, q, case[6]))
 
 
 @pytest.mark.parametrize("shared", [-3, 0, 63, 64, 100, 511, 512, 1 << 30])
