@@ -491,7 +491,9 @@ def shared_prefix_decode(q, k_cache, v_cache, page_table, seq_lens, shared_len, 
 
     q [B*N, Hq, D] bf16 (the last N positions of each request); caches [P, 128, Hkv, D] bf16;
     page_table [B, max_blocks] int32; seq_lens [B] int32 (0: a padding request); shared_len [1]
-    int32: leading tokens that hold the same keys and values for every request. Returns
+    int32: leading tokens that hold the same keys and values for every request; of these the whole
+    64-token steps that every active request's rows see are read once, so a single short request
+    costs the batch its sharing. Returns
     (o [B*N, Hq, D] bf16, lse [B*N, Hq] fp32 or None), written into ``out`` when given. Sums and
     lse are fp32; the softmax weights are rounded to bf16 for their product with V, as in the
     library's other attention calls (relative RMS error of o on random values: 2.3e-3, against

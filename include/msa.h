@@ -427,7 +427,10 @@ MSA_API int msa_append_kv(const uint16_t* k, int64_t k_stride, const uint16_t* v
  * filled one). It says only what may be read once, never what a row sees: the prefix pass takes
  * the whole 64-token steps below min(shared_len, visible keys of the first row of every active
  * request), and each request reads the rest through its own table. shared_len = 0 is a plain
- * paged decode.
+ * paged decode. One short active request so ends the sharing for the whole batch: with 63 requests
+ * on a 65536-token document and one of 40 tokens the prefix pass covers nothing, and each of the 63
+ * reads all of its keys for itself. The answer is the same, the keys are read up to B times; such a
+ * request is better given a call of its own (or seq_lens[b] = 0 in this one).
  * A request with seq_lens[b] = 0 (a padding row of a captured batch), and any row at a negative
  * position, sees no key: o = 0, lse = -inf. Cache cells past a request's length may hold
  * anything, NaN included. (A non-finite V of one of the last N tokens of a request can reach

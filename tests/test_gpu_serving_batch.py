@@ -396,6 +396,16 @@ def test_long_runs(B, N, Hq, Hkv, shared, own):
     check_decode(run_decode(w), ref)
 
 
+@pytest.mark.parametrize("short", [1, 5, 63, 64, 65, 300, 579, 639, 640])
+@pytest.mark.parametrize("B,N,Hq,Hkv", [(4, 1, 64, 8), (5, 3, 32, 2), (24, 1, 64, 4)])
+def test_a_short_request_cuts_the_prefix_not_the_answer(short, B, N, Hq, Hkv):
+    # one request holds fewer of the same 640 leading keys than the others: the prefix pass covers
+    # the whole steps of its first row, down to none
+    w = make_decode([641 + 37 * b for b in range(B)], 640, N, Hq, Hkv, seed=40 + B)
+    w["seq"][B // 2] = short
+    check_decode(run_decode(w), ref_decode(w))
+
+
 LONG = [(1, 1, 16, 16, 0, 45000, [0]),           # B, N, Hq, Hkv, shared, own, claims of shared_len
         (64, 1, 32, 2, 40000, 100, [40000, 0]),  # pairs abreast, and the same keys as private ones
         (3, 1, 8, 1, 70001, 333, [70001, 35000, 0]),   # an odd tile
