@@ -388,7 +388,8 @@ def build_page_tables(prev_lens, new_lens, page_table, free_pages, pages_used, T
     prev_lens, new_lens [B] int32 (tokens held, tokens added); page_table [B, max_blocks] int32,
     updated in place; free_pages [F] int32, taken in order from index pages_used [1] int32 on;
     T token rows (those behind the last token get -1); shared_pages [n] int32: a cached prefix's
-    whole pages, entered for every request that holds at least n*128 tokens. Returns (seq_lens
+    whole pages, entered for every request that holds at least n*128 tokens, whatever its table
+    held: only for a batch whose long requests are all behind that prefix. Returns (seq_lens
     [B], cu_tokens [B+1], slot_map [T], positions [T], pages_used [1]), all int32, written into
     ``out`` when given (no output may be an input).
     """

@@ -372,7 +372,10 @@ MSA_API int msa_index_score_topk_noalloc(const uint16_t* q_idx, const uint16_t* 
  *   rows from cu_tokens[B] to T-1 (padding) get slot and position -1.
  *   pages_used_out[0] = pages_used[0] + sum_b need_b.
  * With shared_pages (num_shared > 0), entries 0..num_shared-1 of every request with
- * prev_lens[b] >= num_shared*128 are set to them: a cached prefix of whole pages.
+ * prev_lens[b] >= num_shared*128 are set to them: a cached prefix of whole pages. The lengths alone
+ * decide, not what the entries held: every row of the call that is long enough has to be behind that
+ * prefix. Requests behind another prefix, or none, go into a call of their own rows (from the
+ * pages_used_out of the first), and once a table has the entries, later steps pass NULL.
  *
  *   prev_lens, new_lens [B] int32; page_table [B, max_blocks] int32 (in/out);
  *   free_pages [num_free] int32; pages_used [1] int32; shared_pages [num_shared] int32 or NULL
