@@ -499,7 +499,8 @@ def shared_prefix_decode(q, k_cache, v_cache, page_table, seq_lens, shared_len, 
     lse are fp32; the softmax weights are rounded to bf16 for their product with V, as in the
     library's other attention calls (relative RMS error of o on random values: 2.3e-3, against
     1.7e-3 for weights in fp32). Without ``workspace`` the scratch comes from the caching allocator
-    for this call alone, so captured graphs and other streams do not share it.
+    for this call alone, so captured graphs and other streams do not share it (59 MB for B 256, N 1,
+    Hq 64, Hkv 8, 0.9 GB for B 4096: see ``msa_shared_prefix_decode_workspace_size``).
     """
     bf16, i32 = torch.bfloat16, torch.int32
     _need(q, "q", bf16, 3)

@@ -101,6 +101,16 @@ def test_decode_workspace_size(lib):
         assert size(*bad) == 0
 
 
+@pytest.mark.parametrize("sizes,megabytes", [
+    ((64, 1, 64, 8), 26), ((256, 1, 64, 8), 59), ((4096, 1, 64, 8), 920), ((512, 4, 128, 8), 930),
+    ((256, 16, 256, 16), 2400),
+])
+def test_decode_workspace_is_as_large_as_documented(lib, sizes, megabytes):
+    # the documented figures are for 152 SMs; without a device the library counts 148
+    got = lib.msa_shared_prefix_decode_workspace_size(*sizes) / 1e6
+    assert 0.95 * megabytes <= got <= 1.05 * megabytes
+
+
 def test_binding_refuses_cpu_tensors_and_shapes(lib):
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
