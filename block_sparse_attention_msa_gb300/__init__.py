@@ -447,9 +447,10 @@ def append_kv(k, v, k_idx, slot_map, k_cache, v_cache, k_idx_pages):
     """Write new tokens into the paged caches, in place (``msa_append_kv``).
 
     k, v [T, Hkv, D] and k_idx [T, Hkv, Di] bf16, token rows dense but their stride free (slices
-    of a fused projection); slot_map [T] int32 from ``build_page_tables`` (negative: skipped;
-    non-negative slots must differ); k_cache, v_cache [P, 128, Hkv, D], k_idx_pages
-    [P, 128, Hkv, Di] bf16. k, v and their caches, or k_idx and its pages, may be None.
+    of a fused projection; 16-byte aligned, a multiple of 8 elements); slot_map [T] int32 from
+    ``build_page_tables`` (negative: skipped; non-negative slots must differ, and no cell written
+    may be a row read); k_cache, v_cache [P, 128, Hkv, D], k_idx_pages [P, 128, Hkv, Di] bf16. k, v
+    and their caches, or k_idx and its pages, may be None.
     """
     if (k is None) != (v is None) or (k is None) != (k_cache is None) or \
             (k is None) != (v_cache is None) or (k_idx is None) != (k_idx_pages is None) or \

@@ -406,8 +406,9 @@ MSA_API int msa_build_page_tables(const int32_t* prev_lens, const int32_t* new_l
  *   k, v [T, Hkv, D] bf16; k_idx [T, Hkv, Di] bf16: rows of Hkv*D (Hkv*Di) dense elements, the
  *   row stride of each given in elements (a slice of a fused projection needs no copy); k and v
  *   may both be NULL, or k_idx (a layer without a key index)
- *   slot_map [T] int32; non-negative slots must differ: which row a repeated slot ends with is
- *   not specified
+ *   slot_map [T] int32; non-negative slots must differ: the cell of a repeated slot ends with a
+ *   mixture of its rows. Rows may lie in the caches themselves (a private copy of a partly filled
+ *   page), but no cell that is written may be a row that is read
  *   k_cache, v_cache [num_pages, 128, Hkv, D], k_idx_pages [num_pages, 128, Hkv, Di] bf16 (out)
  * Tensors are 16-byte aligned, strides multiples of 8 elements. A slot of num_pages*128 or more
  * is not written and sets bit 0 of the device error word.

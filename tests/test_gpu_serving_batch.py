@@ -231,6 +231,22 @@ def test_append_kv(T, Hkv, Di, strided):
         assert not flat.any()
 
 
+@pytest.mark.parametrize("n", [1, 37, 127, 128])
+def test_append_kv_copies_a_page_within_the_caches(n):
+    # the private copies of a partly filled shared page: the rows are cells of the caches
+    g = torch.Generator(device=DEV).manual_seed(n)
+    caches = [torch.randn((6, PAGE, 4, d), generator=g, device=DEV).to(torch.bfloat16) for d in (D, D, 64)]
+    want = [c.clone() for c in caches]
+    for c in want:
+        for page in (0, 4):
+            c[page, :n] = c[2, :n]
+    for page in (0, 4):
+        slots = torch.arange(n, dtype=torch.int32, device=DEV) + page * PAGE
+        msa.append_kv(*(c[2, :n] for c in caches), slots, *caches)
+    for c, w in zip(caches, want):
+        assert torch.equal(c, w)
+
+
 def test_append_kv_skips_bad_slots_and_empty_batches():
     k = torch.ones((3, 2, D), dtype=torch.bfloat16, device=DEV)
     caches = [torch.zeros((2, PAGE, 2, D), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
