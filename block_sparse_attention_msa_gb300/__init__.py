@@ -391,7 +391,7 @@ def build_page_tables(prev_lens, new_lens, page_table, free_pages, pages_used, T
     whole pages, entered for every request that holds at least n*128 tokens, whatever its table
     held: only for a batch whose long requests are all behind that prefix. Returns (seq_lens
     [B], cu_tokens [B+1], slot_map [T], positions [T], pages_used [1]), all int32, written into
-    ``out`` when given (no output may be an input).
+    ``out`` when given (no output may overlap an input or another output).
     """
     i32 = torch.int32
     _sizes("build_page_tables", T, num_pages)

@@ -302,6 +302,23 @@ int msa_build_page_tables(const int32_t* prev_lens, const int32_t* new_lens, int
   if (num_pages * 128 > kInt32Max || (int64_t)max_blocks * 128 > kInt32Max ||
       (int64_t)B * max_blocks > kInt32Max)
     return fail(MSA_ERR_UNSUPPORTED, "%s: slots or table entries exceed int32", name);
+  // [0, kOuts): written; the rest: read. Shared pages that are a later row of the table are let pass:
+  // such a row, when it holds them all, is rewritten with its own values.
+  struct Range {
+    const int32_t* at;
+    int64_t n;
+  };
+  constexpr int kTable = 0, kShared = 6, kOuts = 6, kRanges = 11;
+  const Range r[kRanges] = {{page_table, (int64_t)B * max_blocks}, {seq_lens, B}, {cu_tokens, B + 1},
+                            {slot_map, T}, {positions, T}, {pages_used_out, 1}, {shared_pages, num_shared},
+                            {prev_lens, B}, {new_lens, B}, {pages_used, 1}, {free_pages, num_free}};
+  for (int x = 0; x < kOuts; ++x)
+    for (int y = x + 1; y < kRanges; ++y) {
+      const uintptr_t x0 = reinterpret_cast<uintptr_t>(r[x].at), y0 = reinterpret_cast<uintptr_t>(r[y].at);
+      if (x == kTable && y == kShared) continue;
+      if (r[x].n > 0 && r[y].n > 0 && x0 < y0 + 4 * r[y].n && y0 < x0 + 4 * r[x].n)
+        return fail(MSA_ERR_ARG, "%s: an output overlaps an input or another output", name);
+    }
   msa::PageTablesArgs a{};
   a.prev_lens = prev_lens;
   a.new_lens = new_lens;

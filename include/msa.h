@@ -380,7 +380,7 @@ MSA_API int msa_index_score_topk_noalloc(const uint16_t* q_idx, const uint16_t* 
  *   prev_lens, new_lens [B] int32; page_table [B, max_blocks] int32 (in/out);
  *   free_pages [num_free] int32; pages_used [1] int32; shared_pages [num_shared] int32 or NULL
  *   seq_lens [B], cu_tokens [B+1], slot_map [T], positions [T], pages_used_out [1] int32 (out)
- * No output may be (or overlap) an input. 1 <= B <= 16384; num_pages*128, max_blocks*128 and
+ * No output may be (or overlap) an input or another output. 1 <= B <= 16384; num_pages*128, max_blocks*128 and
  * B*max_blocks < 2^31.
  * Device-side checks: a negative length or one past max_blocks*128 is clamped, token rows past T
  * are dropped, pages_used is clamped to [0, num_free] (all bit 1); a page outside

@@ -191,6 +191,50 @@ def test_page_tables_captured_and_replayed_with_other_lengths():
         assert int(out[4]) == want[5]
 
 
+def test_page_tables_into_given_outputs_step_after_step():
+    # a decode loop's two sets of buffers, each step's lengths and pages used the next one's inputs
+    B, mb, T = 5, 6, 9
+    zeros = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)
+    sets = [[zeros(B), zeros(B + 1), zeros(T), zeros(T), zeros(1)] for _ in range(2)]
+    table, new = torch.full((B, mb), -1, dtype=torch.int32, device=DEV), zeros(B)
+    free = torch.arange(60, dtype=torch.int32, device=DEV).flip(0)
+    prev, used, want_table = [126, 0, 250, 255, 128], 0, np.full((B, mb), -1, dtype=np.int32)
+    table[:, :2] = want = torch.arange(50, 60, dtype=torch.int32).view(B, 2).to(DEV)
+    want_table[:, :2] = want.cpu().numpy()
+    sets[1][0].copy_(i32(prev))
+    for step in range(6):
+        old, out = sets[(step + 1) % 2], sets[step % 2]
+        tokens = [1, 2, 0, 1, 3] if step % 2 else [1, 1, 1, 1, 1]
+        new.copy_(i32(tokens))
+        got = msa.build_page_tables(old[0], new, table, free, old[4], T=T, num_pages=60, out=out)
+        assert all(g.data_ptr() == o.data_ptr() for g, o in zip(got, out, strict=True))
+        want_table, prev, cu, slots, pos, used = ref_tables(prev, tokens, want_table, free.cpu().numpy(), used, T)
+        for g, w in zip((*out, table), (prev, cu, slots, pos, [used], want_table), strict=True):
+            assert np.array_equal(g.cpu().numpy(), np.asarray(w, dtype=np.int32))
+
+
+def test_page_tables_refuse_outputs_that_do_not_fit():
+    zeros = lambda n, dtype=torch.int32: torch.zeros(n, dtype=dtype, device=DEV)
+    B, T = 3, 7
+    args = (zeros(B), zeros(B), zeros((B, 4)), zeros(9), zeros(1))
+    good = [zeros(B), zeros(B + 1), zeros(T), zeros(T), zeros(1)]
+    msa.build_page_tables(*args, T=T, num_pages=9, out=good)
+    for at, x, error in ((0, zeros(B + 1), ValueError), (2, zeros(T - 1), ValueError),
+                         (3, zeros(T, torch.int64), TypeError), (4, zeros(2)[:0], ValueError),
+                         (1, zeros(2 * B + 2)[::2], ValueError), (0, args[0], msa.MSAError),
+                         (3, good[2], msa.MSAError), (0, good[1][1:], msa.MSAError)):
+        with pytest.raises(error):
+            msa.build_page_tables(*args, T=T, num_pages=9, out=[x if i == at else o for i, o in enumerate(good)])
+    with pytest.raises(ValueError):
+        msa.build_page_tables(*args, T=T, num_pages=9, out=good[:4])
+
+
+def test_page_tables_without_token_rows():
+    # no rows are asked for: lengths and tables alone
+    check_tables([0, 100], [0, 0], 4, np.arange(9), 0, 0)
+    check_tables([0, 100, 128], [200, 29, 0], 4, np.arange(9), 0, 0, expect=BAD_LEN)  # every row is past T
+
+
 # ------------------------------------------------------------------------------ append
 
 @pytest.mark.parametrize("T,Hkv,Di,strided", [

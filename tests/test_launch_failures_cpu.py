@@ -72,7 +72,7 @@ P, I, L, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 lib.msa_build_page_tables.argtypes = [P, P, I, I, P, P, I, P, P, I, L, I, P, P, P, P, P, P]
 lib.msa_append_kv.argtypes = [P, L, P, L, P, L, P, I, I, I, I, L, P, P, P, P]
 lib.msa_shared_prefix_decode.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, L, P, P, P, Z, P]
-at = [0x10000 * (i + 1) for i in range(20)]                # device pointers, never dereferenced
+at = [0x1000000 * (i + 1) for i in range(20)]                # device pointers, never dereferenced
 
 def tables(B):
     return lib.msa_build_page_tables(at[0], at[1], B, 8, at[2], at[3], 10, at[4], None, 0, 64, 16, at[5],
@@ -141,3 +141,15 @@ def test_two_batch_sizes_at_once_do_not_lower_each_others_limit(run):
 def test_an_older_error_of_the_thread_is_not_the_calls(run, call):
     # 1: cudaErrorInvalidValue of some earlier call, not yet read; it stays for whoever reads it
     run(f"fake.fake_reset(0)\nfake.fake_leave_error(1)\nassert {call} == 0 and fake.fake_last() == 1")
+
+
+def test_neighbouring_buffers_do_not_overlap(run):
+    # 4 lengths, 10 free pages, 16 rows and a table of 4 x 8 in one allocation, end to end; an empty
+    # buffer overlaps nothing
+    run("""fake.fake_reset(0)
+def call(free, nfree, T, slots, pos):
+    return lib.msa_build_page_tables(0x10000, 0x10010, 4, 8, 0x20000, free, nfree, 0x10020, None, 0, 64, T,
+                                     0x10024, 0x10034, slots, pos, 0x10048, None)
+assert call(0x1004c, 10, 16, 0x10074, 0x100b4) == 0
+assert call(0x10028, 0, 0, 0x20004, 0x20004) == 0
+assert call(0x1004c, 10, 16, 0x10074, 0x100b0) == -1""")

@@ -42,6 +42,26 @@ def test_page_tables_refuse(lib, change, code):
     assert lib.msa_last_error()
 
 
+def at(x):
+    return ctypes.c_void_p(x)
+
+
+@pytest.mark.parametrize("change", [
+    # [4] lengths, [10] free pages, [16] rows, a table of 4 x 8: an output that overlaps an input ...
+    dict(prev=at(0x10000), seq=at(0x10000 + 12)), dict(new=at(0x10000 + 12), cu=at(0x10000)),
+    dict(free=at(0x10000), slots=at(0x10000 + 36)), dict(free=at(0x10000 + 60), pos=at(0x10000)),
+    dict(used=at(0x10000 + 16), cu=at(0x10000)), dict(prev=at(0x10000 + 124), table=at(0x10000)),
+    dict(free=at(0x10000), table=at(0x10000 + 36)), dict(used=at(0x10000 + 4), table=at(0x10000)),
+    dict(shared=at(0x10000), nshared=8, slots=at(0x10000 + 28)),
+    # ... or another output
+    dict(slots=OUT[3]), dict(seq=OUT[1]), dict(out=OUT[5]), dict(cu=at(0x10000), pos=at(0x10000 + 16)),
+    dict(table=at(0x10000), seq=at(0x10000 + 124)), dict(slots=at(0x10000 + 60), pos=at(0x10000)),
+])
+def test_page_tables_refuse_overlapping_outputs(lib, change):
+    assert tables(lib, **change) == ARG
+    assert b"overlap" in lib.msa_last_error()
+
+
 def append(lib, **kw):
     a = dict(k=FAKE, ks=1024, v=FAKE, vs=1024, x=FAKE, xs=1024, slots=FAKE, T=4, Hkv=8, D=128, Di=128,
              pages=16, kc=OUT[0], vc=OUT[1], xc=OUT[2])
