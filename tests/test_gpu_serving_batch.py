@@ -595,6 +595,137 @@ def test_captured_decode_replays_with_other_lengths_and_two_graphs_overlap():
         check_decode(outs[1], ref_decode(ws[b]))
 
 
+def test_garbage_in_the_queries_of_padding_requests_reaches_no_other_row():
+    for seq, shared, N, Hq, Hkv in (([0, 900, 0, 700, 650, 0] * 9, 600, 1, 8, 1), ([0, 500, 513], 448, 3, 32, 2),
+                                    ([300, 0, 417, 0], 0, 2, 16, 4)):
+        w = make_decode(seq, shared, N, Hq, Hkv, seed=50)
+        clean = run_decode(w)
+        check_decode(clean, ref_decode(w))
+        pad = (w["seq"] == 0).repeat_interleave(N)
+        for junk in (float("nan"), float("inf"), -3e38):
+            w["q"][pad] = junk
+            o, lse = run_decode(w)
+            assert torch.equal(o.view(torch.int16), clean[0].view(torch.int16)) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("case", [
+    (3000, 1, 16, 2, 192, 70, 192),       # 94 pairs, more requests than threads
+    (2960, 1, 4, 1, 64, 130, 64),         # 46 pairs and an odd tile
+    (40, 16, 256, 16, 500, 200, 500),     # every size at its largest
+    (16384, 1, 1, 1, 130, 9, 130),        # as many requests as the page tables take
+    (2000, 3, 8, 8, 64, 90, 64),
+], ids=str)
+def test_large_batches(case):
+    w = lr.counting(*case[:6], DEV)
+    lr.check_counting(w, *long_call(w, w["q"], case[6]))
+    if case[0] <= 128:  # codes of 7 bits
+        w = lr.pointing(*case[:6], DEV)
+        for turn in range(lr.turns(w)):
+            q, pos = lr.point_at(w, turn, DEV)
+            lr.check_pointing(w, pos, *long_call(w, q, case[6]))
+
+
+def test_append_on_a_side_stream_in_a_captured_step():
+    """The append runs on a second stream beside other work and joins before the attention, eager and
+    in a graph: the attention waits for both of the streams that it depends on."""
+    w = make_decode([400 + 31 * b for b in range(8)], 320, 1, 32, 4, seed=51)
+    ref = ref_decode(w)
+    d = {k: w[k].to(DEV) for k in ("q", "kc", "vc", "table", "seq")}
+    sl = i32([320]).to(DEV)
+    last = torch.stack([w["table"][b, (n - 1) // PAGE] * PAGE + (n - 1) % PAGE
+                        for b, n in enumerate(w["seq"].tolist())]).to(torch.int32).to(DEV)
+    k, v = (c.view(-1, 4, D)[last.long()].clone() for c in (d["kc"], d["vc"]))
+    q_in, big = torch.zeros_like(d["q"]), torch.zeros(1 << 28, dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+
+    def spoil():
+        for c in (d["kc"], d["vc"]):
+            c.view(-1, 4, D)[last.long()] = 7.0
+        q_in.fill_(3.0)
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            big.add_(1)  # some 80 us before the append
+            msa.append_kv(k, v, None, last, d["kc"], d["vc"], None)
+        q_in.copy_(d["q"])
+        main.wait_stream(side)
+        return msa.shared_prefix_decode(q_in, d["kc"], d["vc"], d["table"], d["seq"], sl)
+
+    spoil()
+    check_decode(step(), ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        spoil()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_decode(out, ref)
+
+
+def test_threads_that_call_at_once_on_streams_of_their_own():
+    import concurrent.futures as cf
+    cases = [([900 - 50 * i, 777, 640 + i], 600, 1, 32, 4) for i in range(4)]
+    ws = [make_decode(*c, seed=60 + i) for i, c in enumerate(cases)]
+    refs = [ref_decode(w) for w in ws]
+    rng = np.random.default_rng(3)
+    lens = [(rng.integers(0, 200, B), rng.integers(0, 3, B)) for B in (5, 7000, 300, 12000)]
+
+    def work(i):
+        w, (prev, new) = ws[i], lens[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            d = {k: x.to(DEV) for k, x in w.items() if isinstance(x, torch.Tensor)}
+            sl = i32([600]).to(DEV)
+            for _ in range(20):
+                o, lse = msa.shared_prefix_decode(d["q"], d["kc"], d["vc"], d["table"], d["seq"], sl)
+                table = torch.zeros((len(prev), 3), dtype=torch.int32, device=DEV)
+                free = torch.arange(len(prev) * 2, dtype=torch.int32, device=DEV)
+                got = msa.build_page_tables(i32(prev).to(DEV), i32(new).to(DEV), table, free, i32([0]).to(DEV),
+                                            T=int(new.sum()) + 3, num_pages=1 << 16)
+            torch.cuda.current_stream().synchronize()
+            return (o, lse), [x.cpu() for x in (table, *got)]
+
+    with cf.ThreadPoolExecutor(4) as ex:
+        for i, (out, got) in enumerate(ex.map(work, range(4))):
+            check_decode(out, refs[i])
+            prev, new = lens[i]
+            want = ref_tables(prev, new, np.zeros((len(prev), 3), dtype=np.int32), np.arange(len(prev) * 2), 0,
+                              int(new.sum()) + 3)
+            for g, x in zip(got, (*want[:5], [want[5]]), strict=True):
+                assert np.array_equal(g.numpy(), np.asarray(x, dtype=np.int32))
+
+
+FRESH = """
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import test_gpu_serving_batch as t, torch, block_sparse_attention_msa_gb300 as msa
+w = t.make_decode([300, 400], 256, 1, 16, 2, seed=1)
+d = {k: x.cuda() for k, x in w.items() if isinstance(x, torch.Tensor)}
+z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+sl, prev, new, table, free, used = z(1) + 256, z(7000) + 5, z(7000) + 1, z((7000, 2)), z(9), z(1)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    seq = msa.build_page_tables(prev, new, table, free, used, T=7000, num_pages=9)[0]
+    out = msa.shared_prefix_decode(d["q"], d["kc"], d["vc"], d["table"], d["seq"], sl)
+g.replay()
+torch.cuda.synchronize()
+assert (seq == 6).all() and msa.device_error() == 0
+t.check_decode(out, t.ref_decode(w))
+"""
+
+
+def test_the_first_call_of_a_process_can_be_a_captured_one():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_out_of_range_page_reads_page_zero():
     w = make_decode([300, 520], 256, 1, 16, 2, seed=9)
     bad = dict(w, table=w["table"].clone())
