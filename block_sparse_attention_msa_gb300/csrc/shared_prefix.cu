@@ -18,6 +18,10 @@
 //  * Only whole 64-key steps below every active request's first visible row go to the prefix;
 //    its remainder is read through each request's own page table, where it also stands. So the
 //    prefix pass needs no mask, and shared_len is a hint about sharing, never about visibility.
+//  * A row that does not see one of its request's last N - 1 keys multiplies that key's V by a weight
+//    of 0 all the same, and 0 * NaN is NaN. So a warp brings these rows of V by plain loads, with
+//    zeros for what is not finite; when there was any, the softmax warps add it to the partials of
+//    the rows that see it.
 //
 // Per lane S = Q K^T (128 x 64 x 128) and O += P V run on tcgen05 with S, P and O in tensor
 // memory; one softmax warpgroup per lane keeps the running reference and sum in fp32. P is rounded
@@ -90,6 +94,14 @@ struct __align__(16) Seg {
   int32_t q_row, pad; // first query row
 };
 constexpr int kQueue = 4;  // segments a lane's feeder is ahead of the slowest reader
+// Rows of V [y, min(z, 64)) of a stage that do not come by bulk copies; z = 0: no more. Each open
+// entry has a stage of its own, of which a private lane has at most three: behind these and the
+// closing entry nothing is overwritten.
+struct Late {
+  int32_t y, z, tok, g, slot;
+};
+constexpr int kLateQueue = 4;
+static_assert(kLateQueue == kQueue, "initialised together");
 
 struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
@@ -97,8 +109,11 @@ struct Bars {
   uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][step & 1]
   uint64_t o_free[2];                    // per segment: O read
   uint64_t seg_full[2][kQueue], seg_free[2][kQueue];
+  uint64_t late_full[2][kLateQueue];
   uint64_t drained[2];
   Seg seg[2][kQueue];
+  Late late[2][kLateQueue];
+  int32_t odd[2];  // a late row of the lane was not finite, in this segment or one before
   uint32_t tmem_base;
   int32_t fail;
   // plan
@@ -138,6 +153,7 @@ struct KParams {
   // tile's segments
   int32_t* prefix;
   int2 *range_s, *range_l, *range_u;  // [Hkv, pairs], [Hkv], [B, units, Hkv]
+  const uint16_t* v_cache;  // for the late rows
   uint16_t* o;
   float* lse;
 };
@@ -373,6 +389,17 @@ __device__ __forceinline__ void issue_o(uint32_t d, uint32_t p_tmem, uint64_t vd
       : "memory");
 }
 
+// Two bf16 numbers, zero in the place of one that is not finite.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+  return x;
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t at, uint2 x) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x.x), "r"(x.y) : "memory");
+}
+
+template <bool LATE>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap qmap_t,
                          const __grid_constant__ CUtensorMap qmap_o,
@@ -396,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.drained[x], 1);
       for (int i = 0; i < kQueue; ++i) {
         mbar_init(&B.seg_full[x][i], 1);
+        mbar_init(&B.late_full[x][i], 1);
         mbar_init(&B.seg_free[x][i], 6);  // readers: four softmax warps, an issuer, a K/V producer
       }
       for (int i = 0; i < 2; ++i) {
@@ -407,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     B.fail = 0;
+    B.odd[0] = B.odd[1] = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -549,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t off_ring = 4 * q_half;
   const int32_t lane_ring = wide ? 2 : 3;               // stages of a private lane
   const int32_t rlen = shared ? kRing : lane_ring;
+  const bool has_late = LATE && !shared;
   // request tiles that leave half of their area free are double-buffered
   const bool twice = !shared && 2 * p.rows_u <= p.q_rows;
   static_assert(128 * (kRegsLoad + kRegsIssue) + 256 * kRegsSoftmax == kThreads * kLaunchRegs,
@@ -583,9 +613,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       int32_t used = 0;                                 // stages begun
       int32_t tok1 = 0, g1 = 0, z1 = 0, tok2 = 0, g2 = 0, z2 = 0;  // steps i - 1 and i - 2
       bool good = true;
-      auto begin = [&](uint32_t bytes) {
+      // Of a step in which the request has z more keys: the first late one (kStep: none), how many.
+      auto late_from = [&](int32_t z) { return max(0, min(z - (LATE ? p.N - 1 : 0), kStep)); };
+      auto late_rows = [&](int32_t z) { return LATE ? max(0, min(z, kStep) - late_from(z)) : 0; };
+      // To the lane's late-row warp: the late rows of V's step i - 2 for the current stage; z = 0: no more.
+      int32_t late_k = 0;
+      auto send_late = [&](int32_t z) {
+        if (lane == 0) {
+          B.late[X][late_k % kLateQueue] = {late_from(z), z, tok2, g2, rbase + r.slot};
+          mbar_arrive(&B.late_full[X][late_k % kLateQueue]);
+        }
+        ++late_k;
+      };
+      // Opens a stage of that many bytes, whose V has z more keys (INT32_MAX: no V). V's late rows come
+      // from the late-row warp, whose arrival is then the stage's.
+      auto begin = [&](uint32_t bytes, int32_t z) {
         if (used >= rlen && !wait_or_fail(&B.kv_empty[rbase + r.slot], r.phase ^ 1u, fail)) return false;
-        if (lane == 0) mbar_expect_tx(&B.kv_full[rbase + r.slot], bytes);
+        const int32_t late = late_rows(z);
+        if (LATE && late > 0) {
+          if (lane == 0) mbar_expect_tx_only(&B.kv_full[rbase + r.slot], bytes - late * 256);
+          send_late(z);
+        } else if (lane == 0) {
+          mbar_expect_tx(&B.kv_full[rbase + r.slot], bytes);
+        }
         __syncwarp();
         ++used;
         return true;
@@ -600,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // last token may hold anything, NaN included, and 0 * NaN is NaN, so those rows are not
       // loaded: zeros come in their place, by the same engine.
       auto load_v = [&]() {
-        if (z2 >= kStep) {
+        const int32_t y = late_from(z2), z = min(z2, kStep);
+        if (y >= kStep) {
           load(&vmap, 0, tok2, g2);
           return;
         }
@@ -610,11 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           int32_t at = 0;
 #pragma unroll 1
           for (int b = 5; b >= 0; --b)
-            if (z2 >> b & 1) {
+            if (y >> b & 1) {
               tma_load_4d(dst + at * 128, &vtail.m[b], full, 0, tok2 + at, lane, g2);
               at += 1 << b;
             }
-          bulk_load(dst + at * 128, g_zero_rows, (kStep - at) * 128, full);
+          if (z < kStep) bulk_load(dst + z * 128, g_zero_rows, (kStep - z) * 128, full);
         }
         __syncwarp();
       };
@@ -644,12 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t key = s.key0 + j * kStep;
           const int32_t tok = __shfl_sync(0xffffffffu, page, j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
           if (i == 0) {
-            begin(single ? kKvTile : kStage);
+            begin(single ? kKvTile : kStage, INT32_MAX);
             load(&kmap, 0, tok, s.g);
             if (single) r.advance(rlen);
           } else {
             if (i > 1) {
-              if (!(good = begin(kStage))) break;
+              if (!(good = begin(kStage, z2))) break;
               load_v();
             }
             load(&kmap, kKvTile, tok, s.g);
@@ -661,13 +712,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tok1 = tok;
           g1 = s.g;
           z1 = s.seq - key;
+          if (lane < 2 * late_rows(z1)) {  // two lines a row: they are there when V's turn comes
+            const uint16_t* v = p.v_cache + ((int64_t)(tok + late_from(z1) + (lane >> 1)) * p.Hkv + s.g) * 128;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (lane & 1) * 64));
+          }
         }
         s = ahead;
         page = page_ahead;
       }
 #pragma unroll 1
       for (int e = 0; e < 2; ++e) {  // the last two steps' V
-        if (good && i > 1 - e && (good = begin(kKvTile))) {
+        if (good && i > 1 - e && (good = begin(kKvTile, z2))) {
           load_v();
           r.advance(rlen);
         }
@@ -675,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         g2 = g1;
         z2 = z1;
       }
+      if (good && has_late) send_late(0);
       if (!good)  // let the copies in flight land before the CTA leaves
         for (int32_t q = max(0, used - rlen); q < used; ++q)
           mbar_wait(&B.kv_full[rbase + q % rlen], (q / rlen) & 1);
@@ -731,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // ================================================================ MMA issuers, one per lane
-    // Warps 12 and 13 (the other two of the warpgroup idle). In order S(0), S(1), then O(i), S(i+2):
+    // Warps 12 and 13. In order S(0), S(1), then O(i), S(i+2):
     // O(i) needs P(i) and V(i); S(i+2) needs K(i+2) and overwrites the tensor memory from which
     // O(i) reads P(i), which it may as the tensor pipe runs one thread's MMAs in issue order; the
     // commit that signals S(i+2) covers O(i). The warp runs in lockstep, an elected lane issues.
@@ -803,6 +859,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!good) {  // the MMAs in flight end before tensor memory is given back
         umma_commit_elect(&B.drained[X]);
         mbar_wait(&B.drained[X], 0);
+      }
+    } else if (has_late) {
+      // ============================================================== late rows of V, a warp per lane
+      // Brings the rows that the producer names, four channels per thread, to the places that the
+      // bulk copies' 128-byte swizzle gives them. (16 x 4 rows on 20011 tokens take 47.9 us so, 47.2
+      // with all rows by bulk copies, and 50.9 with these loads in the producers' own turn. Without the
+      // prefetch, two steps before, 16 x 16 rows take 141.3 us instead of 140.)
+      const int X = warp - 14;
+#pragma unroll 1
+      for (int32_t k = 0;; ++k) {
+        if (!wait_or_fail(&B.late_full[X][k % kLateQueue], (k / kLateQueue) & 1, fail)) break;
+        const Late e = B.late[X][k % kLateQueue];
+        if (e.z <= 0) break;  // no more
+        const int32_t z = min(e.z, kStep);
+        const uint32_t to = sbase + off_ring + e.slot * kStage + (lane >> 4) * kKvHalf + (lane & 1) * 8;
+        const uint2* from = reinterpret_cast<const uint2*>(p.v_cache + ((int64_t)e.tok * p.Hkv + e.g) * 128) + lane;
+        bool odd = false;
+#pragma unroll 1
+        for (int32_t x0 = e.y; x0 < z; x0 += 4) {
+          uint2 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (x0 + u < z) v[u] = from[(int64_t)(x0 + u) * p.Hkv * 32];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int32_t x = x0 + u;
+            if (x < z) {
+              const uint2 f = make_uint2(finite_bf16x2(v[u].x), finite_bf16x2(v[u].y));
+              odd |= f.x != v[u].x || f.y != v[u].y;
+              st_shared_v2(to + x * 128 + ((((lane >> 1) & 7) ^ (x & 7)) << 4), f);
+            }
+          }
+        }
+        odd = __any_sync(0xffffffffu, odd);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read them by that proxy
+        __syncwarp();
+        if (lane == 0) {
+          if (odd) *(volatile int32_t*)&B.odd[X] = 1;
+          mbar_arrive(&B.kv_full[e.slot]);
+        }
+        __syncwarp();
       }
     }
     __syncwarp();
@@ -940,6 +1037,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 16; ++x, po += cap)
             *po = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+      }
+      if (LATE && mine && s.kind == 2 && *(volatile int32_t*)&B.odd[X] != 0) {
+        // rare: what is not finite in V of the segment's late keys that the row sees (their weights are
+        // above 0, so it is added as it is)
+        po -= 32 * cap;
+        const int32_t end = min(s.vis + token, s.key0 + s.n * kStep);
+#pragma unroll 1
+        for (int32_t key = max(s.key0, s.seq - p.N + 1); key < end; ++key) {
+          int32_t page = p.page_table[(int64_t)s.b * p.max_blocks + key / MSA_BLOCK_TOKENS];
+          if (page < 0 || page >= p.num_pages) page = 0;
+          const int64_t cell = (int64_t)page * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+          const uint2* v = reinterpret_cast<const uint2*>(p.v_cache + (cell * p.Hkv + s.g) * 128);
+#pragma unroll 1
+          for (int x = 0; x < 32; ++x) {
+            const uint2 f = make_uint2(finite_bf16x2(v[x].x), finite_bf16x2(v[x].y));
+            if (f.x == v[x].x && f.y == v[x].y) continue;
+            float4 a = po[x * cap];
+            a.x += bf16_lo(v[x].x ^ f.x);
+            a.y += bf16_hi(v[x].x ^ f.x);
+            a.z += bf16_lo(v[x].y ^ f.y);
+            a.w += bf16_hi(v[x].y ^ f.y);
+            po[x * cap] = a;
+          }
+        }
       }
     }
   }
@@ -1145,6 +1266,47 @@ Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
   return y;
 }
 
+struct Maps {
+  CUtensorMap qt, qo, qu, km, vm;
+  TailMaps vt;
+};
+
+template <bool LATE>
+cudaError_t launch_kernels(const Maps& m, const KParams& p, cudaStream_t stream) {
+  cudaError_t e;
+  static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, shared_prefix_kernel<LATE>);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  static std::atomic<size_t> raised[kMaxDevices];
+  e = launch_with_smem(shared_prefix_kernel<LATE>, kSmemBytes, raised, [&] {
+    return cudaLaunchKernelEx(&cfg, shared_prefix_kernel<LATE>, m.qt, m.qo, m.qu, m.km, m.vm, m.vt, p);
+  });
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(p.Hkv * (((int64_t)p.rows_g + kJoinRows - 1) / kJoinRows)));
+  cfg.dynamicSmemBytes = 0;
+  const bool many = (int64_t)cfg.gridDim.x <= p.ctas;  // a CTA of 1024 threads fills an SM
+  cfg.blockDim = dim3(kJoinRows * 32 * (many ? kJoinSplit : 1));
+  e = many ? cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<kJoinSplit>, p)
+           : cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<1>, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 }  // namespace
 
 size_t shared_prefix_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
@@ -1178,6 +1340,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.rows_u = y.rows_u;
   p.q_rows = y.q_rows;
   p.rows_l = y.rows_l;
+  p.v_cache = a.v_cache;
   uint8_t* w = a.workspace;
   p.prefix = reinterpret_cast<int32_t*>(w + y.prefix);
   p.range_s = reinterpret_cast<int2*>(w + y.range_s);
@@ -1193,8 +1356,7 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   p.lse = a.lse;
   // query rows as (channel half, head of the group, row, half, group): a box is G heads of
   // consecutive rows, one 128-byte line each
-  CUtensorMap qt, qo, qu, km, vm;
-  TailMaps vt;
+  Maps m;
   const uint64_t qd[5] = {64, (uint64_t)G, (uint64_t)a.B * a.N, 2, (uint64_t)a.Hkv};
   const uint64_t qs[4] = {256, (uint64_t)a.Hq * 256, 128, (uint64_t)G * 256};
   const uint32_t bt[5] = {64, (uint32_t)G, (uint32_t)y.tpt, 1, 1};
@@ -1204,49 +1366,17 @@ cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t 
   const uint64_t kd[4] = {64, (uint64_t)a.num_pages * 128, 2, (uint64_t)a.Hkv};
   const uint64_t ks[3] = {(uint64_t)a.Hkv * 256, 128, 256};
   const uint32_t bk[4] = {64, kStep, 2, 1};
-  if (!encode_bf16_map(&qt, a.q, 5, qd, qs, bt, true) ||
-      !encode_bf16_map(&qo, a.q, 5, qd, qs, bo, true) ||
-      !encode_bf16_map(&qu, a.q, 5, qd, qs, bu, true) ||
-      !encode_bf16_map(&km, a.k_cache, 4, kd, ks, bk, true) ||
-      !encode_bf16_map(&vm, a.v_cache, 4, kd, ks, bk, true))
+  if (!encode_bf16_map(&m.qt, a.q, 5, qd, qs, bt, true) ||
+      !encode_bf16_map(&m.qo, a.q, 5, qd, qs, bo, true) ||
+      !encode_bf16_map(&m.qu, a.q, 5, qd, qs, bu, true) ||
+      !encode_bf16_map(&m.km, a.k_cache, 4, kd, ks, bk, true) ||
+      !encode_bf16_map(&m.vm, a.v_cache, 4, kd, ks, bk, true))
     return cudaErrorInvalidValue;
   for (int b = 0; b < 6; ++b) {
     const uint32_t box[4] = {64, 1u << b, 1, 1};
-    if (!encode_bf16_map(&vt.m[b], a.v_cache, 4, kd, ks, box, true)) return cudaErrorInvalidValue;
+    if (!encode_bf16_map(&m.vt.m[b], a.v_cache, 4, kd, ks, box, true)) return cudaErrorInvalidValue;
   }
-  cudaError_t e;
-  static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, shared_prefix_kernel);
-    if (e != cudaSuccess) return e;
-    regs.store(fa.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  static std::atomic<size_t> raised[kMaxDevices];
-  e = launch_with_smem(shared_prefix_kernel, kSmemBytes, raised, [&] {
-    return cudaLaunchKernelEx(&cfg, shared_prefix_kernel, qt, qo, qu, km, vm, vt, p);
-  });
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(a.Hkv * (((int64_t)y.rows_g + kJoinRows - 1) / kJoinRows)));
-  cfg.dynamicSmemBytes = 0;
-  const bool many = (int64_t)cfg.gridDim.x <= ctas;  // a CTA of 1024 threads fills an SM
-  cfg.blockDim = dim3(kJoinRows * 32 * (many ? kJoinSplit : 1));
-  cfg.stream = stream;
-  e = many ? cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<kJoinSplit>, p)
-           : cudaLaunchKernelEx(&cfg, shared_prefix_join_kernel<1>, p);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e;
+  return a.N > 1 ? launch_kernels<true>(m, p, stream) : launch_kernels<false>(m, p, stream);
 }
 
 }  // namespace msa

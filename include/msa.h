@@ -437,8 +437,8 @@ MSA_API int msa_append_kv(const uint16_t* k, int64_t k_stride, const uint16_t* v
  * request is better given a call of its own (or seq_lens[b] = 0 in this one).
  * A request with seq_lens[b] = 0 (a padding row of a captured batch), and any row at a negative
  * position, sees no key: o = 0, lse = -inf. Cache cells past a request's length may hold
- * anything, NaN included. (A non-finite V of one of the last N tokens of a request can reach
- * the request's earlier rows too.)
+ * anything, NaN included, and what is not finite in K or V of one of a request's last N tokens
+ * reaches only the rows that see that token.
  * Precision: scores, softmax sums, partial outputs and lse are fp32. The softmax weights are rounded
  * to bf16 for their product with V (the tensor cores take both operands in one type; the library's
  * other attention calls do the same), and o once at the end. So o is off by at most about

@@ -726,6 +726,36 @@ def test_the_first_call_of_a_process_can_be_a_captured_one():
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+@pytest.mark.parametrize("seq,shared,N,Hq,Hkv", [
+    ([300, 421, 515, 260], 256, 4, 32, 4), ([130, 129, 143, 144, 128], 64, 16, 64, 4),
+    ([3, 2, 1, 70, 5], 0, 6, 8, 2), ([1030 + i for i in range(40)], 1024, 2, 64, 4),
+    ([64, 65, 66, 67, 68], 0, 5, 16, 1),
+])
+@pytest.mark.parametrize("what", ["v", "k"])
+def test_non_finite_later_tokens_reach_no_earlier_row(seq, shared, N, Hq, Hkv, what):
+    """Token j of the last N holds NaN or infinity: rows at its position and behind it show it, rows
+    before it are what they are without."""
+    w = make_decode(seq, shared, N, Hq, Hkv, seed=70 + N)
+    clean = ref_decode(w)
+    for back, junk in ((0, float("nan")), (N // 2, float("inf")), (N - 2, float("-inf"))):
+        bad = dict(w, kc=w["kc"].clone(), vc=w["vc"].clone())
+        sees = torch.zeros(len(seq) * N, dtype=torch.bool)
+        for b, n in enumerate(seq):
+            at = n - 1 - back
+            if at < 0 or b % 3 == 2:  # some requests have nothing of the kind
+                continue
+            bad[what + "c"][w["table"][b, at // PAGE], at % PAGE] = junk
+            sees[b * N + N - 1 - back:(b + 1) * N] = True
+        o, lse = run_decode(bad)
+        check_decode((o[~sees.to(DEV)], lse[~sees.to(DEV)]), [x[~sees] for x in clean])
+        seen = o.cpu()[sees]
+        if what == "v":
+            assert not torch.isfinite(seen).any()
+            assert torch.equal(torch.isfinite(lse.cpu()), torch.isfinite(clean[1]))
+        elif back == 0:
+            assert torch.isnan(seen).all()
+
+
 def test_out_of_range_page_reads_page_zero():
     w = make_decode([300, 520], 256, 1, 16, 2, seed=9)
     bad = dict(w, table=w["table"].clone())
