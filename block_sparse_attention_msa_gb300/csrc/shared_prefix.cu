@@ -109,16 +109,17 @@ struct Bars {
   uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][step & 1]
   uint64_t o_free[2];                    // per segment: O read
   uint64_t seg_full[2][kQueue], seg_free[2][kQueue];
-  uint64_t late_full[2][kLateQueue];
   uint64_t drained[2];
   Seg seg[2][kQueue];
-  Late late[2][kLateQueue];
-  int32_t odd[2];  // a late row of the lane was not finite, in this segment or one before
   uint32_t tmem_base;
   int32_t fail;
   // plan
   int32_t w_min[kThreads / 32], w_first[kThreads / 32], w_sum[kThreads / 32];
   int32_t start_b[2], start_rem[2];
+  // with late rows
+  uint64_t late_full[2][kLateQueue];
+  Late late[2][kLateQueue];
+  int32_t odd[2];  // a late row of the lane was not finite, in this segment or one before
 };
 constexpr size_t kSmemBytes = kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.drained[x], 1);
       for (int i = 0; i < kQueue; ++i) {
         mbar_init(&B.seg_full[x][i], 1);
-        mbar_init(&B.late_full[x][i], 1);
+        if (LATE) mbar_init(&B.late_full[x][i], 1);
         mbar_init(&B.seg_free[x][i], 6);  // readers: four softmax warps, an issuer, a K/V producer
       }
       for (int i = 0; i < 2; ++i) {
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     B.fail = 0;
-    B.odd[0] = B.odd[1] = 0;
+    if (LATE) B.odd[0] = B.odd[1] = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int32_t tok1 = 0, g1 = 0, z1 = 0, tok2 = 0, g2 = 0, z2 = 0;  // steps i - 1 and i - 2
       bool good = true;
       // Of a step in which the request has z more keys: the first late one (kStep: none), how many.
-      auto late_from = [&](int32_t z) { return max(0, min(z - (LATE ? p.N - 1 : 0), kStep)); };
+      auto late_from = [&](int32_t z) { return max(0, min(z - (p.N - 1), kStep)); };
       auto late_rows = [&](int32_t z) { return LATE ? max(0, min(z, kStep) - late_from(z)) : 0; };
       // To the lane's late-row warp: the late rows of V's step i - 2 for the current stage; z = 0: no more.
       int32_t late_k = 0;
@@ -629,9 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // from the late-row warp, whose arrival is then the stage's.
       auto begin = [&](uint32_t bytes, int32_t z) {
         if (used >= rlen && !wait_or_fail(&B.kv_empty[rbase + r.slot], r.phase ^ 1u, fail)) return false;
-        const int32_t late = late_rows(z);
-        if (LATE && late > 0) {
-          if (lane == 0) mbar_expect_tx_only(&B.kv_full[rbase + r.slot], bytes - late * 256);
+        if (LATE && late_rows(z) > 0) {
+          if (lane == 0) mbar_expect_tx_only(&B.kv_full[rbase + r.slot], bytes - late_rows(z) * 256);
           send_late(z);
         } else if (lane == 0) {
           mbar_expect_tx(&B.kv_full[rbase + r.slot], bytes);
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // last token may hold anything, NaN included, and 0 * NaN is NaN, so those rows are not
       // loaded: zeros come in their place, by the same engine.
       auto load_v = [&]() {
-        const int32_t y = late_from(z2), z = min(z2, kStep);
+        const int32_t y = LATE ? late_from(z2) : z2;
         if (y >= kStep) {
           load(&vmap, 0, tok2, g2);
           return;
@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(dst + at * 128, &vtail.m[b], full, 0, tok2 + at, lane, g2);
               at += 1 << b;
             }
-          if (z < kStep) bulk_load(dst + z * 128, g_zero_rows, (kStep - z) * 128, full);
+          if (LATE) at = min(z2, kStep);
+          if (!LATE || at < kStep) bulk_load(dst + at * 128, g_zero_rows, (kStep - at) * 128, full);
         }
         __syncwarp();
       };
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tok1 = tok;
           g1 = s.g;
           z1 = s.seq - key;
-          if (lane < 2 * late_rows(z1)) {  // two lines a row: they are there when V's turn comes
+          if (LATE && lane < 2 * late_rows(z1)) {  // two lines a row: they are there when V's turn comes
             const uint16_t* v = p.v_cache + ((int64_t)(tok + late_from(z1) + (lane >> 1)) * p.Hkv + s.g) * 128;
             asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (lane & 1) * 64));
           }
