@@ -14,7 +14,7 @@
 // search there. The bytes are few (a 32768-token step writes 0.5 MB): the launch and the chain
 // load -> scan -> search -> page -> store bound the time, so a step of few tokens takes one CTA.
 // Measured, replayed from a graph: 2.5 us for 8 requests of one token, 4.1 us for 61 requests and
-// 65453 token rows (128 GB/s), 6.4 us for 512 requests behind 256 shared pages (262656 token rows and
+// 65453 token rows (128 GB/s), 6.6 us for 512 requests behind 256 shared pages (262656 token rows and
 // 131072 shared entries, 2.6 MB: 0.4 TB/s). A launch that is one load and one store deep takes 1.9 us.
 #include "common.cuh"
 #include "host_util.h"

@@ -33,12 +33,13 @@
 // chain S -> softmax -> O of one step does not bound the rate.
 //
 // Measured (64 query heads on 8 KV heads, N = 1, one call replayed from a graph): 256 requests on
-// 32K shared tokens with 1 to 1024 private ones 256 us (1090 TFLOP/s); 64 on 64K with 1 to 2048
-// 128 us (4.2 TB/s); 64 with 1 to 8192 behind 2000 176 us (6.2 TB/s); 8 on 60K with 1 to 512 53 us
-// (4.8 TB/s). The pairs alone (256 requests, 32K shared tokens, one private) run at 1330 TFLOP/s,
-// 70% of what a dense bf16 product reaches: what is left is the handover between each
-// step's softmax and MMAs, and the power limit (1360 W in a loop, the SM clock at 1.72 to 1.95 GHz).
-// Private work alone (64 requests of 8K tokens) reads 6.6 TB/s, 97% of a copy.
+// 32K shared tokens with 1 to 1024 private ones 253 to 271 us, by the GPU (1030 to 1100 TFLOP/s); 64
+// on 64K with 1 to 2048 127 to 132 us (4.1 to 4.3 TB/s); 64 with 1 to 8192 behind 2000 178 us (6.1
+// TB/s); 8 on 60K with 1 to 512 53 us (4.8 TB/s). The pairs alone (256 requests, 32K shared tokens,
+// one private) run at 1320 TFLOP/s, 70% of what a dense bf16 product reaches: what is left is the
+// handover between each step's softmax and MMAs, and the power limit (1360 W in a loop, the SM
+// clock at 1.72 to 1.95 GHz). Private work alone (64 requests of 8K tokens) reads 6.6 TB/s, 98% of a
+// copy.
 // What was slower: one issuer for both lanes (207 -> 260 us), the lanes' softmax taking turns
 // (207 -> 292 us), two warpgroups per lane on half of the keys each, four issuers (equal).
 #include "common.cuh"
@@ -1230,9 +1231,9 @@ Layout layout_of(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas) {
   y.rows_u = G * (N < y.tpt ? N : y.tpt);
   y.q_rows = y.rows_u <= 64 && y.rows_g - 256 * y.pairs <= 64 ? 64 : 128;
   y.rows_l = (y.rows_g - 256 * y.pairs + 7) / 8 * 8;
-  // pairs that walk the prefix together: enough that DRAM feeds them (4 to 8 of the CTAs on one
-  // stream of keys), few enough that whole runs of them split the CTAs evenly, and without idle
-  // places in the last round
+  // pairs that walk the prefix together, at most 16: enough that DRAM feeds them (four or more on one
+  // stream of keys where there are as many), few enough that whole runs of them split the CTAs
+  // evenly, and without idle places in the last round (9, 11 or 13 pairs all walk together)
   y.abreast = 1;
   float best = 1e30f;
   for (int32_t n = 1; n <= 16 && n <= y.pairs; ++n) {

@@ -433,8 +433,10 @@ MSA_API int msa_append_kv(const uint16_t* k, int64_t k_stride, const uint16_t* v
  * request), and each request reads the rest through its own table. shared_len = 0 is a plain
  * paged decode. One short active request so ends the sharing for the whole batch: with 63 requests
  * on a 65536-token document and one of 40 tokens the prefix pass covers nothing, and each of the 63
- * reads all of its keys for itself. The answer is the same, the keys are read up to B times; such a
- * request is better given a call of its own (or seq_lens[b] = 0 in this one).
+ * reads all of its keys for itself (64 requests with 64 heads: 1.7 ms instead of 0.1). The answer is
+ * the same, the keys are read up to B times; such a request is better given a call of its own (and
+ * seq_lens[b] = 0 in this one). Padding requests keep their rows in the prefix pass: 8 requests on
+ * 60032 tokens take 56 us, in a batch padded to 64 116 us and to 256 317 us.
  * A request with seq_lens[b] = 0 (a padding row of a captured batch), and any row at a negative
  * position, sees no key: o = 0, lse = -inf. Cache cells past a request's length may hold
  * anything, NaN included, and what is not finite in K or V of one of a request's last N tokens
