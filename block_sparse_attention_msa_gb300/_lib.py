@@ -47,6 +47,13 @@ SIGNATURES = [
     ("msa_shared_prefix_decode_workspace_size", SZ, [I32, I32, I32, I32]),
     ("msa_shared_prefix_decode", ctypes.c_int,
      [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, P, P, P, SZ, P]),
+    ("msa_chunk_attention_workspace_size", SZ, [I32, I32, I32, I32, I32]),
+    ("msa_chunk_attention", ctypes.c_int,
+     [P, I64, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, P, P, P, SZ, P]),
+    ("msa_append_kv_fp8", ctypes.c_int, [P, I64, P, I64, P, I32, I32, I32, I64, P, P, P, P, P]),
+    ("msa_gather_kv_fp8", ctypes.c_int, [P, P, P, P, I64, P, I32, I32, I32, P, P, P]),
+    ("msa_paged_sparse_decode_fp8", ctypes.c_int,
+     [P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I64, P, P, P, SZ, P]),
     ("msa_last_error", ctypes.c_char_p, []),
     ("msa_device_error", ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     ("msa_version", ctypes.c_char_p, []),

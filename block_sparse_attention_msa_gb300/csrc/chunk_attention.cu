@@ -1,0 +1,1230 @@
+// Causal attention of a ragged batch over the paged cache: request b's new tokens (any number of them,
+// its last positions) see every key of the request up to their own. One call serves prompts, chunks of
+// prompts behind a cached prefix, and decode rows, mixed in one batch as a scheduler packs them.
+//
+// Softmax attention over a key set that is split into parts needs of each part only
+//   m = max s,  l = sum 2^(s - m),  O = sum 2^(s - m) v      (s in log2 units)
+// and the parts join as M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.
+//
+//  * Tiles. The G heads of a KV group see the same keys, so 128 / G tokens x G heads are the 128 rows of a
+//    tcgen05.mma tile. Two tiles with the same keys share each K/V step that a CTA loads ("shared" units).
+//    Tokens that fill one tile at most (decode rows, the rest of a chunk) give each of the CTA's two
+//    lanes a KV group, or half of the keys, of its own: their MMAs run far below their rate, but a step's
+//    keys take longer to arrive than the padded MMAs take.
+//  * Units. A tile pair (or tile) is cut along its keys into pieces of at most max(8 steps, an eighth
+//    of what is left per CTA... see piece_cost) so that the last units to start are short. A piece that is
+//    its whole tile writes the output itself; others leave partials that a second kernel joins in
+//    their order. The plan kernel makes the list of units from the lengths on the GPU, so a call can be
+//    captured once and replayed with other lengths. CTAs take units from the list one after the other;
+//    which CTA takes which changes no result.
+//  * The order (request, group, last tiles first, pieces) lets the CTAs that run at the same time read
+//    the same keys, and DRAM once.
+//  * V cells that a row must not use (later tokens of its request, what lies behind its last token) are
+//    multiplied by weights of 0, and 0 * NaN is NaN. So in steps that hold such cells two warps
+//    look through V in shared memory before the MMAs: rows behind the request's end become zeros, and so
+//    does what is not finite, which the softmax warps then add to the rows that see it.
+//
+// Per lane S = Q K^T (128 x 64 x 128) and O += P V run on tcgen05 with S, P and O in tensor memory; one
+// softmax warpgroup per lane keeps the running reference and sum in fp32. P is rounded to bf16 for its
+// product, as tensor cores take it beside V in bf16 (2^-9 of each weight at most); its sum l is taken
+// before that rounding. A step is 64 keys because then S has two buffers per lane next to O (2 lanes x
+// (2 x 64 + 128) = 512 columns): S(i+1) is ready when the softmax of step i ends.
+#include <math.h>
+
+#include "common.cuh"
+#include "host_util.h"
+#include "kernels.h"
+#include "softmax_math.cuh"
+
+MSA_DEFINE_ERROR_WORD(chunk)
+
+namespace msa {
+
+namespace {
+
+constexpr int kThreads = 512;                    // warpgroups: loads, softmax x 2, MMA issue
+constexpr int kLaunchRegs = 128;                 // registers per thread at launch, then split
+constexpr int kRegsLoad = 64, kRegsIssue = 64, kRegsSoftmax = 192;
+static_assert(128 * (kRegsLoad + kRegsIssue) + 256 * kRegsSoftmax == kThreads * kLaunchRegs, "register split");
+constexpr int kStep = 64;                        // keys per step
+constexpr uint32_t kQHalf = 128 * 128;           // 128 rows x 64 channels bf16
+constexpr uint32_t kQTile = 2 * kQHalf;
+constexpr uint32_t kKvHalf = kStep * 128;        // 64 keys x 64 channels bf16
+constexpr uint32_t kKvTile = 2 * kKvHalf;        // K or V of one step: 16 KB, one slot of the ring
+constexpr int kSlots = 10;
+constexpr uint32_t kOffRing = 2 * kQTile;
+constexpr uint32_t kOffBar = kOffRing + kSlots * kKvTile;
+constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFarSum = 16384.f;  // of a step's P: beyond it the softmax's reference moves
+// s log2(e) - m in one fma is off by what m was rounded by, the same for all keys of a row: a common
+// factor of P and l. Beyond this magnitude of m it would leave fp32's range, and m is subtracted first.
+constexpr float kFarRef = 16777216.f;
+constexpr int kMinPiece = 8;        // steps of a piece, where the whole call has as many per CTA
+
+// What a CTA does next: for each lane a tile and a run of steps.
+struct __align__(16) Unit {
+  int32_t n[2];     // steps; 0: nothing for the lane. Both 0: there are no more units.
+  int32_t key0[2];  // first keys
+  int32_t g[2];     // groups
+  int32_t part[2];  // first row of the lane's partial, or -1: the run is the whole tile
+  int32_t b;        // page-table row
+  int32_t row;      // first token row of the (first) tile
+  int32_t tokens;   // of the tile, or of both
+  int32_t pos;      // position of the first token
+  int32_t seq;      // keys that the request holds
+  int32_t shared;   // 1: two tiles on the same steps
+  int32_t pad[2];
+};
+static_assert(sizeof(Unit) == 64, "read by 16 lanes");
+// A tile whose pieces are to be joined.
+struct __align__(16) JoinTile {
+  int32_t row, rows, g;  // first token row, valid rows, group
+  int32_t part;          // first row of the first piece's partial
+  int32_t step;          // rows from piece to piece
+  int32_t pieces, cap;   // cap: rows of a partial
+  int32_t pad;
+};
+struct Header {
+  int32_t units, joins, ticket;
+};
+
+struct KParams {
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_tokens;
+  int32_t B, T, G, Hq, Hkv, max_blocks;
+  int64_t num_pages;
+  int32_t gs;         // log2 of G
+  int32_t tpt;        // tokens per tile: 128 / G
+  int32_t ctas;
+  int32_t cap_units, cap_joins;
+  int64_t cap_rows;
+  Header* head;
+  Unit* units;
+  JoinTile* joins;
+  float* po;          // partials: O as [32 channel quads][cap rows][4] fp32 from row * 128 on
+  float2* ml;         // (m, l) per row
+  const uint16_t* v_cache;
+  uint16_t* o;
+  float* lse;
+};
+
+// ------------------------------------------------------------------------------ plan
+constexpr int kPlanThreads = 1024;
+
+struct Request {
+  int32_t t0, n, seq;  // first token row, new tokens, keys held
+};
+__device__ __forceinline__ Request request_of(const KParams& p, int b, bool& bad) {
+  Request r;
+  const int32_t c0 = p.cu_tokens[b], c1 = p.cu_tokens[b + 1], s = p.seq_lens[b];
+  r.t0 = min(max(c0, 0), p.T);
+  r.n = max(min(c1, p.T) - r.t0, 0);
+  const int32_t hi = p.max_blocks * MSA_BLOCK_TOKENS;
+  r.seq = min(max(s, 0), hi);
+  bad = c0 < 0 || c1 > p.T || c1 < c0 || s < r.n || s > hi;
+  return r;
+}
+// Items of a request: its pairs of tiles x groups, then a last single tile's lane pairs.
+struct Shape {
+  int32_t np, single, ps, items;
+};
+__device__ __forceinline__ Shape shape_of(const KParams& p, int32_t n) {
+  Shape s;
+  const int32_t w = 2 * p.tpt;
+  s.np = (n + w - 1) / w;
+  s.single = n > 0 && n - (s.np - 1) * w <= p.tpt;
+  s.ps = s.np - s.single;
+  s.items = s.ps * p.Hkv + (s.single ? max(1, p.Hkv / 2) : 0);
+  return s;
+}
+struct Item {
+  int32_t b, row, tokens, pos, seq, g, shared;
+  int32_t steps, cost;  // cost: steps of the CTA
+};
+__device__ __forceinline__ Item item_of(const KParams& p, int b, const Request& r, const Shape& s, int32_t i) {
+  Item t;
+  const int32_t w = 2 * p.tpt;
+  t.b = b;
+  t.seq = r.seq;
+  int32_t j = s.np - 1;
+  t.shared = i < s.ps * p.Hkv;
+  if (t.shared) {
+    t.g = i / s.ps;
+    j = s.ps - 1 - (i - t.g * s.ps);
+  } else {
+    t.g = 2 * (i - s.ps * p.Hkv);
+  }
+  t.row = r.t0 + j * w;
+  t.tokens = min(w, r.n - j * w);
+  t.pos = r.seq - r.n + j * w;
+  t.steps = max(1, (t.pos + t.tokens + kStep - 1) / kStep);
+  t.cost = !t.shared && p.Hkv == 1 ? (t.steps + 1) / 2 : t.steps;
+  return t;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+// Exclusive scan over the CTA; total of all threads.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t incl = warp_scan(x, lane);
+  __syncthreads();  // sums is free
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) sums[lane] = warp_scan(sums[lane], lane);
+  __syncthreads();
+  total = sums[31];
+  return incl - x + (warp > 0 ? sums[warp - 1] : 0);
+}
+static_assert(kPlanThreads == 1024, "block_scan: 32 warps");
+
+// Pieces of an item at which `left` steps of the whole call, its own among them, are still to come:
+// half of a CTA's share of them each, so that the CTAs end together.
+__device__ __forceinline__ int32_t pieces_of(const KParams& p, int32_t cost, int64_t left, int32_t least) {
+  const int32_t most = (int32_t)max((int64_t)least, (left + 2 * p.ctas - 1) / (2 * p.ctas));
+  return (cost + most - 1) / most;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ KParams p) {
+  extern __shared__ int32_t first_item[];  // [B + 1]
+  __shared__ int64_t sums[32];
+  const int tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the requests' items
+  int64_t items = 0;
+  bool any_bad = false;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int32_t n = 0;
+    if (b < p.B) {
+      bool bad;
+      const Request r = request_of(p, b, bad);
+      any_bad |= bad;
+      n = shape_of(p, r.n).items;
+    }
+    int64_t total;
+    const int64_t at = items + block_scan(n, sums, total);
+    if (b < p.B) first_item[b] = (int32_t)min(at, kMaxChunkItems);
+    items += total;
+  }
+  if (items > kMaxChunkItems) {  // token ranges that overlap: not seen with lengths that add up
+    items = kMaxChunkItems;
+    any_bad = true;
+  }
+  if (tid == 0) first_item[p.B] = (int32_t)items;
+  if (any_bad) msa_record_error(kErrBadBlock);
+  __syncthreads();
+  // a thread has a run of items
+  const int32_t per = (int32_t)((items + kPlanThreads - 1) / kPlanThreads);
+  const int32_t i0 = (int32_t)min(items, (int64_t)tid * per), i1 = (int32_t)min(items, (int64_t)i0 + per);
+  int32_t b_first = 0;
+  if (i0 < i1) {
+    int32_t lo = 0, hi = p.B;  // first_item[lo] <= i0 < first_item[hi]
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) / 2;
+      if (first_item[mid] <= i0) lo = mid;
+      else hi = mid;
+    }
+    b_first = lo;
+  }
+  auto each = [&](auto&& f) {
+    int32_t b = b_first, i = i0;
+    while (i < i1) {
+      while (first_item[b + 1] <= i) ++b;
+      bool bad;
+      const Request r = request_of(p, b, bad);
+      const Shape s = shape_of(p, r.n);
+      const int32_t end = min(i1, first_item[b + 1]);
+      for (; i < end; ++i) f(item_of(p, b, r, s, i - first_item[b]));
+    }
+  };
+  int64_t cost = 0, all;
+  each([&](const Item& t) { cost += t.cost; });
+  const int64_t before = block_scan(cost, sums, all);
+  const int32_t least = (int32_t)min((int64_t)kMinPiece, max((int64_t)2, (all + p.ctas - 1) / p.ctas));
+  // runs of an item's lanes in all pieces, and what they need
+  auto runs_of = [&](const Item& t, int32_t pieces) {
+    return !t.shared && p.Hkv == 1 && (pieces > 1 || t.steps >= 4) ? 2 * pieces : pieces;
+  };
+  auto cap_of = [&](const Item& t) { return t.shared ? 128 : ((t.tokens << p.gs) + 7) / 8 * 8; };
+  int64_t left = all - before;
+  int32_t n_units = 0, n_joins = 0;
+  int64_t n_rows = 0;
+  each([&](const Item& t) {
+    const int32_t pieces = pieces_of(p, t.cost, left, least), runs = runs_of(t, pieces);
+    const int32_t lanes = t.shared || p.Hkv > 1 ? 2 : 1;
+    n_units += pieces;
+    if (runs > 1) {
+      n_joins += lanes;
+      n_rows += (int64_t)runs * lanes * cap_of(t);
+    }
+    left -= t.cost;
+  });
+  int64_t total_units, total_joins, total_rows;
+  int64_t at_unit = block_scan(n_units, sums, total_units);
+  int64_t at_join = block_scan(n_joins, sums, total_joins);
+  int64_t at_row = block_scan(n_rows, sums, total_rows);
+  if (tid == 0) {
+    p.head->units = (int32_t)min(total_units, (int64_t)p.cap_units);
+    p.head->joins = (int32_t)min(total_joins, (int64_t)p.cap_joins);
+    p.head->ticket = p.ctas;  // the first units are the CTAs' own numbers
+    // not seen with lengths that add up: the workspace is sized for those
+    if (total_units > p.cap_units || total_joins > p.cap_joins || total_rows > p.cap_rows)
+      msa_record_error(kErrBadBlock);
+  }
+  left = all - before;
+  each([&](const Item& t) {
+    const int32_t pieces = pieces_of(p, t.cost, left, least), runs = runs_of(t, pieces);
+    const int32_t lanes = t.shared || p.Hkv > 1 ? 2 : 1, cap = cap_of(t);
+    const bool halves = lanes == 1 && runs > 1;  // the lanes take neighbouring runs of one tile
+    const int64_t rows = runs > 1 ? (int64_t)runs * lanes * cap : 0;
+    const bool fits = at_row + rows <= p.cap_rows;
+    auto begin = [&](int32_t run) { return (int32_t)((int64_t)t.steps * run / runs); };
+    for (int32_t k = 0; k < pieces; ++k) {
+      if (at_unit + k >= p.cap_units) break;
+      Unit u{};
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        if (X == 1 && lanes == 1 && !halves) break;
+        const int32_t run = halves ? 2 * k + X : k;
+        const int32_t s0 = begin(run);
+        u.n[X] = fits ? begin(run + 1) - s0 : 0;
+        u.key0[X] = s0 * kStep;
+        u.g[X] = t.shared || lanes == 1 ? t.g : t.g + X;
+        u.part[X] = runs > 1 ? (int32_t)(at_row + ((int64_t)run * lanes + (halves ? 0 : X)) * cap) : -1;
+      }
+      if (!fits) u.n[0] = 1;  // keeps the list's end marker apart
+      u.b = t.b;
+      u.row = t.row;
+      u.tokens = fits ? t.tokens : 0;
+      u.pos = t.pos;
+      u.seq = t.seq;
+      u.shared = t.shared && fits;
+      const int4* src = reinterpret_cast<const int4*>(&u);
+      int4* dst = reinterpret_cast<int4*>(p.units + at_unit + k);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) dst[x] = src[x];
+    }
+    if (runs > 1)
+      for (int32_t X = 0; X < lanes; ++X) {
+        if (at_join + X >= p.cap_joins) break;
+        JoinTile j{};
+        const int32_t tile = t.shared ? X : 0;
+        j.row = t.row + tile * p.tpt;
+        j.rows = fits ? min(p.tpt, t.tokens - tile * p.tpt) << p.gs : 0;
+        j.g = t.shared || lanes == 1 ? t.g : t.g + X;
+        j.part = (int32_t)(at_row + (int64_t)X * cap);
+        j.step = lanes * cap;
+        j.pieces = runs;
+        j.cap = cap;
+        p.joins[at_join + X] = j;
+      }
+    at_unit += pieces;
+    if (runs > 1) at_join += lanes;
+    at_row += rows;
+    left -= t.cost;
+  });
+}
+
+// ------------------------------------------------------------------------------ attention
+// Rows of V [y, 64) of a slot that some row of the tiles must not use; from z on they lie behind the
+// request's end. slot < 0: no more. Each open entry has a slot of its own.
+struct Late {
+  int32_t y, z, slot, lanes;  // lanes: bit X: lane X reads it
+};
+constexpr int kLate = 16;
+static_assert(kLate > kSlots + 1, "an entry is not overwritten while it is open");
+constexpr int kQueue = 2;
+
+struct Bars {
+  uint64_t kv_full[kSlots], kv_empty[kSlots];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][the lane's step & 1]
+  uint64_t o_free[2];
+  uint64_t unit_full[kQueue], unit_free[kQueue];
+  uint64_t late_full[kLate];
+  uint64_t drained[2];
+  Unit unit[kQueue];
+  Late late[kLate];
+  int32_t odd[2];  // what is not finite was taken out of V, in this unit of the lane or one before
+  uint32_t tmem_base;
+  int32_t fail;
+};
+constexpr size_t kSmemBytes = kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+struct RingPos {
+  int32_t slot;
+  uint32_t phase;  // parity of the slot's current use
+  __device__ __forceinline__ void advance(int32_t n) {
+    slot += n;
+    if (slot >= kSlots) {
+      slot -= kSlots;
+      phase ^= 1u;
+    }
+  }
+  __device__ __forceinline__ RingPos after(int32_t n) const {
+    RingPos r = *this;
+    r.advance(n);
+    return r;
+  }
+};
+
+// Bounded wait of a converged warp; every thread gets the same answer. The flag that another role's
+// timeout sets is read only while the phase is open.
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *fail != 0)) return false;
+  }
+  msa_record_error(kErrTimeout);
+  *fail = 1;
+  return false;
+}
+// wait_or_fail for two barriers at once: half of the warp tests either.
+__device__ __forceinline__ bool wait_two_or_fail(uint64_t* bar0, uint32_t par0, uint64_t* bar1, uint32_t par1,
+                                                 volatile int32_t* fail) {
+  const bool lo = (threadIdx.x & 16) == 0;
+  const uint32_t bar = smem_u32(lo ? bar0 : bar1), par = lo ? par0 : par1;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_addr(bar, par))) return true;
+    if (__any_sync(0xffffffffu, *fail != 0)) return false;
+  }
+  msa_record_error(kErrTimeout);
+  *fail = 1;
+  return false;
+}
+// A value that is the same in all threads of a converged warp, in a form that lets the compiler see
+// it: operands of tensor-core and bulk-copy instructions that it cannot prove uniform cost a loop
+// over the threads each.
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Half of S = Q K^T: the four K-16 products of one channel half of 128-byte-swizzled tiles, issued
+// by one elected lane of the converged warp.
+__device__ __forceinline__ void issue_s(uint32_t d, uint64_t qd, uint64_t kd, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 t, 0, 1;\n setp.ne.b32 f, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(d),
+      "l"(qd), "l"(kd), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// O (+)= P V: four K-16 products, P in tensor memory (8 columns per 16 keys), V rows 2 KB apart.
+__device__ __forceinline__ void issue_o(uint32_t d, uint32_t p_tmem, uint64_t vd, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, t, f;\n .reg .b64 b;\n .reg .b32 a;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 t, 0, 1;\n setp.ne.b32 f, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
+      " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 16;\n add.s64 b, %2, 256;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 24;\n add.s64 b, %2, 384;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(d),
+      "r"(p_tmem), "l"(vd), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Two bf16 numbers, zero in the place of one that is not finite.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+  return x;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attention_kernel(const __grid_constant__ CUtensorMap qmap_t, const __grid_constant__ CUtensorMap qmap_1,
+                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                           const __grid_constant__ KParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];  // 1024: the swizzle atoms
+  Bars& B = *reinterpret_cast<Bars*>(smem + kOffBar);
+  volatile int32_t* fail = &B.fail;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = uniform(tid >> 5);
+  if (smem_u32(smem) & 1023u) {  // not seen: the declared alignment is kept
+    msa_record_error(kErrTimeout);
+    return;
+  }
+  if (tid == 64) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&B.kv_full[i], 2);   // the producer twice, or the two late-row warps
+      mbar_init(&B.kv_empty[i], 2);  // both issuers, or one and the producer
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&B.q_full[x], 1);
+      mbar_init(&B.q_empty[x], 1);
+      mbar_init(&B.o_free[x], 4);
+      mbar_init(&B.drained[x], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&B.s_full[x][i], 1);
+        mbar_init(&B.o_full[x][i], 1);
+        mbar_init(&B.p_full[x][i], 4);
+      }
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&B.unit_full[i], 1);
+      mbar_init(&B.unit_free[i], 11);  // readers: eight softmax warps, two issuers, the query loader
+    }
+    for (int i = 0; i < kLate; ++i) mbar_init(&B.late_full[i], 1);
+    B.fail = 0;
+    B.odd[0] = B.odd[1] = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&B.tmem_base)), "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+    tma_prefetch_desc(&qmap_t);
+    tma_prefetch_desc(&qmap_1);
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = uniform((int32_t)B.tmem_base);
+  const uint32_t sbase = smem_u32(smem);
+  // The plan ends here, and with it what precedes it in the stream. The join may be scheduled as CTAs of
+  // this kernel leave; it waits for all of their stores.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // The k-th unit for one of its readers.
+  auto take = [&](int32_t& k, Unit& u) {
+    const int q = k & (kQueue - 1);
+    if (!wait_or_fail(&B.unit_full[q], (k / kQueue) & 1, fail)) return false;
+    const Unit& e = B.unit[q];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      u.n[x] = uniform(e.n[x]);
+      u.key0[x] = uniform(e.key0[x]);
+      u.g[x] = uniform(e.g[x]);
+      u.part[x] = uniform(e.part[x]);
+    }
+    u.b = uniform(e.b);
+    u.row = uniform(e.row);
+    u.tokens = uniform(e.tokens);
+    u.pos = uniform(e.pos);
+    u.seq = uniform(e.seq);
+    u.shared = uniform(e.shared);
+    __syncwarp();
+    mbar_arrive_if(&B.unit_free[q], lane == 0);
+    ++k;
+    return true;
+  };
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    if (warp == 0) {
+      // ============================================================== units and K/V
+      // Takes units, publishes them and loads their keys and values, in the order in which the MMAs use
+      // them: V(i - 2), K(i) for each step i of the CTA's steps, a unit's behind the other's. A step of
+      // lanes with keys of their own has two slots for each.
+      RingPos r{0, 0};
+      int32_t used = 0;     // slots begun
+      int32_t late_n = 0;   // late entries
+      bool good = true;
+      struct Src {
+        int32_t tok[2], g[2], y[2], z[2];
+        int32_t lanes;  // bit X: lane X has the step; 4: both read one slot; 0: no step
+      };
+      // One slot: 64 rows of the map's tensor from token row tok on. `alone`: one lane reads it.
+      auto slot = [&](const CUtensorMap* map, int32_t tok, int32_t g, bool alone, bool late, int32_t y, int32_t z,
+                      int32_t lanes) {
+        if (used >= kSlots && !wait_or_fail(&B.kv_empty[r.slot], r.phase ^ 1u, fail)) return false;
+        const int32_t ut = uniform(tok), ug = uniform(g), us = uniform(r.slot);
+        if (lane == 0) {
+          uint64_t* full = &B.kv_full[us];
+          if (alone) mbar_arrive(&B.kv_empty[us]);
+          if (late) {
+            const int32_t q = late_n & (kLate - 1);
+            B.late[q] = {y, z, us, lanes};
+            full = &B.late_full[q];
+          } else {
+            mbar_arrive(full);
+          }
+          mbar_expect_tx(full, kKvTile);
+          tma_load_4d(smem + kOffRing + us * kKvTile, map, full, 0, ut, 0, ug);
+        }
+        __syncwarp();
+        if (late) ++late_n;
+        ++used;
+        r.advance(1);
+        return true;
+      };
+      auto emit = [&](const CUtensorMap* map, const Src& s, bool v) {
+        auto one = [&](int X, bool alone, int32_t lanes) {
+          return slot(map, s.tok[X], s.g[X], alone, v && s.y[X] < kStep, max(s.y[X], 0), max(s.z[X], 0), lanes);
+        };
+        if (s.lanes & 4) return one(0, false, 3);
+        if ((s.lanes & 1) && !one(0, true, 1)) return false;
+        if ((s.lanes & 2) && !one(1, true, 2)) return false;
+        return true;
+      };
+      const int32_t total = p.head->units;
+      int32_t ticket = blockIdx.x, k = 0;
+      Src d1, d2;
+      d1.lanes = d2.lanes = 0;
+#pragma unroll 1
+      for (;;) {
+        // ---- the next unit
+        const int q = k & (kQueue - 1);
+        const bool end = ticket >= total;
+        int32_t word = 0;
+        if (!end && lane < 16) word = reinterpret_cast<const int32_t*>(p.units + ticket)[lane];
+        if (k >= kQueue && !(good = wait_or_fail(&B.unit_free[q], (k / kQueue - 1) & 1, fail))) break;
+        if (lane < 16) reinterpret_cast<int32_t*>(&B.unit[q])[lane] = word;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.unit_full[q]);
+        ++k;
+        if (end) break;
+        int32_t n[2], key0[2], g[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          n[x] = __shfl_sync(0xffffffffu, word, x);
+          key0[x] = __shfl_sync(0xffffffffu, word, 2 + x);
+          g[x] = __shfl_sync(0xffffffffu, word, 4 + x);
+        }
+        const int32_t b = __shfl_sync(0xffffffffu, word, 8), pos = __shfl_sync(0xffffffffu, word, 11);
+        const int32_t seq = __shfl_sync(0xffffffffu, word, 12), shared = __shfl_sync(0xffffffffu, word, 13);
+        const int32_t steps = max(n[0], n[1]);
+        int32_t next = 0;
+        // the pages of 32 steps from j on of a lane's run, one per thread
+        auto look_up = [&](int x, int32_t j) {
+          const int32_t jj = j + lane, key = key0[x] + jj * kStep;
+          const bool has = jj < n[x] && key < seq;
+          int32_t page = has ? p.page_table[(int64_t)b * p.max_blocks + key / MSA_BLOCK_TOKENS] : 0;
+          const bool bad = page < 0 || page >= p.num_pages;
+          if (bad) page = 0;
+          if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
+          return page;
+        };
+        const bool apart = n[1] > 0 && key0[1] != key0[0];
+        int32_t page[2] = {0, 0};
+#pragma unroll 1
+        for (int32_t j = 0; j < steps; ++j) {
+          if ((j & 31) == 0) {
+            page[0] = look_up(0, j);
+            page[1] = apart ? look_up(1, j) : page[0];
+          }
+          if (j == max(0, steps - 6) && lane == 0) next = atomicAdd(&p.head->ticket, 1);
+          Src s;
+          s.lanes = shared ? 4 : (j < n[0] ? 1 : 0) | (j < n[1] ? 2 : 0);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int32_t key = key0[x] + j * kStep;
+            s.tok[x] = __shfl_sync(0xffffffffu, page[x], j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+            s.g[x] = g[x];
+            s.y[x] = pos + 1 - key;
+            s.z[x] = seq - key;
+          }
+          if (!(good = emit(&vmap, d2, true) && emit(&kmap, s, false))) break;
+          d2 = d1;
+          d1 = s;
+        }
+        if (!good) break;
+        ticket = __shfl_sync(0xffffffffu, next, 0);
+      }
+      good = good && emit(&vmap, d2, true) && emit(&vmap, d1, true);
+      if (good && lane == 0) {  // the late-row warps' end
+        B.late[late_n & (kLate - 1)] = {0, 0, -1, 0};
+        mbar_arrive(&B.late_full[late_n & (kLate - 1)]);
+      }
+      if (!good) {  // let the copies in flight land before the CTA leaves
+        for (int32_t q = max(0, used - kSlots); q < used; ++q)
+          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.kv_full[q % kSlots], (q / kSlots) & 1, 1000); ++x) {
+          }
+        for (int32_t q = max(0, late_n - kLate); q < late_n; ++q)
+          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.late_full[q % kLate], (q / kLate) & 1, 1000); ++x) {
+          }
+      }
+    } else if (warp == 1) {
+      // ============================================================== query tiles
+      int32_t k = 0, done[2] = {0, 0};
+      Unit u;
+      bool good = true;
+#pragma unroll 1
+      while (good && take(k, u) && (u.n[0] | u.n[1]) != 0) {
+#pragma unroll
+        for (int X = 0; X < 2; ++X) {
+          if (u.n[X] == 0) continue;
+          if (done[X] > 0 && !(good = wait_or_fail(&B.q_empty[X], (done[X] - 1) & 1, fail))) break;
+          if (lane == 0) {
+            // one token's rows for a decode row: the others of the tile may hold anything
+            const bool single = u.tokens == 1;
+            const CUtensorMap* map = single ? &qmap_1 : &qmap_t;
+            uint8_t* dst = smem + X * kQTile;
+            const int32_t row = u.row + (u.shared ? X * p.tpt : 0);
+            mbar_expect_tx(&B.q_full[X], (single ? p.G : 128) * 256);
+            tma_load_5d(dst, map, &B.q_full[X], 0, 0, row, 0, u.g[X]);
+            tma_load_5d(dst + kQHalf, map, &B.q_full[X], 0, 0, row, 1, u.g[X]);
+          }
+          __syncwarp();
+          ++done[X];
+        }
+      }
+      if (!good || *fail)
+        for (int X = 0; X < 2; ++X)  // let the copies in flight land before the CTA leaves
+          for (int x = 0; x < 1000 && done[X] > 0 && !mbar_try_wait_hint(&B.q_full[X], (done[X] - 1) & 1, 1000); ++x) {
+          }
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp < 14) {
+      // ================================================================ MMA issuers, one per lane
+      // For each step i of the CTA: O(i - 2), S(i). O needs P and V; S(i) needs K(i) and overwrites the
+      // tensor memory from which O(i - 2) reads P, which it may as the tensor pipe runs one thread's MMAs
+      // in issue order. The warp runs in lockstep, an elected lane issues.
+      const int X = warp - 12;
+      const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
+      const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
+      const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
+      const uint64_t qd = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
+      const uint64_t kd0 = umma_desc_sw128(sbase + kOffRing, 16, 1024);
+      const uint64_t vd0 = umma_desc_sw128(sbase + kOffRing, kKvHalf, 1024);
+      constexpr uint32_t kMine = 1, kTwo = 2, kOpens = 4, kAny = 8;  // of a step
+      uint32_t d1 = 0, d2 = 0;
+      Unit u;
+      u.n[0] = u.n[1] = u.shared = 0;
+      int32_t k = 0, j = 0, steps = 0, n_s = 0, n_o = 0, opened = 0, tiles = 0;
+      RingPos r{0, 0};
+      bool good = true, more = true;
+#pragma unroll 1
+      while (more || d1 || d2) {
+        if (d2) {  // O of the step before the last
+          if (d2 & kMine) {
+            const RingPos at = (d2 & kTwo) && X ? r.after(1) : r;
+            const uint32_t buf = n_o & 1;
+            if ((d2 & kOpens) && opened++ > 0 && !(good = wait_or_fail(&B.o_free[X], opened & 1, fail))) break;
+            if (!(good = wait_two_or_fail(&B.kv_full[at.slot], at.phase, &B.p_full[X][buf], (n_o >> 1) & 1, fail)))
+              break;
+            tmem_fence_after();
+            const int32_t us = uniform(at.slot);
+            issue_o(o_tmem, s_tmem + buf * 64, vd0 + us * (kKvTile >> 4), idesc_o, (d2 & kOpens) ? 0 : 1);
+            umma_commit_elect(&B.o_full[X][buf]);
+            umma_commit_elect(&B.kv_empty[us]);
+            ++n_o;
+          }
+          r.advance((d2 & kTwo) ? 2 : 1);
+        }
+        uint32_t d = 0;
+        if (more) {
+          if (j == steps) {
+            if (!(good = take(k, u))) break;
+            j = 0;
+            steps = max(u.n[0], u.n[1]);
+            more = steps > 0;
+          }
+          if (more) {
+            const int32_t mine = X ? u.n[1] : u.n[0], other = X ? u.n[0] : u.n[1];
+            d = kAny | (j < mine ? kMine : 0u) | (!u.shared && j < mine && j < other ? kTwo : 0u) |
+                (j == 0 && mine > 0 ? kOpens : 0u);
+            if (d & kMine) {
+              const RingPos at = (d & kTwo) && X ? r.after(1) : r;
+              const uint32_t buf = n_s & 1;
+              if (j == 0) {
+                if (!(good = wait_or_fail(&B.q_full[X], tiles & 1, fail))) break;
+                ++tiles;
+              }
+              if (!(good = wait_or_fail(&B.kv_full[at.slot], at.phase, fail))) break;
+              tmem_fence_after();
+              const int32_t us = uniform(at.slot);
+              const uint64_t kd = kd0 + us * (kKvTile >> 4);
+              issue_s(s_tmem + buf * 64, qd, kd, idesc_s, 0);
+              issue_s(s_tmem + buf * 64, qd + (kQHalf >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
+              umma_commit_elect(&B.s_full[X][buf]);
+              umma_commit_elect(&B.kv_empty[us]);
+              if (j == mine - 1) umma_commit_elect(&B.q_empty[X]);
+              ++n_s;
+            }
+            r.advance((d & kTwo) ? 2 : 1);
+            ++j;
+          }
+        }
+        d2 = d1;
+        d1 = d;
+      }
+      if (!good) {  // the MMAs in flight end before tensor memory is given back
+        umma_commit_elect(&B.drained[X]);
+        mbar_wait(&B.drained[X], 0);
+      }
+    } else {
+      // ================================================================ late rows of V, a channel half each
+      const int h = warp - 14;
+#pragma unroll 1
+      for (int32_t k = 0;; ++k) {
+        const int q = k & (kLate - 1);
+        if (!wait_or_fail(&B.late_full[q], (k / kLate) & 1, fail)) break;
+        const Late e = B.late[q];
+        if (e.slot < 0) break;  // no more
+        const uint32_t at = sbase + kOffRing + e.slot * kKvTile + h * kKvHalf + (lane & 7) * 16;
+        bool odd = false;
+#pragma unroll 1
+        for (int32_t x0 = e.y & ~3; x0 < kStep; x0 += 16) {  // lanes 8 i .. 8 i + 7: one row
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int32_t x = x0 + 4 * i + (lane >> 3);
+            if (x < kStep) v[i] = ld_shared_v4(at + x * 128);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int32_t x = x0 + 4 * i + (lane >> 3);
+            if (x < e.y || x >= kStep) continue;
+            if (x >= e.z) {
+              st_shared_v4(at + x * 128, make_uint4(0, 0, 0, 0));
+              continue;
+            }
+            const uint4 f = make_uint4(finite_bf16x2(v[i].x), finite_bf16x2(v[i].y), finite_bf16x2(v[i].z),
+                                       finite_bf16x2(v[i].w));
+            if (f.x != v[i].x || f.y != v[i].y || f.z != v[i].z || f.w != v[i].w) {
+              odd = true;
+              st_shared_v4(at + x * 128, f);
+            }
+          }
+        }
+        odd = __any_sync(0xffffffffu, odd);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it by that proxy
+        __syncwarp();
+        if (lane == 0) {
+          if (odd && (e.lanes & 1)) *(volatile int32_t*)&B.odd[0] = 1;
+          if (odd && (e.lanes & 2)) *(volatile int32_t*)&B.odd[1] = 1;
+          mbar_arrive(&B.kv_full[e.slot]);
+        }
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ================================================================ softmax, outputs and partials
+    const int X = (warp - 4) >> 2;
+    const int row = (tid - 128) & 127;  // tile row = tensor memory lane
+    const uint32_t lane_addr = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_tmem = tmem + lane_addr + X * 128;
+    const uint32_t o_tmem = tmem + lane_addr + 256 + X * 128;
+    const int32_t token = row >> p.gs;
+    int32_t n = 0, k = 0;
+    Unit u;
+    bool good = true;
+#pragma unroll 1
+    while (good && take(k, u) && (u.n[0] | u.n[1]) != 0) {
+      const int32_t steps = X ? u.n[1] : u.n[0];
+      if (steps == 0) continue;
+      const int32_t tile = u.shared ? X * p.tpt : 0;  // its first token within the unit's
+      const int32_t rows = min(p.tpt, u.tokens - tile) << p.gs;
+      const int32_t first_vis = u.pos + tile + 1;     // keys that the tile's first row sees
+      const int32_t key0 = X ? u.key0[1] : u.key0[0], g = X ? u.g[1] : u.g[0], part = X ? u.part[1] : u.part[0];
+      const bool act = 32 * (warp & 3) < rows;  // a warp of padding rows only keeps the barriers
+      const bool mine = row < rows;  // the rows behind hold whatever the query area held before
+      float m_run = -INFINITY, m_nat = 0.f, l = 0.f;  // running reference (log2 units; natural) and sum
+      int32_t kb = key0;
+#pragma unroll 1
+      for (int32_t j = 0; j < steps; ++j, ++n, kb += kStep) {
+        if (!(good = wait_or_fail(&B.s_full[X][n & 1], (n >> 1) & 1, fail))) break;
+        tmem_fence_after();
+        const uint32_t sb = s_tmem + (n & 1) * 64;
+        if (act) {
+          float l4[4];
+          uint32_t pk[32];
+          // Any reference near the row's maximum serves for m: P and its sums keep their relative
+          // precision as long as nothing overflows. So P is taken against the reference there is, and
+          // its sum, needed anyway, tells whether a score lies far above it; only then, and on a
+          // unit's first step, a second pass takes the maximum.
+#pragma unroll 1
+          for (bool exact = j == 0;; exact = true) {
+            float v[kStep];
+            tmem_ld32(sb, v);
+            tmem_ld32(sb + 32, v + 32);
+            tmem_wait_ld();
+            if (first_vis - kb < kStep) {  // uniform: the step holds a key some row does not see
+              const int32_t vis = first_vis + token - kb;
+#pragma unroll
+              for (int x = 0; x < kStep; ++x)
+                if (x >= vis) v[x] = -INFINITY;
+            }
+            if (exact) {
+              float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+              for (int x = 4; x < kStep; x += 2) m4[(x >> 1) & 3] = max3(m4[(x >> 1) & 3], v[x], v[x + 1]);
+              const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]), m2 = mx * kLog2e;
+              float factor = 1.f;
+              if (m_run == -INFINITY) {
+                m_run = m2;  // nothing in O yet
+                m_nat = mx;
+              } else if (mine && m2 > m_run) {
+                factor = ex2(m_run - m2);
+                m_run = m2;
+                m_nat = mx;
+                l *= factor;
+              }
+              if (__any_sync(0xffffffffu, factor != 1.f)) {
+                // rescale O once O(n-1) has completed (S(n) says that O(n-2) has, so the barrier's
+                // parity is unambiguous)
+                if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
+                tmem_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(o_tmem + c * 16, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * factor);
+                  tmem_st16(o_tmem + c * 16, o);
+                }
+              }
+            }
+            float off = m_run == -INFINITY ? 0.f : -m_run;
+            if (__any_sync(0xffffffffu, mine && fabsf(off) > kFarRef)) {
+              off = 0.f;
+              if (m_run != -INFINITY)
+#pragma unroll
+                for (int x = 0; x < kStep; ++x) v[x] -= m_nat;
+            }
+            l4[0] = l4[1] = l4[2] = l4[3] = 0.f;
+#pragma unroll
+            for (int x = 0; x < kStep; x += 2) {
+              fma2(v[x], v[x + 1], v[x], v[x + 1], kLog2e, kLog2e, off, off);
+              v[x] = ex2(v[x]);
+              v[x + 1] = ex2(v[x + 1]);
+              add2(l4[x & 2], l4[(x & 2) + 1], v[x], v[x + 1]);
+              pk[x >> 1] = pack_bf16x2(v[x], v[x + 1]);
+            }
+            l4[0] = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            if (exact || !__any_sync(0xffffffffu, mine && (l4[0] > kFarSum || m_run == -INFINITY))) break;
+          }
+          if (!good) break;
+          l += l4[0];
+          tmem_st32(sb, pk);
+          tmem_wait_st();
+        }
+        tmem_fence_before();
+        __syncwarp();
+        mbar_arrive_if(&B.p_full[X][n & 1], lane == 0);
+      }
+      if (!good) break;
+      // ---------------- the output, or the run's partial
+      const int64_t out = ((int64_t)(u.row + tile + token)) * p.Hq + (g << p.gs) + (row & (p.G - 1));
+      const int32_t cap = u.shared ? 128 : ((u.tokens << p.gs) + 7) / 8 * 8;
+      float scale = 1.f;
+      if (part < 0) {
+        scale = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: o = 0, lse = -inf
+        if (mine && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
+      } else if (mine) {
+        p.ml[part + row] = make_float2(m_run, l);
+      }
+      if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
+      tmem_fence_after();
+      const bool odd = *(volatile int32_t*)&B.odd[X] != 0;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float o[64];
+        if (act) {
+          tmem_ld32(o_tmem + c * 64, o);
+          tmem_ld32(o_tmem + c * 64 + 32, o + 32);
+          tmem_wait_ld();
+        }
+        if (c == 1) {  // all of O is read: the next unit may overwrite it
+          tmem_fence_before();
+          __syncwarp();
+          mbar_arrive_if(&B.o_free[X], lane == 0);
+        }
+        if (!mine) continue;
+        if (odd) {
+          // rare: what is not finite in V of the late keys that the row sees (their weights are above 0, so
+          // it is added as it is)
+          const int32_t end = min(first_vis + token, key0 + steps * kStep);
+#pragma unroll 1
+          for (int32_t key = max(key0, u.pos + 1); key < end; ++key) {
+            int32_t page = p.page_table[(int64_t)u.b * p.max_blocks + key / MSA_BLOCK_TOKENS];
+            if (page < 0 || page >= p.num_pages) page = 0;
+            const int64_t cell = (int64_t)page * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+            const uint2* v = reinterpret_cast<const uint2*>(p.v_cache + (cell * p.Hkv + g) * 128 + c * 64);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const uint2 w = v[x], f = make_uint2(finite_bf16x2(w.x), finite_bf16x2(w.y));
+              if (f.x != w.x || f.y != w.y) {
+                o[4 * x] += bf16_lo(w.x ^ f.x);
+                o[4 * x + 1] += bf16_hi(w.x ^ f.x);
+                o[4 * x + 2] += bf16_lo(w.y ^ f.y);
+                o[4 * x + 3] += bf16_hi(w.y ^ f.y);
+              }
+            }
+          }
+        }
+        if (part < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + out * 128 + c * 64);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            dst[x] = make_uint4(pack_bf16x2(o[8 * x] * scale, o[8 * x + 1] * scale),
+                                pack_bf16x2(o[8 * x + 2] * scale, o[8 * x + 3] * scale),
+                                pack_bf16x2(o[8 * x + 4] * scale, o[8 * x + 5] * scale),
+                                pack_bf16x2(o[8 * x + 6] * scale, o[8 * x + 7] * scale));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.po + (int64_t)part * 128) + (int64_t)c * 16 * cap + row;
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            dst[(int64_t)x * cap] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+      }
+    }
+  }
+  // ------------------------------------------------------------------ teardown
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------------------ join
+// A CTA joins eight rows of a tile at a time; a thread owns four channels of one row, so a warp reads
+// whole 128-byte lines of the partials' [channel quad][row][4] layout. A row's pieces are dealt to
+// kSplit threads, four loads in flight each, and joined through shared memory.
+constexpr int kJoinRows = 8;
+constexpr int kJoinSplit = 4;
+constexpr int kJoinThreads = kJoinRows * 32 * kJoinSplit;
+
+struct Joined {
+  float m, l;
+  float4 acc;
+};
+// Adds up to four parts (n of them valid) to j.
+__device__ __forceinline__ void join_four(Joined& j, const float2 (&ml)[4], const float4 (&o)[4], int n) {
+  float m = j.m;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < n) m = fmaxf(m, ml[u].x);
+  const float f = j.m == m ? 1.f : ex2(j.m - m);  // 2^(-inf) = 0 for the first parts
+  j.m = m;
+  j.l *= f;
+  j.acc.x *= f;
+  j.acc.y *= f;
+  j.acc.z *= f;
+  j.acc.w *= f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u >= n || (ml[u].x == -INFINITY && ml[u].y == 0.f)) continue;  // the row saw no key there
+    const float w = ex2(ml[u].x - m);
+    j.l += w * ml[u].y;
+    j.acc.x += w * o[u].x;
+    j.acc.y += w * o[u].y;
+    j.acc.z += w * o[u].z;
+    j.acc.w += w * o[u].w;
+  }
+}
+
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KParams p) {
+  __shared__ float2 s_ml[kJoinSplit][kJoinRows * 32];
+  __shared__ float4 s_o[kJoinSplit][kJoinRows * 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = threadIdx.x % (kJoinRows * 32), split = threadIdx.x / (kJoinRows * 32);
+  const int32_t quad = t / kJoinRows;
+  const int32_t tasks = p.head->joins * (128 / kJoinRows);
+#pragma unroll 1
+  for (int32_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const JoinTile e = p.joins[task / (128 / kJoinRows)];
+    const int32_t r0 = task % (128 / kJoinRows) * kJoinRows;
+    if (r0 >= e.rows) continue;  // uniform
+    const int32_t r = r0 + (t & (kJoinRows - 1));
+    const bool valid = r < e.rows;
+    Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (valid) {
+      const float2* mls = p.ml + e.part + r;
+      const float4* os = reinterpret_cast<const float4*>(p.po + (int64_t)e.part * 128) + (int64_t)quad * e.cap + r;
+      for (int32_t k = split; k < e.pieces; k += 4 * kJoinSplit) {
+        float2 ml[4];
+        float4 o[4];
+        int have = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int64_t x = k + u * kJoinSplit;
+          if (x < e.pieces) {
+            ml[u] = __ldcs(mls + x * e.step);
+            o[u] = __ldcs(os + x * e.step * 32);
+            ++have;
+          }
+        }
+        join_four(j, ml, o, have);
+      }
+    }
+    s_ml[split][t] = make_float2(j.m, j.l);
+    s_o[split][t] = j.acc;
+    __syncthreads();
+    if (split == 0) {
+      float2 ml[4];
+      float4 o[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = u + 1 < kJoinSplit ? u + 1 : 0;
+        ml[u] = s_ml[x][t];
+        o[u] = s_o[x][t];
+      }
+      join_four(j, ml, o, kJoinSplit - 1);
+      if (valid) {
+        const float inv = j.l == 0.f ? 0.f : 1.0f / j.l;  // a row that sees no key: o = 0, lse = -inf
+        const int64_t out = (int64_t)(e.row + (r >> p.gs)) * p.Hq + (e.g << p.gs) + (r & (p.G - 1));
+        *reinterpret_cast<uint2*>(p.o + out * 128 + quad * 4) =
+            make_uint2(pack_bf16x2(j.acc.x * inv, j.acc.y * inv), pack_bf16x2(j.acc.z * inv, j.acc.w * inv));
+        if (quad == 0 && p.lse) p.lse[out] = j.l == 0.f ? -INFINITY : (j.m + log2f(j.l)) * kLn2;
+      }
+    }
+    __syncthreads();  // the shared parts are read
+  }
+}
+
+// ------------------------------------------------------------------------------ host
+struct Layout {
+  int32_t cap_units, cap_joins;
+  int64_t cap_rows;
+  size_t units, joins, ml, po, total;
+};
+
+Layout layout_of(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks, int ctas) {
+  Layout y{};
+  const int64_t G = Hq / Hkv, tpt = 128 / G, requests = B < T ? B : T;
+  // pairs of tiles and single tiles
+  const int64_t items = Hkv * (T / (2 * tpt) + requests);
+  // Pieces of the items that are cut: an item of c steps with r still to come, itself included, has
+  // ceil(c / max(8, r / 2 ctas)) pieces, at most 2 c / that for more than one. r falls to 0 over the call,
+  // so the sum is at most 2 * 2 ctas * (1 + log(most steps / 8)); with less than 8 steps per CTA pieces
+  // are as short as these, and at most 2 * ctas.
+  const double most = 2.0 * max_blocks / kMinPiece;
+  const int64_t cut = (int64_t)(4.0 * ctas * (1.0 + (most > 1 ? log(most) : 0.0))) + 16;
+  const int64_t rows = (T * G + 7) / 8 * 8;
+  // one KV group: single tiles that are not cut have two runs as well
+  const int64_t halves = Hkv == 1 ? requests : 0;
+  y.cap_units = (int32_t)(items + cut);
+  y.cap_joins = (int32_t)(2 * cut + halves);
+  y.cap_rows = 2 * cut * (rows < 128 ? rows : 128) + (halves ? 2 * (T * G + 8 * halves) : 0);
+  size_t at = align_up(sizeof(Header), 256);
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  y.units = take((size_t)y.cap_units * sizeof(Unit));
+  y.joins = take((size_t)y.cap_joins * sizeof(JoinTile));
+  y.ml = take((size_t)y.cap_rows * sizeof(float2));
+  y.po = take((size_t)y.cap_rows * 128 * sizeof(float));
+  y.total = at;
+  return y;
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks, int ctas) {
+  return layout_of(B, T, Hq, Hkv, max_blocks, ctas).total;
+}
+
+cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
+  const int ctas = sm_count();
+  const Layout y = layout_of(a.B, a.T, a.Hq, a.Hkv, a.max_blocks, ctas);
+  const int32_t G = a.Hq / a.Hkv;
+  KParams p{};
+  p.page_table = a.page_table;
+  p.seq_lens = a.seq_lens;
+  p.cu_tokens = a.cu_tokens;
+  p.B = a.B;
+  p.T = a.T;
+  p.G = G;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.max_blocks = a.max_blocks;
+  p.num_pages = a.num_pages;
+  while ((1 << p.gs) < G) ++p.gs;
+  p.tpt = 128 / G;
+  p.ctas = ctas;
+  p.cap_units = y.cap_units;
+  p.cap_joins = y.cap_joins;
+  p.cap_rows = y.cap_rows;
+  uint8_t* w = a.workspace;
+  p.head = reinterpret_cast<Header*>(w);
+  p.units = reinterpret_cast<Unit*>(w + y.units);
+  p.joins = reinterpret_cast<JoinTile*>(w + y.joins);
+  p.ml = reinterpret_cast<float2*>(w + y.ml);
+  p.po = reinterpret_cast<float*>(w + y.po);
+  p.v_cache = a.v_cache;
+  p.o = a.o;
+  p.lse = a.lse;
+  // query rows as (channel half, head of the group, token row, half, group): a box is G heads of
+  // consecutive token rows, one 128-byte line each
+  CUtensorMap qt, q1, km, vm;
+  const uint64_t qd[5] = {64, (uint64_t)G, (uint64_t)a.T, 2, (uint64_t)a.Hkv};
+  const uint64_t qs[4] = {256, (uint64_t)a.q_stride * 2, 128, (uint64_t)G * 256};
+  const uint32_t bt[5] = {64, (uint32_t)G, (uint32_t)p.tpt, 1, 1};
+  const uint32_t b1[5] = {64, (uint32_t)G, 1, 1, 1};
+  // cache cells as (channel half, token, half, group): a box is both halves of 64 tokens
+  const uint64_t kd[4] = {64, (uint64_t)a.num_pages * 128, 2, (uint64_t)a.Hkv};
+  const uint64_t ks[3] = {(uint64_t)a.Hkv * 256, 128, 256};
+  const uint32_t bk[4] = {64, kStep, 2, 1};
+  if (!encode_bf16_map(&qt, a.q, 5, qd, qs, bt, true) || !encode_bf16_map(&q1, a.q, 5, qd, qs, b1, true) ||
+      !encode_bf16_map(&km, a.k_cache, 4, kd, ks, bk, true) || !encode_bf16_map(&vm, a.v_cache, 4, kd, ks, bk, true))
+    return cudaErrorInvalidValue;
+  static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, chunk_attention_kernel);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const size_t plan_smem = (size_t)(a.B + 1) * sizeof(int32_t);
+  static std::atomic<size_t> raised_plan[kMaxDevices], raised[kMaxDevices];
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = plan_smem;
+  cudaError_t e = launch_with_smem(chunk_plan_kernel, (kMaxRequests + 1) * sizeof(int32_t), raised_plan,
+                                   [&] { return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p); });
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  e = launch_with_smem(chunk_attention_kernel, kSmemBytes, raised,
+                       [&] { return cudaLaunchKernelEx(&cfg, chunk_attention_kernel, qt, q1, km, vm, p); });
+  if (e != cudaSuccess) return e;
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, chunk_join_kernel, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+}  // namespace msa

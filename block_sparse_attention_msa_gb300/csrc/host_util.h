@@ -51,6 +51,17 @@ inline bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const 
   return r == CUDA_SUCCESS;
 }
 
+// Map of `rows` rows of 128 bytes, box of `box_rows` of them, 128-byte swizzle.
+inline bool encode_u8_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t gdim[2] = {128, rows}, gstr[1] = {128};
+  const cuuint32_t bdim[2] = {128, box_rows}, estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gdim, gstr, bdim, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;

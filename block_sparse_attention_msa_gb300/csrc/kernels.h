@@ -272,6 +272,61 @@ struct SharedPrefixArgs {
 size_t shared_prefix_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int ctas);
 cudaError_t launch_shared_prefix_decode(const SharedPrefixArgs& a, cudaStream_t stream);
 
+// ------------------------------------------------------------------ quantised cache
+// Caches [num_pages, Hkv, 128, 128] e4m3, scales [num_pages, Hkv, 128] (exponent + 127).
+struct AppendFp8Args {
+  const uint16_t *k, *v;        // [T, Hkv, 128]
+  int64_t k_stride, v_stride;   // elements between token rows
+  const int32_t* slot_map;      // [T]
+  int32_t T, Hkv;
+  int64_t num_pages;
+  uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
+};
+cudaError_t launch_append_kv_fp8(const AppendFp8Args& a, cudaStream_t stream);
+
+struct GatherFp8Args {
+  const uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
+  int64_t num_pages;
+  const int32_t* slots;         // [T]
+  int32_t T, Hkv;
+  uint16_t *k, *v;              // [T, Hkv, 128]
+};
+cudaError_t launch_gather_kv_fp8(const GatherFp8Args& a, cudaStream_t stream);
+
+struct DecodeFp8Args {
+  const uint16_t* q;            // [R, Hq, 128]
+  const uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
+  const int32_t* fpt;           // [R*Hkv, topk]
+  const int32_t* lens;          // [R*Hkv]
+  int32_t R, Hq, Hkv, topk;
+  int64_t num_pages;
+  uint16_t* o;                  // [R, Hq, 128]
+  float* lse;                   // [R, Hq] or null
+  float* part_o;                // workspace [R*Hkv, topk, G, 128]
+  float* part_lse;              // workspace [R*Hkv, topk, G]
+};
+cudaError_t launch_paged_decode_fp8(const DecodeFp8Args& a, cudaStream_t stream);
+
+// ------------------------------------------------------------------ chunk attention
+struct ChunkArgs {
+  const uint16_t* q;            // [T, Hq, 128]
+  int64_t q_stride;             // elements between token rows
+  const uint16_t* k_cache;      // [num_pages, 128, Hkv, 128]
+  const uint16_t* v_cache;
+  const int32_t* page_table;    // [B, max_blocks]
+  const int32_t* seq_lens;      // [B]
+  const int32_t* cu_tokens;     // [B + 1]
+  int32_t B, T, Hq, Hkv, max_blocks;
+  int64_t num_pages;
+  uint16_t* o;                  // [T, Hq, 128]
+  float* lse;                   // [T, Hq] or null
+  uint8_t* workspace;
+};
+// Work items (a pair of query tiles, or a tile, of one KV group) are counted in shared memory.
+constexpr int64_t kMaxChunkItems = 1 << 20;
+size_t chunk_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks, int ctas);
+cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device errors
 cudaError_t read_device_errors(uint32_t* word);
 

@@ -22,6 +22,9 @@ cudaError_t msa_read_error_stage(uint32_t* w);
 cudaError_t msa_read_error_tables(uint32_t* w);
 cudaError_t msa_read_error_append(uint32_t* w);
 cudaError_t msa_read_error_spd(uint32_t* w);
+cudaError_t msa_read_error_kvq(uint32_t* w);
+cudaError_t msa_read_error_dec8(uint32_t* w);
+cudaError_t msa_read_error_chunk(uint32_t* w);
 
 namespace {
 
@@ -444,6 +447,183 @@ int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache, const u
   return cuda_status(msa::launch_shared_prefix_decode(a, as_stream(stream)), name);
 }
 
+// ------------------------------------------------------------------------------ quantised cache
+static int check_fp8_caches(const char* name, const uint8_t* k_cache, const uint8_t* v_cache,
+                            const uint8_t* k_scale, const uint8_t* v_scale, int32_t Hkv, int32_t D,
+                            int64_t num_pages) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale) return fail(MSA_ERR_ARG, "%s: null tensor pointer", name);
+  if (num_pages <= 0) return fail(MSA_ERR_ARG, "%s: num_pages=%lld", name, (long long)num_pages);
+  if (D != 128) return fail(MSA_ERR_UNSUPPORTED, "%s: D=%d (only 128)", name, D);
+  if (!pow2_upto(Hkv, 16)) return fail(MSA_ERR_UNSUPPORTED, "%s: Hkv=%d", name, Hkv);
+  if (num_pages > kInt32Max || num_pages * 128 * Hkv > kInt32Max)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: num_pages*128*Hkv exceeds int32", name);
+  const void* ptrs[] = {k_cache, v_cache, k_scale, v_scale};
+  for (auto x : ptrs)
+    if (reinterpret_cast<uintptr_t>(x) & 15)
+      return fail(MSA_ERR_ARG, "%s: tensors must be 16-byte aligned", name);
+  return MSA_OK;
+}
+
+int msa_append_kv_fp8(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                      const int32_t* slot_map, int32_t T, int32_t Hkv, int32_t D, int64_t num_pages,
+                      uint8_t* k_cache, uint8_t* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                      void* stream) {
+  const char* name = "msa_append_kv_fp8";
+  if (T == 0) return ok();
+  if (T < 0) return fail(MSA_ERR_ARG, "%s: T=%d", name, T);
+  if (!k || !v || !slot_map) return fail(MSA_ERR_ARG, "%s: null tensor pointer", name);
+  const int rc = check_fp8_caches(name, k_cache, v_cache, k_scale, v_scale, Hkv, D, num_pages);
+  if (rc != MSA_OK) return rc;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
+    return fail(MSA_ERR_ARG, "%s: tensors must be 16-byte aligned", name);
+  if ((k_stride | v_stride) < 0 || ((k_stride | v_stride) & 7))
+    return fail(MSA_ERR_ARG, "%s: row strides must be non-negative multiples of 8 elements", name);
+  msa::AppendFp8Args a{};
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.slot_map = slot_map;
+  a.T = T;
+  a.Hkv = Hkv;
+  a.num_pages = num_pages;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return cuda_status(msa::launch_append_kv_fp8(a, as_stream(stream)), name);
+}
+
+int msa_gather_kv_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const uint8_t* k_scale,
+                      const uint8_t* v_scale, int64_t num_pages, const int32_t* slots, int32_t T,
+                      int32_t Hkv, int32_t D, uint16_t* k, uint16_t* v, void* stream) {
+  const char* name = "msa_gather_kv_fp8";
+  if (T == 0) return ok();
+  if (T < 0) return fail(MSA_ERR_ARG, "%s: T=%d", name, T);
+  if (!k || !v || !slots) return fail(MSA_ERR_ARG, "%s: null tensor pointer", name);
+  const int rc = check_fp8_caches(name, k_cache, v_cache, k_scale, v_scale, Hkv, D, num_pages);
+  if (rc != MSA_OK) return rc;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
+    return fail(MSA_ERR_ARG, "%s: tensors must be 16-byte aligned", name);
+  msa::GatherFp8Args a{};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.num_pages = num_pages;
+  a.slots = slots;
+  a.T = T;
+  a.Hkv = Hkv;
+  a.k = k;
+  a.v = v;
+  return cuda_status(msa::launch_gather_kv_fp8(a, as_stream(stream)), name);
+}
+
+int msa_paged_sparse_decode_fp8(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                const uint8_t* k_scale, const uint8_t* v_scale,
+                                const int32_t* flat_page_table, const int32_t* flat_kv_lens, int32_t R,
+                                int32_t Hq, int32_t Hkv, int32_t D, int32_t topk, int64_t num_pages,
+                                uint16_t* o, float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  const char* name = "msa_paged_sparse_decode_fp8";
+  if (R == 0) return ok();
+  if (!q || !flat_page_table || !flat_kv_lens || !o) return fail(MSA_ERR_ARG, "%s: null tensor pointer", name);
+  if (R < 0 || topk < 1 || topk > 64) return fail(MSA_ERR_ARG, "%s: R=%d topk=%d", name, R, topk);
+  const int rc = check_fp8_caches(name, k_cache, v_cache, k_scale, v_scale, Hkv, D, num_pages);
+  if (rc != MSA_OK) return rc;
+  if (Hq <= 0 || Hq % Hkv != 0 || !pow2_upto(Hq / Hkv, 16))
+    return fail(MSA_ERR_UNSUPPORTED, "%s: Hq=%d Hkv=%d", name, Hq, Hkv);
+  if ((int64_t)R * Hq * topk > kInt32Max)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: R*Hq*topk exceeds int32", name);
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o)) & 15)
+    return fail(MSA_ERR_ARG, "%s: tensors must be 16-byte aligned", name);
+  const size_t need = msa_paged_sparse_decode_workspace_size(R, Hq, Hkv, topk);
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return fail(MSA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", name,
+                workspace, workspace_bytes, need);
+  msa::DecodeFp8Args a{};
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.fpt = flat_page_table;
+  a.lens = flat_kv_lens;
+  a.R = R;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.topk = topk;
+  a.num_pages = num_pages;
+  a.o = o;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(
+      static_cast<uint8_t*>(workspace) + msa::ws_align((size_t)R * Hq * topk * 128 * sizeof(float)));
+  return cuda_status(msa::launch_paged_decode_fp8(a, as_stream(stream)), name);
+}
+
+// ------------------------------------------------------------------------------ chunk attention
+// Work items of a call: pairs of query tiles and single tiles, per KV group.
+static int64_t chunk_items(int32_t B, int32_t T, int32_t Hq, int32_t Hkv) {
+  return (int64_t)Hkv * (T / (2 * (128 / (Hq / Hkv))) + (B < T ? B : T));
+}
+
+size_t msa_chunk_attention_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks) {
+  if (B <= 0 || B > msa::kMaxRequests || T <= 0 || max_blocks <= 0 || (int64_t)max_blocks * 128 > kInt32Max - 128 ||
+      !pow2_upto(Hkv, 16) || Hq <= 0 || Hq % Hkv || !pow2_upto(Hq / Hkv, 16) || (int64_t)T * Hq > kInt32Max ||
+      chunk_items(B, T, Hq, Hkv) > msa::kMaxChunkItems)
+    return 0;
+  return msa::chunk_workspace_bytes(B, T, Hq, Hkv, max_blocks, msa::sm_count());
+}
+
+int msa_chunk_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache, const uint16_t* v_cache,
+                        const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_tokens, int32_t B,
+                        int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_blocks, int64_t num_pages,
+                        uint16_t* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* name = "msa_chunk_attention";
+  if (B == 0 || T == 0) return ok();
+  if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !cu_tokens || !o)
+    return fail(MSA_ERR_ARG, "%s: null tensor pointer", name);
+  if (B < 0 || T < 0 || max_blocks < 1 || num_pages <= 0)
+    return fail(MSA_ERR_ARG, "%s: B=%d T=%d max_blocks=%d num_pages=%lld", name, B, T, max_blocks,
+                (long long)num_pages);
+  if (D != 128) return fail(MSA_ERR_UNSUPPORTED, "%s: D=%d (only 128)", name, D);
+  if (!pow2_upto(Hkv, 16) || Hq <= 0 || Hq % Hkv != 0 || !pow2_upto(Hq / Hkv, 16))
+    return fail(MSA_ERR_UNSUPPORTED, "%s: Hq=%d Hkv=%d", name, Hq, Hkv);
+  if (num_pages > kInt32Max || num_pages * 128 > kInt32Max || (int64_t)max_blocks * 128 > kInt32Max - 128)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: num_pages*128 or max_blocks*128 exceeds int32", name);
+  if (B > msa::kMaxRequests) return fail(MSA_ERR_UNSUPPORTED, "%s: B=%d (at most %d)", name, B, msa::kMaxRequests);
+  if ((int64_t)T * Hq > kInt32Max || chunk_items(B, T, Hq, Hkv) > msa::kMaxChunkItems)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: B=%d T=%d Hq=%d Hkv=%d: too many query tiles", name, B, T, Hq, Hkv);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) |
+                         reinterpret_cast<uintptr_t>(v_cache) | reinterpret_cast<uintptr_t>(o);
+  if (bits & 15) return fail(MSA_ERR_ARG, "%s: tensors must be 16-byte aligned", name);
+  if ((T > 1 && q_stride < (int64_t)Hq * 128) || q_stride < 0 || (q_stride & 7) || q_stride > ((int64_t)1 << 38))
+    return fail(MSA_ERR_ARG, "%s: q's row stride must be a multiple of 8 elements, Hq*D at least", name);
+  const size_t need = msa_chunk_attention_workspace_size(B, T, Hq, Hkv, max_blocks);
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return fail(MSA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", name,
+                workspace, workspace_bytes, need);
+  msa::ChunkArgs a{};
+  a.q = q;
+  a.q_stride = T > 1 ? q_stride : (int64_t)Hq * 128;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.cu_tokens = cu_tokens;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.max_blocks = max_blocks;
+  a.num_pages = num_pages;
+  a.o = o;
+  a.lse = lse;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  return cuda_status(msa::launch_chunk_attention(a, as_stream(stream)), name);
+}
+
 // ------------------------------------------------------------------------------ prefill
 size_t msa_sparse_prefill_workspace_size(int32_t T, int64_t S_kv, int32_t Hq, int32_t Hkv,
                                          int32_t topk) {
@@ -636,7 +816,8 @@ int msa_device_error(uint32_t* word) {
                                          msa_read_error_dec, msa_read_error_pre,
                                          msa_read_error_dense, msa_read_error_stage,
                                          msa_read_error_tables, msa_read_error_append,
-                                         msa_read_error_spd};
+                                         msa_read_error_spd, msa_read_error_kvq,
+                                         msa_read_error_dec8, msa_read_error_chunk};
   for (auto rd : readers) {
     w = 0;
     e = rd(&w);

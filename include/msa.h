@@ -473,6 +473,90 @@ MSA_API int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache,
                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * Serving batch -- causal attention of a ragged batch of new tokens over the paged cache: prompts,
+ * chunks of prompts behind a cached prefix and decode rows, mixed as a scheduler packs them.
+ *
+ * Request b's new tokens are the token rows cu_tokens[b] .. cu_tokens[b+1] - 1 (n_b of them, 0 or
+ * more), at its last positions: row t at pos = seq_lens[b] - n_b + t - cu_tokens[b]. Their keys and
+ * values are in the cache already (msa_build_page_tables and msa_append_kv make these arguments). For
+ * head h of group g:
+ *   s_n = q[t,h,:] . k_cache[page_table[b, n/128], n%128, g, :],  n = 0..pos;
+ *   o[t,h,:] = softmax(s) . V;  lse[t,h] = log sum_n exp(s_n).
+ * A row at a negative position (seq_lens[b] < n_b) sees no key: o = 0, lse = -inf. Rows before
+ * cu_tokens[0] and from cu_tokens[B] on (the padding of a captured step) are left as they were. Cells
+ * that a row does not see may hold anything, NaN and infinities included.
+ *
+ *   q [T, Hq, D] bf16 (pre-scaled), rows of Hq*D dense elements, q_stride elements apart (a multiple
+ *   of 8; a slice of a fused projection needs no copy)
+ *   k_cache, v_cache [num_pages, 128, Hkv, D] bf16; page_table [B, max_blocks] int32
+ *   seq_lens [B], cu_tokens [B+1] int32
+ *   o [T, Hq, D] bf16, lse [T, Hq] fp32 or NULL (out; neither may overlap an input)
+ *   workspace >= msa_chunk_attention_workspace_size(B, T, Hq, Hkv, max_blocks) bytes, 256-byte
+ *   aligned, any contents (its size goes with the current device's SM count). Calls that may run
+ *   concurrently need separate workspaces. It holds the list of work and the fp32 partials of the most
+ *   pieces that any lengths lead to, about 130 KB for each of 600 * (1 + log(max_blocks / 4)) pieces
+ *   (less where T * G < 128): with 152 SMs 13 MB for one row of G 8 and 128 blocks, 0.46 GB for 2048
+ *   rows and 485 blocks, 0.56 GB for 1024.
+ * B <= 16384, T*Hq in int32. Lengths and tables are read on the device: a captured call can be
+ * replayed with other values in the same buffers. cu_tokens out of order or outside [0, T], lengths
+ * below n_b or above max_blocks*128 are clamped and set bit 1 of the device error word, a page id
+ * out of range is read as page 0 and sets bit 0. The result depends only on the inputs and the
+ * device's SM count (no run-to-run variation). Sums and lse are fp32; the softmax weights are rounded to
+ * bf16 for their product with V, as in the library's other attention calls.
+ * ------------------------------------------------------------------------------------ */
+MSA_API size_t msa_chunk_attention_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv,
+                                                  int32_t max_blocks);
+
+MSA_API int msa_chunk_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                const uint16_t* v_cache, const int32_t* page_table,
+                                const int32_t* seq_lens, const int32_t* cu_tokens, int32_t B, int32_t T,
+                                int32_t Hq, int32_t Hkv, int32_t D, int32_t max_blocks,
+                                int64_t num_pages, uint16_t* o, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Quantised K/V cache -- rows quantised as they are written, read back, and sparse decode on them.
+ *
+ * A row is one token of one KV group. Its 128 channels are e4m3 numbers (no infinity; 448 the
+ * largest) with one power of two: k_cache, v_cache [num_pages, Hkv, 128, D] e4m3 bytes (a page of a
+ * group is 16 KB in one piece) and k_scale, v_scale [num_pages, Hkv, 128] bytes e + 127. The value of a
+ * channel is number * 2^e. Slots (page*128 + offset) and virtual pages (page*128*Hkv + group) are those
+ * of the bf16 caches, so one set of tables serves both.
+ *
+ * msa_append_kv_fp8: for every token row t with slot_map[t] >= 0 and every group, e is the smallest
+ *   integer in [-127, 119] for which every finite |x| <= 448 * 2^e (119: rows beyond are held at
+ *   448 * 2^119), and x is stored as the e4m3 number nearest to x * 2^-e, ties to even; what is not
+ *   finite is stored as NaN. Every other cell is left as it was. k, v [T, Hkv, D] bf16 with row strides
+ *   in elements as in msa_append_kv; non-negative slots must differ.
+ * msa_gather_kv_fp8: k[t], v[t] = the values of cell slots[t], exact in bf16 (rounded once where they
+ *   leave its range). Rows with a negative slot are left as they were; a slot may stand for several
+ *   rows. With the slots of a request's tokens in order this is its contiguous K and V
+ *   (msa_sparse_prefill), or, T a multiple of 128, pages of a bf16 cache (msa_chunk_attention).
+ * msa_paged_sparse_decode_fp8: msa_paged_sparse_decode on the values of the quantised cache, with the
+ *   same tables and the same workspace size. e4m3 numbers are multiplied as they are; q and the softmax
+ *   weights are rounded to fp16 for it (q after a power of two for its head, so at 2^-39 of the
+ *   head's largest magnitude at most; weights at 2^-11 of their value).
+ * Tensors are 16-byte aligned. num_pages*128*Hkv must fit int32. A slot of num_pages*128 or more is
+ * skipped, a virtual page out of range read as page 0, group 0; both set bit 0 of the device error word.
+ * ------------------------------------------------------------------------------------ */
+MSA_API int msa_append_kv_fp8(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                              const int32_t* slot_map, int32_t T, int32_t Hkv, int32_t D,
+                              int64_t num_pages, uint8_t* k_cache, uint8_t* v_cache, uint8_t* k_scale,
+                              uint8_t* v_scale, void* stream);
+
+MSA_API int msa_gather_kv_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const uint8_t* k_scale,
+                              const uint8_t* v_scale, int64_t num_pages, const int32_t* slots, int32_t T,
+                              int32_t Hkv, int32_t D, uint16_t* k, uint16_t* v, void* stream);
+
+MSA_API int msa_paged_sparse_decode_fp8(const uint16_t* q, const uint8_t* k_cache,
+                                        const uint8_t* v_cache, const uint8_t* k_scale,
+                                        const uint8_t* v_scale, const int32_t* flat_page_table,
+                                        const int32_t* flat_kv_lens, int32_t R, int32_t Hq, int32_t Hkv,
+                                        int32_t D, int32_t topk, int64_t num_pages, uint16_t* o,
+                                        float* lse, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Diagnostics.
  * ------------------------------------------------------------------------------------ */
 /* Thread-local message of the last failing call on this host thread ("" if none). */
