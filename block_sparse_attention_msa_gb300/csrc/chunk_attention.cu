@@ -62,28 +62,37 @@ constexpr float kFarSum = 16384.f;  // of a step's P: beyond it the softmax's re
 // factor of P and l. Beyond this magnitude of m it would leave fp32's range, and m is subtracted first.
 constexpr float kFarRef = 16777216.f;
 constexpr int kMinPiece = 8;        // steps of a piece, where the whole call has as many per CTA
+// Of the cut into equal runs: relative time of a step of a shared unit and of lanes with keys of their own
+// (which HBM feeds at the copy rate when all CTAs have such), and what a tile's end and beginning take.
+constexpr int32_t kSharedCost = 4, kOwnCost = 7, kTileCost = 7;
+constexpr int32_t kLeastRun = 2 * kOwnCost;
 
+// What the two lanes of a unit have.
+enum : int32_t {
+  kHeads = 0,   // a tile of a KV group each, on the same keys
+  kShared = 1,  // neighbouring tiles of one group: they share the steps
+  kHalves = 2,  // one tile, of a single KV group: lane 1 takes its later keys and hands lane 0 its part
+};
 // What a CTA does next: for each lane a tile and a run of steps.
 struct __align__(16) Unit {
   int32_t n[2];     // steps; 0: nothing for the lane. Both 0: there are no more units.
   int32_t key0[2];  // first keys
   int32_t g[2];     // groups
-  int32_t part[2];  // first row of the lane's partial, or -1: the run is the whole tile
+  int32_t part;     // first row of the partials, lane 1's tile_rows behind lane 0's; -1: whole tiles
+  int32_t kind;
   int32_t b;        // page-table row
   int32_t row;      // first token row of the (first) tile
   int32_t tokens;   // of the tile, or of both
   int32_t pos;      // position of the first token
   int32_t seq;      // keys that the request holds
-  int32_t shared;   // 1: two tiles on the same steps
-  int32_t pad[2];
+  int32_t pad[3];
 };
-static_assert(sizeof(Unit) == 64, "read by 16 lanes");
+static_assert(sizeof(Unit) == 64, "four 16-byte loads");
 // A tile whose pieces are to be joined.
 struct __align__(16) JoinTile {
   int32_t row, rows, g;  // first token row, valid rows, group
-  int32_t part;          // first row of the first piece's partial
-  int32_t step;          // rows from piece to piece
-  int32_t pieces, cap;   // cap: rows of a partial
+  int32_t first, rest;   // first rows of the first and the second piece's partial; then 2 * tile_rows further each
+  int32_t pieces, cap;   // cap: rows of a partial, a multiple of 8
   int32_t pad;
 };
 struct Header {
@@ -100,12 +109,14 @@ struct KParams {
   int32_t tpt;        // tokens per tile: 128 / G
   int32_t ctas;
   int32_t cap_units, cap_joins;
-  int64_t cap_rows;
+  int32_t cap_pieces;  // of 2 * tile_rows rows
+  int32_t tile_rows;   // rows of a tile's partial: 128, or as many as all new tokens fill
   Header* head;
   Unit* units;
   JoinTile* joins;
   float* po;          // partials: O as [32 channel quads][cap rows][4] fp32 from row * 128 on
   float2* ml;         // (m, l) per row
+  float* half_po;     // kHalves: lane 1's part, per CTA
   const uint16_t* v_cache;
   uint16_t* o;
   float* lse;
@@ -141,8 +152,12 @@ __device__ __forceinline__ Shape shape_of(const KParams& p, int32_t n) {
   return s;
 }
 struct Item {
-  int32_t b, row, tokens, pos, seq, g, shared;
+  int32_t b, row, tokens, pos, seq, g, kind;
   int32_t steps, cost;  // cost: steps of the CTA
+  __device__ __forceinline__ int32_t tiles() const { return kind == kHalves ? 1 : 2; }
+  __device__ __forceinline__ int32_t cap(const KParams& p) const {
+    return kind == kShared ? 128 : ((tokens << p.gs) + 7) / 8 * 8;
+  }
 };
 __device__ __forceinline__ Item item_of(const KParams& p, int b, const Request& r, const Shape& s, int32_t i) {
   Item t;
@@ -150,8 +165,8 @@ __device__ __forceinline__ Item item_of(const KParams& p, int b, const Request& 
   t.b = b;
   t.seq = r.seq;
   int32_t j = s.np - 1;
-  t.shared = i < s.ps * p.Hkv;
-  if (t.shared) {
+  t.kind = i < s.ps * p.Hkv ? kShared : (p.Hkv > 1 ? kHeads : kHalves);
+  if (t.kind == kShared) {
     t.g = i / s.ps;
     j = s.ps - 1 - (i - t.g * s.ps);
   } else {
@@ -161,8 +176,66 @@ __device__ __forceinline__ Item item_of(const KParams& p, int b, const Request& 
   t.tokens = min(w, r.n - j * w);
   t.pos = r.seq - r.n + j * w;
   t.steps = max(1, (t.pos + t.tokens + kStep - 1) / kStep);
-  t.cost = !t.shared && p.Hkv == 1 ? (t.steps + 1) / 2 : t.steps;
+  t.cost = t.kind == kHalves ? (t.steps + 1) / 2 : t.steps;
   return t;
+}
+// Steps [s0, s1) of an item's cost; its partials go to rows `part` on.
+__device__ __forceinline__ Unit unit_of(const Item& t, int32_t s0, int32_t s1, int32_t part) {
+  Unit u{};
+  u.n[0] = s1 - s0;
+  u.key0[0] = s0 * kStep;
+  u.g[0] = u.g[1] = t.g;
+  if (t.kind == kHalves) {
+    u.key0[1] = (t.cost + s0) * kStep;
+    u.n[1] = max(0, min(t.steps, t.cost + s1) - (t.cost + s0));
+  } else {
+    u.key0[1] = u.key0[0];
+    u.n[1] = u.n[0];
+    u.g[1] += t.kind == kHeads;
+  }
+  u.part = part;
+  u.kind = t.kind;
+  u.b = t.b;
+  u.row = t.row;
+  u.tokens = t.tokens;
+  u.pos = t.pos;
+  u.seq = t.seq;
+  return u;
+}
+// Tile X of an item for the join; `valid`: whether there is anything to join.
+__device__ __forceinline__ JoinTile join_of(const KParams& p, const Item& t, int32_t X, bool valid, int32_t first,
+                                            int32_t rest, int32_t pieces) {
+  JoinTile j{};
+  const int32_t tile = t.kind == kShared ? X * p.tpt : 0;
+  j.row = t.row + tile;
+  j.rows = valid && X < t.tiles() ? min(p.tpt, t.tokens - tile) << p.gs : 0;
+  j.g = t.kind == kHeads ? t.g + X : t.g;
+  j.first = first + X * p.tile_rows;
+  j.rest = rest + X * p.tile_rows;
+  j.pieces = pieces;
+  j.cap = t.cap(p);
+  return j;
+}
+__device__ __forceinline__ void store_join(JoinTile* to, const JoinTile& j) {
+  reinterpret_cast<int4*>(to)[0] = make_int4(j.row, j.rows, j.g, j.first);
+  reinterpret_cast<int4*>(to)[1] = make_int4(j.rest, j.pieces, j.cap, 0);
+}
+
+// The cut into equal runs counts in units of time.
+__device__ __forceinline__ int32_t step_cost(int32_t kind) { return kind == kShared ? kSharedCost : kOwnCost; }
+__device__ __forceinline__ int32_t run_cost(const Item& t) { return t.cost * step_cost(t.kind) + kTileCost; }
+// ... of all pairs of one group of a request, and of the whole request.
+__device__ __forceinline__ int32_t pairs_cost(const KParams& p, const Request& r, const Shape& s) {
+  int32_t sum = 0;
+#pragma unroll 1
+  for (int32_t j = 0; j < s.ps; ++j) sum += run_cost(item_of(p, 0, r, s, j));
+  return sum;
+}
+__device__ __forceinline__ int32_t request_cost(const KParams& p, const Request& r) {
+  const Shape s = shape_of(p, r.n);
+  int32_t sum = p.Hkv * pairs_cost(p, r, s);
+  if (s.single) sum += run_cost(item_of(p, 0, r, s, p.Hkv * s.ps)) * max(1, p.Hkv / 2);
+  return sum;
 }
 
 __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
@@ -252,86 +325,48 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   each([&](const Item& t) { cost += t.cost; });
   const int64_t before = block_scan(cost, sums, all);
   const int32_t least = (int32_t)min((int64_t)kMinPiece, max((int64_t)2, (all + p.ctas - 1) / p.ctas));
-  // runs of an item's lanes in all pieces, and what they need
-  auto runs_of = [&](const Item& t, int32_t pieces) {
-    return !t.shared && p.Hkv == 1 && (pieces > 1 || t.steps >= 4) ? 2 * pieces : pieces;
-  };
-  auto cap_of = [&](const Item& t) { return t.shared ? 128 : ((t.tokens << p.gs) + 7) / 8 * 8; };
+  // units and, of these, pieces of items that are cut, and cut items
   int64_t left = all - before;
-  int32_t n_units = 0, n_joins = 0;
-  int64_t n_rows = 0;
+  int32_t n_units = 0, n_cut = 0, n_pieces = 0;
   each([&](const Item& t) {
-    const int32_t pieces = pieces_of(p, t.cost, left, least), runs = runs_of(t, pieces);
-    const int32_t lanes = t.shared || p.Hkv > 1 ? 2 : 1;
+    const int32_t pieces = pieces_of(p, t.cost, left, least);
     n_units += pieces;
-    if (runs > 1) {
-      n_joins += lanes;
-      n_rows += (int64_t)runs * lanes * cap_of(t);
-    }
+    n_cut += pieces > 1;
+    n_pieces += pieces > 1 ? pieces : 0;
     left -= t.cost;
   });
-  int64_t total_units, total_joins, total_rows;
+  int64_t total_units, total_cut;  // two counts of 32 bits in one scan
   int64_t at_unit = block_scan(n_units, sums, total_units);
-  int64_t at_join = block_scan(n_joins, sums, total_joins);
-  int64_t at_row = block_scan(n_rows, sums, total_rows);
+  const int64_t at = block_scan((int64_t)n_cut << 32 | n_pieces, sums, total_cut);
+  int32_t at_cut = (int32_t)(at >> 32), at_piece = (int32_t)at;
+  const bool over = total_units > p.cap_units || (total_cut >> 32) * 2 > p.cap_joins || (int32_t)total_cut > p.cap_pieces;
   if (tid == 0) {
     p.head->units = (int32_t)min(total_units, (int64_t)p.cap_units);
-    p.head->joins = (int32_t)min(total_joins, (int64_t)p.cap_joins);
+    p.head->joins = (int32_t)min((total_cut >> 32) * 2, (int64_t)p.cap_joins);
     p.head->ticket = p.ctas;  // the first units are the CTAs' own numbers
-    // not seen with lengths that add up: the workspace is sized for those
-    if (total_units > p.cap_units || total_joins > p.cap_joins || total_rows > p.cap_rows)
-      msa_record_error(kErrBadBlock);
+    if (over) msa_record_error(kErrBadBlock);  // not seen with lengths that add up: the workspace is sized for those
   }
   left = all - before;
   each([&](const Item& t) {
-    const int32_t pieces = pieces_of(p, t.cost, left, least), runs = runs_of(t, pieces);
-    const int32_t lanes = t.shared || p.Hkv > 1 ? 2 : 1, cap = cap_of(t);
-    const bool halves = lanes == 1 && runs > 1;  // the lanes take neighbouring runs of one tile
-    const int64_t rows = runs > 1 ? (int64_t)runs * lanes * cap : 0;
-    const bool fits = at_row + rows <= p.cap_rows;
-    auto begin = [&](int32_t run) { return (int32_t)((int64_t)t.steps * run / runs); };
-    for (int32_t k = 0; k < pieces; ++k) {
-      if (at_unit + k >= p.cap_units) break;
-      Unit u{};
-#pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        if (X == 1 && lanes == 1 && !halves) break;
-        const int32_t run = halves ? 2 * k + X : k;
-        const int32_t s0 = begin(run);
-        u.n[X] = fits ? begin(run + 1) - s0 : 0;
-        u.key0[X] = s0 * kStep;
-        u.g[X] = t.shared || lanes == 1 ? t.g : t.g + X;
-        u.part[X] = runs > 1 ? (int32_t)(at_row + ((int64_t)run * lanes + (halves ? 0 : X)) * cap) : -1;
-      }
-      if (!fits) u.n[0] = 1;  // keeps the list's end marker apart
-      u.b = t.b;
-      u.row = t.row;
-      u.tokens = fits ? t.tokens : 0;
-      u.pos = t.pos;
-      u.seq = t.seq;
-      u.shared = t.shared && fits;
+    const int32_t pieces = pieces_of(p, t.cost, left, least);
+    const bool cut = pieces > 1, fits = !cut || at_piece + pieces <= p.cap_pieces;
+    for (int32_t k = 0; k < pieces && at_unit + k < p.cap_units; ++k) {
+      Unit u = unit_of(t, (int32_t)((int64_t)t.cost * k / pieces), (int32_t)((int64_t)t.cost * (k + 1) / pieces),
+                       cut ? (at_piece + k) * 2 * p.tile_rows : -1);
+      if (!fits) u.tokens = 0;  // nowhere to go
       const int4* src = reinterpret_cast<const int4*>(&u);
       int4* dst = reinterpret_cast<int4*>(p.units + at_unit + k);
 #pragma unroll
       for (int x = 0; x < 4; ++x) dst[x] = src[x];
     }
-    if (runs > 1)
-      for (int32_t X = 0; X < lanes; ++X) {
-        if (at_join + X >= p.cap_joins) break;
-        JoinTile j{};
-        const int32_t tile = t.shared ? X : 0;
-        j.row = t.row + tile * p.tpt;
-        j.rows = fits ? min(p.tpt, t.tokens - tile * p.tpt) << p.gs : 0;
-        j.g = t.shared || lanes == 1 ? t.g : t.g + X;
-        j.part = (int32_t)(at_row + (int64_t)X * cap);
-        j.step = lanes * cap;
-        j.pieces = runs;
-        j.cap = cap;
-        p.joins[at_join + X] = j;
-      }
+    if (cut) {
+      for (int32_t X = 0; X < 2 && 2 * at_cut + X < p.cap_joins; ++X)
+        store_join(p.joins + 2 * at_cut + X, join_of(p, t, X, fits, at_piece * 2 * p.tile_rows,
+                                                     (at_piece + 1) * 2 * p.tile_rows, pieces));
+      ++at_cut;
+      at_piece += pieces;
+    }
     at_unit += pieces;
-    if (runs > 1) at_join += lanes;
-    at_row += rows;
     left -= t.cost;
   });
 }
@@ -354,11 +389,15 @@ struct Bars {
   uint64_t unit_full[kQueue], unit_free[kQueue];
   uint64_t late_full[kLate];
   uint64_t drained[2];
+  uint64_t half_full, half_free;  // kHalves: lane 1's part is there, is read
+  float2 half_ml[128];
   Unit unit[kQueue];
   Late late[kLate];
   int32_t odd[2];  // what is not finite was taken out of V, in this unit of the lane or one before
   uint32_t tmem_base;
   int32_t fail;
+  // cut into equal runs
+  int32_t w_sum[kThreads / 32], start_b, start_off, total, workers;
 };
 constexpr size_t kSmemBytes = kOffBar + ((sizeof(Bars) + 15) / 16) * 16;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -457,6 +496,9 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// SELF: the CTAs cut the whole call into equal runs of steps among them, each for itself from the lengths;
+// else they take the units that the plan kernel listed.
+template <bool SELF>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attention_kernel(const __grid_constant__ CUtensorMap qmap_t, const __grid_constant__ CUtensorMap qmap_1,
                            const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -491,6 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.unit_free[i], 11);  // readers: eight softmax warps, two issuers, the query loader
     }
     for (int i = 0; i < kLate; ++i) mbar_init(&B.late_full[i], 1);
+    mbar_init(&B.half_full, 4);
+    mbar_init(&B.half_free, 4);
     B.fail = 0;
     B.odd[0] = B.odd[1] = 0;
     mbar_fence_init();
@@ -516,6 +560,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this kernel leave; it waits for all of their stores.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (SELF) {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int32_t sum = 0;
+    bool any_bad = false;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      bool bad;
+      sum += request_cost(p, request_of(p, b, bad));
+      any_bad |= bad;
+    }
+    if (any_bad && blockIdx.x == 0) msa_record_error(kErrBadBlock);
+    int32_t before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    if (lane == 31) B.w_sum[warp] = before;
+    if (tid == 0) B.start_b = p.B;
+    __syncthreads();
+    before -= sum;
+    int32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += B.w_sum[w];
+      total += B.w_sum[w];
+    }
+    const int32_t workers = max(1, min((int32_t)gridDim.x, total / kLeastRun));
+    const int32_t x0 = (int32_t)((int64_t)total * min((int32_t)blockIdx.x, workers) / workers);
+    if (before <= x0 && x0 < before + sum) {  // this CTA starts in one of the thread's requests
+      int32_t off = x0 - before;
+      int b = b0;
+#pragma unroll 1
+      for (; b < b1; ++b) {
+        bool bad;
+        const int32_t c = request_cost(p, request_of(p, b, bad));
+        if (off < c) break;
+        off -= c;
+      }
+      B.start_b = b;
+      B.start_off = off;
+    }
+    if (tid == 0) {
+      B.total = total;
+      B.workers = workers;
+    }
+    __syncthreads();
+  }
   // The k-th unit for one of its readers.
   auto take = [&](int32_t& k, Unit& u) {
     const int q = k & (kQueue - 1);
@@ -526,14 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       u.n[x] = uniform(e.n[x]);
       u.key0[x] = uniform(e.key0[x]);
       u.g[x] = uniform(e.g[x]);
-      u.part[x] = uniform(e.part[x]);
     }
+    u.part = uniform(e.part);
+    u.kind = uniform(e.kind);
     u.b = uniform(e.b);
     u.row = uniform(e.row);
     u.tokens = uniform(e.tokens);
     u.pos = uniform(e.pos);
     u.seq = uniform(e.seq);
-    u.shared = uniform(e.shared);
     __syncwarp();
     mbar_arrive_if(&B.unit_free[q], lane == 0);
     ++k;
@@ -550,9 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int32_t used = 0;     // slots begun
       int32_t late_n = 0;   // late entries
       bool good = true;
+      // A step's sources: token rows; late rows y and end z of either lane's V, 8 bits each; groups (8 bits
+      // each) and lanes (bit 16 + X: lane X has the step, bit 18: both read one slot; 0: no step).
       struct Src {
-        int32_t tok[2], g[2], y[2], z[2];
-        int32_t lanes;  // bit X: lane X has the step; 4: both read one slot; 0: no step
+        int32_t tok[2], late, what;
       };
       // One slot: 64 rows of the map's tensor from token row tok on. `alone`: one lane reads it.
       auto slot = [&](const CUtensorMap* map, int32_t tok, int32_t g, bool alone, bool late, int32_t y, int32_t z,
@@ -580,77 +674,175 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto emit = [&](const CUtensorMap* map, const Src& s, bool v) {
         auto one = [&](int X, bool alone, int32_t lanes) {
-          return slot(map, s.tok[X], s.g[X], alone, v && s.y[X] < kStep, max(s.y[X], 0), max(s.z[X], 0), lanes);
+          const int32_t y = s.late >> (16 * X) & 255, z = s.late >> (16 * X + 8) & 255;
+          return slot(map, s.tok[X], s.what >> (8 * X) & 255, alone, v && y < kStep, y, z, lanes);
         };
-        if (s.lanes & 4) return one(0, false, 3);
-        if ((s.lanes & 1) && !one(0, true, 1)) return false;
-        if ((s.lanes & 2) && !one(1, true, 2)) return false;
+        if (s.what >> 18 & 1) return one(0, false, 3);
+        if ((s.what >> 16 & 1) && !one(0, true, 1)) return false;
+        if ((s.what >> 17 & 1) && !one(1, true, 2)) return false;
         return true;
       };
-      const int32_t total = p.head->units;
-      int32_t ticket = blockIdx.x, k = 0;
-      Src d1, d2;
-      d1.lanes = d2.lanes = 0;
-#pragma unroll 1
-      for (;;) {
-        // ---- the next unit
-        const int q = k & (kQueue - 1);
-        const bool end = ticket >= total;
-        int32_t word = 0;
-        if (!end && lane < 16) word = reinterpret_cast<const int32_t*>(p.units + ticket)[lane];
-        if (k >= kQueue && !(good = wait_or_fail(&B.unit_free[q], (k / kQueue - 1) & 1, fail))) break;
-        if (lane < 16) reinterpret_cast<int32_t*>(&B.unit[q])[lane] = word;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.unit_full[q]);
-        ++k;
-        if (end) break;
-        int32_t n[2], key0[2], g[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          n[x] = __shfl_sync(0xffffffffu, word, x);
-          key0[x] = __shfl_sync(0xffffffffu, word, 2 + x);
-          g[x] = __shfl_sync(0xffffffffu, word, 4 + x);
-        }
-        const int32_t b = __shfl_sync(0xffffffffu, word, 8), pos = __shfl_sync(0xffffffffu, word, 11);
-        const int32_t seq = __shfl_sync(0xffffffffu, word, 12), shared = __shfl_sync(0xffffffffu, word, 13);
-        const int32_t steps = max(n[0], n[1]);
-        int32_t next = 0;
-        // the pages of 32 steps from j on of a lane's run, one per thread
-        auto look_up = [&](int x, int32_t j) {
-          const int32_t jj = j + lane, key = key0[x] + jj * kStep;
-          const bool has = jj < n[x] && key < seq;
-          int32_t page = has ? p.page_table[(int64_t)b * p.max_blocks + key / MSA_BLOCK_TOKENS] : 0;
-          const bool bad = page < 0 || page >= p.num_pages;
-          if (bad) page = 0;
-          if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
-          return page;
-        };
-        const bool apart = n[1] > 0 && key0[1] != key0[0];
-        int32_t page[2] = {0, 0};
-#pragma unroll 1
-        for (int32_t j = 0; j < steps; ++j) {
-          if ((j & 31) == 0) {
-            page[0] = look_up(0, j);
-            page[1] = apart ? look_up(1, j) : page[0];
+      // ---- where the units come from
+      int32_t ticket = blockIdx.x, total = 0;
+      int32_t w_b = 0, w_i = 0, w_off = 0, w_left = 0;  // SELF: request, item, offset in it, what is left of the run
+      bool joins = false;
+      if (SELF) {
+        const int32_t c = blockIdx.x, W = B.workers;
+        if (c < W) w_left = (int32_t)((int64_t)B.total * (c + 1) / W) - (int32_t)((int64_t)B.total * c / W);
+        if (B.start_b >= p.B) w_left = 0;
+        if (w_left > 0) {
+          w_b = B.start_b;
+          w_off = B.start_off;
+          bool bad;
+          const Request q = request_of(p, w_b, bad);
+          const Shape h = shape_of(p, q.n);
+          if (h.ps > 0) {
+            const int32_t group = pairs_cost(p, q, h), g = min(p.Hkv, w_off / group);
+            w_off -= g * group;
+            w_i = g * h.ps;
           }
-          if (j == max(0, steps - 6) && lane == 0) next = atomicAdd(&p.head->ticket, 1);
-          Src s;
-          s.lanes = shared ? 4 : (j < n[0] ? 1 : 0) | (j < n[1] ? 2 : 0);
+#pragma unroll 1
+          for (; w_i < h.items; ++w_i) {
+            const int32_t cost = run_cost(item_of(p, w_b, q, h, w_i));
+            if (w_off < cost) break;
+            w_off -= cost;
+          }
+        }
+      } else {
+        total = p.head->units;
+      }
+      auto next_unit = [&]() {
+        Unit u{};
+        if constexpr (!SELF) {
+          if (ticket < total) {
+            const int4* src = reinterpret_cast<const int4*>(p.units + ticket);
+            int4* dst = reinterpret_cast<int4*>(&u);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) dst[x] = src[x];
+            int32_t t = 0;
+            if (lane == 0) t = atomicAdd(&p.head->ticket, 1);
+            ticket = __shfl_sync(0xffffffffu, t, 0);
+          }
+          return u;
+        } else {
+#pragma unroll 1
+          while (w_left > 0 && w_b < p.B) {
+            bool bad;
+            const Request q = request_of(p, w_b, bad);
+            const Shape h = shape_of(p, q.n);
+            if (w_i >= h.items) {
+              ++w_b;
+              w_i = 0;
+              continue;
+            }
+            const Item t = item_of(p, w_b, q, h, w_i);
+            const int32_t a0 = w_off, cost = run_cost(t), a1 = min(cost, a0 + w_left), per = step_cost(t.kind);
+            const int32_t s0 = min(t.cost, (a0 + per - 1) / per), s1 = min(t.cost, (a1 + per - 1) / per);
+            const int32_t c = blockIdx.x, C = gridDim.x, row = 2 * p.tile_rows;
+            // where the item begins, from the run's end
+            const int64_t W = B.workers, all = B.total;
+            const int64_t begin = all * (c + 1) / W - w_left - a0;
+            w_left -= a1 - a0;
+            w_off = a1;
+            if (a1 == cost) {
+              ++w_i;
+              w_off = 0;
+            }
+            if (s0 >= s1) continue;
+            // a run has at most one piece that ends an item that it did not begin, and one that begins an item
+            // without ending it
+            if (s0 == 0 && s1 == t.cost) {
+              u = unit_of(t, s0, s1, -1);
+            } else {
+              u = unit_of(t, s0, s1, (s0 == 0 ? C + c : c) * row);
+              if (s0 > 0 && s1 == t.cost) {
+                int32_t c0 = max(0, min((int32_t)(begin * W / all), c));
+                while (c0 > 0 && all * c0 / W > begin) --c0;
+                while (c0 < c && all * (c0 + 1) / W <= begin) ++c0;
+                if (lane < 2)
+                  store_join(p.joins + 2 * c + lane, join_of(p, t, lane, true, (C + c0) * row, (c0 + 1) * row, c - c0 + 1));
+                joins = true;
+              }
+            }
+            break;
+          }
+          return u;
+        }
+      };
+      int32_t k = 0;
+      int32_t page[2] = {0, 0}, ahead[2] = {0, 0};
+      // the pages of 32 steps from j on of a lane's run, one per thread
+      auto look_up = [&](const Unit& u, int x, int32_t j) {
+        const int32_t jj = j + lane, key = u.key0[x] + jj * kStep;
+        const bool has = jj < u.n[x] && key < u.seq;
+        int32_t at = has ? p.page_table[(int64_t)u.b * p.max_blocks + key / MSA_BLOCK_TOKENS] : 0;
+        const bool bad = at < 0 || at >= p.num_pages;
+        if (bad) at = 0;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
+        return at;
+      };
+      // Publishes the next unit and looks up its first pages.
+      auto publish = [&]() {
+        const Unit u = next_unit();
+        const int q = k & (kQueue - 1);
+        if (k >= kQueue && !wait_or_fail(&B.unit_free[q], (k / kQueue - 1) & 1, fail)) return false;
+        if (lane == 0) {
+          B.unit[q] = u;
+          mbar_arrive(&B.unit_full[q]);
+        }
+        __syncwarp();
+        ++k;
+        ahead[0] = look_up(u, 0, 0);
+        ahead[1] = u.kind == kHalves ? look_up(u, 1, 0) : ahead[0];
+        return true;
+      };
+      Src d1, d2;
+      d1.what = d2.what = 0;
+      good = publish();
+#pragma unroll 1
+      while (good) {
+        Unit u;
+        {
+          const Unit& e = B.unit[(k - 1) & (kQueue - 1)];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int32_t key = key0[x] + j * kStep;
-            s.tok[x] = __shfl_sync(0xffffffffu, page[x], j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
-            s.g[x] = g[x];
-            s.y[x] = pos + 1 - key;
-            s.z[x] = seq - key;
+            u.n[x] = uniform(e.n[x]);
+            u.key0[x] = uniform(e.key0[x]);
+            u.g[x] = uniform(e.g[x]);
           }
+          u.kind = uniform(e.kind);
+          u.b = uniform(e.b);
+          u.pos = uniform(e.pos);
+          u.seq = uniform(e.seq);
+        }
+        const int32_t steps = u.n[0];
+        if (steps == 0) break;
+        page[0] = ahead[0];
+        page[1] = ahead[1];
+        const int32_t at = max(0, steps - 5);  // the ring is full by then: looking ahead costs nothing
+#pragma unroll 1
+        for (int32_t j = 0; j < steps; ++j) {
+          if (j > 0 && (j & 31) == 0) {
+            page[0] = look_up(u, 0, j);
+            page[1] = u.kind == kHalves ? look_up(u, 1, j) : page[0];
+          }
+          Src s;
+          s.late = 0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int32_t key = u.key0[x] + j * kStep;
+            s.tok[x] = __shfl_sync(0xffffffffu, page[x], j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+            const int32_t y = max(0, min(u.pos + 1 - key, kStep)), z = max(0, min(u.seq - key, kStep));
+            s.late |= (y | z << 8) << (16 * x);
+          }
+          s.what = u.g[0] | u.g[1] << 8 | (u.kind == kShared ? 1 << 18 : 1 << 16 | (j < u.n[1] ? 1 << 17 : 0));
           if (!(good = emit(&vmap, d2, true) && emit(&kmap, s, false))) break;
           d2 = d1;
           d1 = s;
+          if (j == at && !(good = publish())) break;
         }
-        if (!good) break;
-        ticket = __shfl_sync(0xffffffffu, next, 0);
       }
+      if (SELF && lane < 2 && !joins) store_join(p.joins + 2 * blockIdx.x + lane, JoinTile{});
       good = good && emit(&vmap, d2, true) && emit(&vmap, d1, true);
       if (good && lane == 0) {  // the late-row warps' end
         B.late[late_n & (kLate - 1)] = {0, 0, -1, 0};
@@ -680,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool single = u.tokens == 1;
             const CUtensorMap* map = single ? &qmap_1 : &qmap_t;
             uint8_t* dst = smem + X * kQTile;
-            const int32_t row = u.row + (u.shared ? X * p.tpt : 0);
+            const int32_t row = u.row + (u.kind == kShared ? X * p.tpt : 0);
             mbar_expect_tx(&B.q_full[X], (single ? p.G : 128) * 256);
             tma_load_5d(dst, map, &B.q_full[X], 0, 0, row, 0, u.g[X]);
             tma_load_5d(dst + kQHalf, map, &B.q_full[X], 0, 0, row, 1, u.g[X]);
@@ -712,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kMine = 1, kTwo = 2, kOpens = 4, kAny = 8;  // of a step
       uint32_t d1 = 0, d2 = 0;
       Unit u;
-      u.n[0] = u.n[1] = u.shared = 0;
+      u.n[0] = u.n[1] = u.kind = 0;
       int32_t k = 0, j = 0, steps = 0, n_s = 0, n_o = 0, opened = 0, tiles = 0;
       RingPos r{0, 0};
       bool good = true, more = true;
@@ -744,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (more) {
             const int32_t mine = X ? u.n[1] : u.n[0], other = X ? u.n[0] : u.n[1];
-            d = kAny | (j < mine ? kMine : 0u) | (!u.shared && j < mine && j < other ? kTwo : 0u) |
+            d = kAny | (j < mine ? kMine : 0u) | (u.kind != kShared && j < mine && j < other ? kTwo : 0u) |
                 (j == 0 && mine > 0 ? kOpens : 0u);
             if (d & kMine) {
               const RingPos at = (d & kTwo) && X ? r.after(1) : r;
@@ -831,17 +1023,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tmem = tmem + lane_addr + X * 128;
     const uint32_t o_tmem = tmem + lane_addr + 256 + X * 128;
     const int32_t token = row >> p.gs;
-    int32_t n = 0, k = 0;
+    int32_t n = 0, k = 0, halved = 0;
     Unit u;
     bool good = true;
 #pragma unroll 1
     while (good && take(k, u) && (u.n[0] | u.n[1]) != 0) {
       const int32_t steps = X ? u.n[1] : u.n[0];
       if (steps == 0) continue;
-      const int32_t tile = u.shared ? X * p.tpt : 0;  // its first token within the unit's
+      const int32_t tile = u.kind == kShared ? X * p.tpt : 0;  // its first token within the unit's
       const int32_t rows = min(p.tpt, u.tokens - tile) << p.gs;
       const int32_t first_vis = u.pos + tile + 1;     // keys that the tile's first row sees
-      const int32_t key0 = X ? u.key0[1] : u.key0[0], g = X ? u.g[1] : u.g[0], part = X ? u.part[1] : u.part[0];
+      const int32_t key0 = X ? u.key0[1] : u.key0[0], g = X ? u.g[1] : u.g[0];
+      const int32_t part = u.part < 0 ? -1 : u.part + X * p.tile_rows;
+      const bool halves = u.kind == kHalves && u.n[1] > 0;
       const bool act = 32 * (warp & 3) < rows;  // a warp of padding rows only keeps the barriers
       const bool mine = row < rows;  // the rows behind hold whatever the query area held before
       float m_run = -INFINITY, m_nat = 0.f, l = 0.f;  // running reference (log2 units; natural) and sum
@@ -932,16 +1126,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!good) break;
       // ---------------- the output, or the run's partial
       const int64_t out = ((int64_t)(u.row + tile + token)) * p.Hq + (g << p.gs) + (row & (p.G - 1));
-      const int32_t cap = u.shared ? 128 : ((u.tokens << p.gs) + 7) / 8 * 8;
+      const int32_t cap = u.kind == kShared ? 128 : ((u.tokens << p.gs) + 7) / 8 * 8;
+      if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
+      tmem_fence_after();
+      float f0 = 1.f, f1 = 0.f;  // weights of the lanes' parts
+      float4* half = nullptr;    // lane 1's part, for which lane 0 waits
+      if (halves) {
+        half = reinterpret_cast<float4*>(p.half_po) + (int64_t)blockIdx.x * 128 * 32 + row;
+        if (X == 1) {
+          if (halved > 0 && !(good = wait_or_fail(&B.half_free, (halved - 1) & 1, fail))) break;
+          B.half_ml[row] = make_float2(m_run, l);
+        } else {
+          if (!(good = wait_or_fail(&B.half_full, halved & 1, fail))) break;
+          const float2 o = B.half_ml[row];
+          const float m = fmaxf(m_run, o.x);
+          if (o.x != -INFINITY || o.y != 0.f) f1 = ex2(o.x - m);  // lane 1's keys count for the row
+          if (m_run != m) f0 = ex2(m_run - m);
+          m_run = m;
+          l = l * f0 + (f1 != 0.f ? o.y * f1 : 0.f);
+        }
+        ++halved;
+      }
       float scale = 1.f;
       if (part < 0) {
         scale = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: o = 0, lse = -inf
-        if (mine && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
-      } else if (mine) {
+        if (mine && p.lse && !(halves && X == 1)) p.lse[out] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
+      } else if (mine && !(halves && X == 1)) {
         p.ml[part + row] = make_float2(m_run, l);
       }
-      if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
-      tmem_fence_after();
       const bool odd = *(volatile int32_t*)&B.odd[X] != 0;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -979,6 +1191,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (halves) {
+          if (X == 1) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              __stcg(half + (c * 16 + x) * 128, make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+            continue;
+          }
+#pragma unroll
+          for (int x = 0; x < 64; ++x) o[x] *= f0;
+          if (f1 != 0.f)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float4 h = __ldcg(half + (c * 16 + x) * 128);
+              o[4 * x] = fmaf(h.x, f1, o[4 * x]);
+              o[4 * x + 1] = fmaf(h.y, f1, o[4 * x + 1]);
+              o[4 * x + 2] = fmaf(h.z, f1, o[4 * x + 2]);
+              o[4 * x + 3] = fmaf(h.w, f1, o[4 * x + 3]);
+            }
+        }
         if (part < 0) {
           uint4* dst = reinterpret_cast<uint4*>(p.o + out * 128 + c * 64);
 #pragma unroll
@@ -994,6 +1225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[(int64_t)x * cap] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
       }
+      if (halves) {  // lane 1's part is written, or read
+        __threadfence_block();
+        __syncwarp();
+        mbar_arrive_if(X == 1 ? &B.half_full : &B.half_free, lane == 0);
+      }
     }
   }
   // ------------------------------------------------------------------ teardown
@@ -1007,9 +1243,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------------------ join
-// A CTA joins eight rows of a tile at a time; a thread owns four channels of one row, so a warp reads
-// whole 128-byte lines of the partials' [channel quad][row][4] layout. A row's pieces are dealt to
-// kSplit threads, four loads in flight each, and joined through shared memory.
+// A CTA joins a tile: four groups of 256 threads take eight rows each, a thread four channels of one row, so
+// a warp reads whole 128-byte lines of the partials' [channel quad][row][4] layout. With fewer rows the
+// groups deal a row's pieces among them, four loads in flight each, and join through shared memory.
 constexpr int kJoinRows = 8;
 constexpr int kJoinSplit = 4;
 constexpr int kJoinThreads = kJoinRows * 32 * kJoinSplit;
@@ -1043,55 +1279,63 @@ __device__ __forceinline__ void join_four(Joined& j, const float2 (&ml)[4], cons
   }
 }
 
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KParams p) {
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KParams p, int32_t tiles) {
   __shared__ float2 s_ml[kJoinSplit][kJoinRows * 32];
   __shared__ float4 s_o[kJoinSplit][kJoinRows * 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int t = threadIdx.x % (kJoinRows * 32), split = threadIdx.x / (kJoinRows * 32);
+  const int t = threadIdx.x % (kJoinRows * 32), group = threadIdx.x / (kJoinRows * 32);
   const int32_t quad = t / kJoinRows;
-  const int32_t tasks = p.head->joins * (128 / kJoinRows);
+  if (tiles == 0) tiles = p.head->joins;
 #pragma unroll 1
-  for (int32_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const JoinTile e = p.joins[task / (128 / kJoinRows)];
-    const int32_t r0 = task % (128 / kJoinRows) * kJoinRows;
-    if (r0 >= e.rows) continue;  // uniform
-    const int32_t r = r0 + (t & (kJoinRows - 1));
-    const bool valid = r < e.rows;
-    Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (valid) {
-      const float2* mls = p.ml + e.part + r;
-      const float4* os = reinterpret_cast<const float4*>(p.po + (int64_t)e.part * 128) + (int64_t)quad * e.cap + r;
-      for (int32_t k = split; k < e.pieces; k += 4 * kJoinSplit) {
-        float2 ml[4];
-        float4 o[4];
-        int have = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t x = k + u * kJoinSplit;
-          if (x < e.pieces) {
-            ml[u] = __ldcs(mls + x * e.step);
-            o[u] = __ldcs(os + x * e.step * 32);
-            ++have;
-          }
-        }
-        join_four(j, ml, o, have);
-      }
-    }
-    s_ml[split][t] = make_float2(j.m, j.l);
-    s_o[split][t] = j.acc;
-    __syncthreads();
-    if (split == 0) {
-      float2 ml[4];
-      float4 o[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int x = u + 1 < kJoinSplit ? u + 1 : 0;
-        ml[u] = s_ml[x][t];
-        o[u] = s_o[x][t];
-      }
-      join_four(j, ml, o, kJoinSplit - 1);
+  for (int32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const JoinTile e = p.joins[tile];
+    if (e.rows <= 0) continue;
+    const int32_t split = e.rows <= kJoinRows ? 4 : (e.rows <= 2 * kJoinRows ? 2 : 1);
+    const int32_t step = 2 * p.tile_rows;
+#pragma unroll 1
+    for (int32_t r0 = 0; r0 < e.rows; r0 += kJoinRows * kJoinSplit / split) {
+      const int32_t part = group % split;
+      const int32_t r = r0 + group / split * kJoinRows + (t & (kJoinRows - 1));
+      const bool valid = r < e.rows;
+      Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       if (valid) {
+#pragma unroll 1
+        for (int32_t k = part; k < e.pieces; k += 4 * split) {
+          float2 ml[4];
+          float4 o[4];
+          int have = 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int32_t x = k + u * split;
+            if (x < e.pieces) {
+              const int64_t at = x == 0 ? e.first : e.rest + (int64_t)(x - 1) * step;
+              ml[u] = __ldcs(p.ml + at + r);
+              o[u] = __ldcs(reinterpret_cast<const float4*>(p.po) + at * 32 + (int64_t)quad * e.cap + r);
+              ++have;
+            }
+          }
+          join_four(j, ml, o, have);
+        }
+      }
+      if (split > 1) {
+        s_ml[group][t] = make_float2(j.m, j.l);
+        s_o[group][t] = j.acc;
+        __syncthreads();
+        if (part == 0) {
+          float2 ml[4];
+          float4 o[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int x = group + (u + 1 < split ? u + 1 : 0);
+            ml[u] = s_ml[x][t];
+            o[u] = s_o[x][t];
+          }
+          join_four(j, ml, o, split - 1);
+        }
+        __syncthreads();  // the shared parts are read
+      }
+      if (valid && part == 0) {
         const float inv = j.l == 0.f ? 0.f : 1.0f / j.l;  // a row that sees no key: o = 0, lse = -inf
         const int64_t out = (int64_t)(e.row + (r >> p.gs)) * p.Hq + (e.g << p.gs) + (r & (p.G - 1));
         *reinterpret_cast<uint2*>(p.o + out * 128 + quad * 4) =
@@ -1099,34 +1343,41 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
         if (quad == 0 && p.lse) p.lse[out] = j.l == 0.f ? -INFINITY : (j.m + log2f(j.l)) * kLn2;
       }
     }
-    __syncthreads();  // the shared parts are read
   }
 }
 
 // ------------------------------------------------------------------------------ host
 struct Layout {
-  int32_t cap_units, cap_joins;
-  int64_t cap_rows;
-  size_t units, joins, ml, po, total;
+  bool self;
+  int32_t cap_units, cap_joins, cap_pieces, tile_rows;
+  size_t units, joins, ml, po, half, total;
 };
 
 Layout layout_of(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks, int ctas) {
   Layout y{};
   const int64_t G = Hq / Hkv, tpt = 128 / G, requests = B < T ? B : T;
   // pairs of tiles and single tiles
-  const int64_t items = Hkv * (T / (2 * tpt) + requests);
-  // Pieces of the items that are cut: an item of c steps with r still to come, itself included, has
-  // ceil(c / max(8, r / 2 ctas)) pieces, at most 2 c / that for more than one. r falls to 0 over the call,
-  // so the sum is at most 2 * 2 ctas * (1 + log(most steps / 8)); with less than 8 steps per CTA pieces
-  // are as short as these, and at most 2 * ctas.
-  const double most = 2.0 * max_blocks / kMinPiece;
-  const int64_t cut = (int64_t)(4.0 * ctas * (1.0 + (most > 1 ? log(most) : 0.0))) + 16;
+  const int64_t pairs = Hkv * (T / (2 * tpt)), items = pairs + Hkv * requests;
   const int64_t rows = (T * G + 7) / 8 * 8;
-  // one KV group: single tiles that are not cut have two runs as well
-  const int64_t halves = Hkv == 1 ? requests : 0;
-  y.cap_units = (int32_t)(items + cut);
-  y.cap_joins = (int32_t)(2 * cut + halves);
-  y.cap_rows = 2 * cut * (rows < 128 ? rows : 128) + (halves ? 2 * (T * G + 8 * halves) : 0);
+  y.tile_rows = (int32_t)(rows < 128 ? rows : 128);
+  // Equal runs where tokens fill one tile per request on average, or there are few pairs: keys are then read
+  // by few CTAs each, and what counts is that all CTAs have work, without the plan kernel's time.
+  y.self = (T <= B * tpt || pairs <= 2 * ctas) &&
+           items * ((2 * (int64_t)max_blocks + 1) * kOwnCost + kTileCost) <= 2147483647;
+  if (y.self) {
+    y.cap_joins = 2 * ctas;
+    y.cap_pieces = 2 * ctas;  // of a run's first and last item
+  } else {
+    // Pieces of the items that are cut: an item of c steps with r still to come, itself included, has
+    // ceil(c / max(8, r / 2 ctas)) pieces, at most 2 c / that for more than one. r falls to 0 over the call,
+    // so the sum is at most 2 * 2 ctas * (1 + log(most steps / 8)); with less than 8 steps per CTA pieces
+    // are as short as these, and at most 2 * ctas.
+    const double most = 2.0 * max_blocks / kMinPiece;
+    const int64_t cut = (int64_t)(4.0 * ctas * (1.0 + (most > 1 ? log(most) : 0.0))) + 16;
+    y.cap_units = (int32_t)(items + cut);
+    y.cap_joins = (int32_t)(2 * cut);
+    y.cap_pieces = (int32_t)cut;
+  }
   size_t at = align_up(sizeof(Header), 256);
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -1135,10 +1386,54 @@ Layout layout_of(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_bloc
   };
   y.units = take((size_t)y.cap_units * sizeof(Unit));
   y.joins = take((size_t)y.cap_joins * sizeof(JoinTile));
-  y.ml = take((size_t)y.cap_rows * sizeof(float2));
-  y.po = take((size_t)y.cap_rows * 128 * sizeof(float));
+  y.ml = take((size_t)y.cap_pieces * 2 * y.tile_rows * sizeof(float2));
+  y.po = take((size_t)y.cap_pieces * 2 * y.tile_rows * 128 * sizeof(float));
+  y.half = take(Hkv == 1 ? (size_t)ctas * 128 * 128 * sizeof(float) : 0);
   y.total = at;
   return y;
+}
+
+template <bool SELF>
+cudaError_t launch_kernels(const CUtensorMap& qt, const CUtensorMap& q1, const CUtensorMap& km, const CUtensorMap& vm,
+                           const KParams& p, cudaStream_t stream) {
+  cudaError_t e;
+  static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, chunk_attention_kernel<SELF>);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (!SELF) {
+    static std::atomic<size_t> raised[kMaxDevices];
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = (size_t)(p.B + 1) * sizeof(int32_t);
+    e = launch_with_smem(chunk_plan_kernel, (kMaxRequests + 1) * sizeof(int32_t), raised,
+                         [&] { return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p); });
+    if (e != cudaSuccess) return e;
+  }
+  static std::atomic<size_t> raised[kMaxDevices];
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  e = launch_with_smem(chunk_attention_kernel<SELF>, kSmemBytes, raised,
+                       [&] { return cudaLaunchKernelEx(&cfg, chunk_attention_kernel<SELF>, qt, q1, km, vm, p); });
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(2 * p.ctas));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, chunk_join_kernel, p, SELF ? 2 * p.ctas : 0);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 }  // namespace
@@ -1167,13 +1462,15 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
   p.ctas = ctas;
   p.cap_units = y.cap_units;
   p.cap_joins = y.cap_joins;
-  p.cap_rows = y.cap_rows;
+  p.cap_pieces = y.cap_pieces;
+  p.tile_rows = y.tile_rows;
   uint8_t* w = a.workspace;
   p.head = reinterpret_cast<Header*>(w);
   p.units = reinterpret_cast<Unit*>(w + y.units);
   p.joins = reinterpret_cast<JoinTile*>(w + y.joins);
   p.ml = reinterpret_cast<float2*>(w + y.ml);
   p.po = reinterpret_cast<float*>(w + y.po);
+  p.half_po = reinterpret_cast<float*>(w + y.half);
   p.v_cache = a.v_cache;
   p.o = a.o;
   p.lse = a.lse;
@@ -1191,40 +1488,7 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
   if (!encode_bf16_map(&qt, a.q, 5, qd, qs, bt, true) || !encode_bf16_map(&q1, a.q, 5, qd, qs, b1, true) ||
       !encode_bf16_map(&km, a.k_cache, 4, kd, ks, bk, true) || !encode_bf16_map(&vm, a.v_cache, 4, kd, ks, bk, true))
     return cudaErrorInvalidValue;
-  static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes fa;
-    const cudaError_t e = cudaFuncGetAttributes(&fa, chunk_attention_kernel);
-    if (e != cudaSuccess) return e;
-    regs.store(fa.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const size_t plan_smem = (size_t)(a.B + 1) * sizeof(int32_t);
-  static std::atomic<size_t> raised_plan[kMaxDevices], raised[kMaxDevices];
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = plan_smem;
-  cudaError_t e = launch_with_smem(chunk_plan_kernel, (kMaxRequests + 1) * sizeof(int32_t), raised_plan,
-                                   [&] { return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p); });
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  e = launch_with_smem(chunk_attention_kernel, kSmemBytes, raised,
-                       [&] { return cudaLaunchKernelEx(&cfg, chunk_attention_kernel, qt, q1, km, vm, p); });
-  if (e != cudaSuccess) return e;
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, chunk_join_kernel, p);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e;
+  return y.self ? launch_kernels<true>(qt, q1, km, vm, p, stream) : launch_kernels<false>(qt, q1, km, vm, p, stream);
 }
 
 }  // namespace msa

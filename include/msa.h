@@ -493,10 +493,12 @@ MSA_API int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache,
  *   o [T, Hq, D] bf16, lse [T, Hq] fp32 or NULL (out; neither may overlap an input)
  *   workspace >= msa_chunk_attention_workspace_size(B, T, Hq, Hkv, max_blocks) bytes, 256-byte
  *   aligned, any contents (its size goes with the current device's SM count). Calls that may run
- *   concurrently need separate workspaces. It holds the list of work and the fp32 partials of the most
- *   pieces that any lengths lead to, about 130 KB for each of 600 * (1 + log(max_blocks / 4)) pieces
- *   (less where T * G < 128): with 152 SMs 13 MB for one row of G 8 and 128 blocks, 0.46 GB for 2048
- *   rows and 485 blocks, 0.56 GB for 1024.
+ *   concurrently need separate workspaces. It holds fp32 partials, 520 bytes per row of 2 * min(128,
+ *   T * Hq / Hkv) rows a piece. Where T <= B * 128 * Hkv / Hq (one tile of query rows per request on
+ *   average) or few pairs of tiles come together, CTAs cut the keys into equal runs, at most two pieces per
+ *   SM: 40 MB with 152 SMs (2.5 MB for one row of G 8); else, for long prompts, it also holds the list of
+ *   work, and the most pieces that any lengths lead to, 600 * (1 + log(max_blocks / 4)): 0.46 GB for 2048
+ *   rows of one request with G 8 and 485 blocks, 0.53 GB for 1024 blocks.
  * B <= 16384, T*Hq in int32. Lengths and tables are read on the device: a captured call can be
  * replayed with other values in the same buffers. cu_tokens out of order or outside [0, T], lengths
  * below n_b or above max_blocks*128 are clamped and set bit 1 of the device error word, a page id
