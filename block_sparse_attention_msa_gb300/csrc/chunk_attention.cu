@@ -379,14 +379,15 @@ struct Late {
 };
 constexpr int kLate = 16;
 static_assert(kLate > kSlots + 1, "an entry is not overwritten while it is open");
-constexpr int kQueue = 2;
+constexpr int kQueue = 4;  // units that the feeder is ahead of the slowest reader at most
 
 struct Bars {
   uint64_t kv_full[kSlots], kv_empty[kSlots];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[2][2], q_empty[2][2];  // [lane][the lane's tile & 1]
   uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][the lane's step & 1]
   uint64_t o_free[2];
   uint64_t unit_full[kQueue], unit_free[kQueue];
+  uint64_t want;  // the producer nears the end of a unit
   uint64_t late_full[kLate];
   uint64_t drained[2];
   uint64_t half_full, half_free;  // kHalves: lane 1's part is there, is read
@@ -500,7 +501,8 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint4 v) {
 // else they take the units that the plan kernel listed.
 template <bool SELF>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_attention_kernel(const __grid_constant__ CUtensorMap qmap_t, const __grid_constant__ CUtensorMap qmap_1,
+    chunk_attention_kernel(const __grid_constant__ CUtensorMap qmap_t, const __grid_constant__ CUtensorMap qmap_h,
+                           const __grid_constant__ CUtensorMap qmap_1,
                            const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const __grid_constant__ KParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];  // 1024: the swizzle atoms
@@ -518,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.kv_empty[i], 2);  // both issuers, or one and the producer
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&B.q_full[x], 1);
-      mbar_init(&B.q_empty[x], 1);
       mbar_init(&B.o_free[x], 4);
       mbar_init(&B.drained[x], 1);
       for (int i = 0; i < 2; ++i) {
+        mbar_init(&B.q_full[x][i], 1);
+        mbar_init(&B.q_empty[x][i], 1);
         mbar_init(&B.s_full[x][i], 1);
         mbar_init(&B.o_full[x][i], 1);
         mbar_init(&B.p_full[x][i], 4);
@@ -530,9 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&B.unit_full[i], 1);
-      mbar_init(&B.unit_free[i], 11);  // readers: eight softmax warps, two issuers, the query loader
+      mbar_init(&B.unit_free[i], 12);  // readers: eight softmax warps, two issuers, the K/V and query loaders
     }
     for (int i = 0; i < kLate; ++i) mbar_init(&B.late_full[i], 1);
+    mbar_init(&B.want, 1);
     mbar_init(&B.half_full, 4);
     mbar_init(&B.half_free, 4);
     B.fail = 0;
@@ -549,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
     tma_prefetch_desc(&qmap_t);
+    tma_prefetch_desc(&qmap_h);
     tma_prefetch_desc(&qmap_1);
   }
   tmem_fence_before();
@@ -609,6 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
+  // Tiles of at most 64 rows (a wider group's token of 128 rows is none).
+  auto is_small = [&](const Unit& u) { return u.kind != kShared && u.tokens << p.gs <= 64; };
   // The k-th unit for one of its readers.
   auto take = [&](int32_t& k, Unit& u) {
     const int q = k & (kQueue - 1);
@@ -635,10 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
     if (warp == 0) {
-      // ============================================================== units and K/V
-      // Takes units, publishes them and loads their keys and values, in the order in which the MMAs use
-      // them: V(i - 2), K(i) for each step i of the CTA's steps, a unit's behind the other's. A step of
-      // lanes with keys of their own has two slots for each.
+      // ============================================================== K/V
+      // Loads the units' keys and values in the order in which the MMAs use them: V(i - 2), K(i) for each
+      // step i of the CTA's steps, a unit's behind the other's. A step of lanes with keys of their own has
+      // two slots for each.
       RingPos r{0, 0};
       int32_t used = 0;     // slots begun
       int32_t late_n = 0;   // late entries
@@ -682,9 +688,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((s.what >> 17 & 1) && !one(1, true, 2)) return false;
         return true;
       };
-      // ---- where the units come from
+      int32_t k = 0, page[2] = {0, 0};
+      // the pages of 32 steps from j on of a lane's run, one per thread
+      auto look_up = [&](const Unit& u, int x, int32_t j) {
+        const int32_t jj = j + lane, key = u.key0[x] + jj * kStep;
+        const bool has = jj < u.n[x] && key < u.seq;
+        int32_t at = has ? p.page_table[(int64_t)u.b * p.max_blocks + key / MSA_BLOCK_TOKENS] : 0;
+        const bool bad = at < 0 || at >= p.num_pages;
+        if (bad) at = 0;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
+        return at;
+      };
+      Src d1, d2;
+      d1.what = d2.what = 0;
+      Unit u;
+      while (good && (good = take(k, u)) && u.n[0] > 0) {
+        const int32_t steps = u.n[0];
+#pragma unroll 1
+        for (int32_t j = 0; j < steps; ++j) {
+          if ((j & 31) == 0) {
+            page[0] = look_up(u, 0, j);
+            page[1] = u.kind == kHalves ? look_up(u, 1, j) : page[0];
+          }
+          Src s;
+          s.late = 0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int32_t key = u.key0[x] + j * kStep;
+            s.tok[x] = __shfl_sync(0xffffffffu, page[x], j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+            const int32_t y = max(0, min(u.pos + 1 - key, kStep)), z = max(0, min(u.seq - key, kStep));
+            s.late |= (y | z << 8) << (16 * x);
+          }
+          s.what = u.g[0] | u.g[1] << 8 | (u.kind == kShared ? 1 << 18 : 1 << 16 | (j < u.n[1] ? 1 << 17 : 0));
+          if (!(good = emit(&vmap, d2, true) && emit(&kmap, s, false))) break;
+          d2 = d1;
+          d1 = s;
+          if (!SELF) mbar_arrive_if(&B.want, lane == 0 && j == max(0, steps - 6));
+        }
+      }
+      good = good && emit(&vmap, d2, true) && emit(&vmap, d1, true);
+      if (good && lane == 0) {  // the late-row warps' end
+        B.late[late_n & (kLate - 1)] = {0, 0, -1, 0};
+        mbar_arrive(&B.late_full[late_n & (kLate - 1)]);
+      }
+      if (!good) {  // let the copies in flight land before the CTA leaves
+        for (int32_t q = max(0, used - kSlots); q < used; ++q)
+          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.kv_full[q % kSlots], (q / kSlots) & 1, 1000); ++x) {
+          }
+        for (int32_t q = max(0, late_n - kLate); q < late_n; ++q)
+          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.late_full[q % kLate], (q / kLate) & 1, 1000); ++x) {
+          }
+      }
+    } else if (warp == 2) {
+      // ============================================================== units
       int32_t ticket = blockIdx.x, total = 0;
       int32_t w_b = 0, w_i = 0, w_off = 0, w_left = 0;  // SELF: request, item, offset in it, what is left of the run
+      Request w_q{};
+      Shape w_h{};
       bool joins = false;
       if (SELF) {
         const int32_t c = blockIdx.x, W = B.workers;
@@ -694,16 +754,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           w_b = B.start_b;
           w_off = B.start_off;
           bool bad;
-          const Request q = request_of(p, w_b, bad);
-          const Shape h = shape_of(p, q.n);
-          if (h.ps > 0) {
-            const int32_t group = pairs_cost(p, q, h), g = min(p.Hkv, w_off / group);
+          w_q = request_of(p, w_b, bad);
+          w_h = shape_of(p, w_q.n);
+          if (w_h.ps > 0) {
+            const int32_t group = pairs_cost(p, w_q, w_h), g = min(p.Hkv, w_off / group);
             w_off -= g * group;
-            w_i = g * h.ps;
+            w_i = g * w_h.ps;
           }
 #pragma unroll 1
-          for (; w_i < h.items; ++w_i) {
-            const int32_t cost = run_cost(item_of(p, w_b, q, h, w_i));
+          for (; w_i < w_h.items; ++w_i) {
+            const int32_t cost = run_cost(item_of(p, w_b, w_q, w_h, w_i));
             if (w_off < cost) break;
             w_off -= cost;
           }
@@ -727,21 +787,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll 1
           while (w_left > 0 && w_b < p.B) {
-            bool bad;
-            const Request q = request_of(p, w_b, bad);
-            const Shape h = shape_of(p, q.n);
-            if (w_i >= h.items) {
-              ++w_b;
+            if (w_i >= w_h.items) {
               w_i = 0;
+              if (++w_b < p.B) {
+                bool bad;
+                w_q = request_of(p, w_b, bad);
+                w_h = shape_of(p, w_q.n);
+              }
               continue;
             }
-            const Item t = item_of(p, w_b, q, h, w_i);
+            const Item t = item_of(p, w_b, w_q, w_h, w_i);
             const int32_t a0 = w_off, cost = run_cost(t), a1 = min(cost, a0 + w_left), per = step_cost(t.kind);
             const int32_t s0 = min(t.cost, (a0 + per - 1) / per), s1 = min(t.cost, (a1 + per - 1) / per);
             const int32_t c = blockIdx.x, C = gridDim.x, row = 2 * p.tile_rows;
-            // where the item begins, from the run's end
-            const int64_t W = B.workers, all = B.total;
-            const int64_t begin = all * (c + 1) / W - w_left - a0;
             w_left -= a1 - a0;
             w_off = a1;
             if (a1 == cost) {
@@ -756,6 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               u = unit_of(t, s0, s1, (s0 == 0 ? C + c : c) * row);
               if (s0 > 0 && s1 == t.cost) {
+                // the CTA in whose run the item begins
+                const int64_t W = B.workers, all = B.total, begin = all * (c + 1) / W - w_left - a1;
                 int32_t c0 = max(0, min((int32_t)(begin * W / all), c));
                 while (c0 > 0 && all * c0 / W > begin) --c0;
                 while (c0 < c && all * (c0 + 1) / W <= begin) ++c0;
@@ -769,122 +829,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           return u;
         }
       };
-      int32_t k = 0;
-      int32_t page[2] = {0, 0}, ahead[2] = {0, 0};
-      // the pages of 32 steps from j on of a lane's run, one per thread
-      auto look_up = [&](const Unit& u, int x, int32_t j) {
-        const int32_t jj = j + lane, key = u.key0[x] + jj * kStep;
-        const bool has = jj < u.n[x] && key < u.seq;
-        int32_t at = has ? p.page_table[(int64_t)u.b * p.max_blocks + key / MSA_BLOCK_TOKENS] : 0;
-        const bool bad = at < 0 || at >= p.num_pages;
-        if (bad) at = 0;
-        if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
-        return at;
-      };
-      // Publishes the next unit and looks up its first pages.
-      auto publish = [&]() {
+      bool good = true;
+#pragma unroll 1
+      for (int32_t k = 0; good; ++k) {
+        // a listed unit is taken no earlier than needed, so that it goes to the CTA that is free first
+        if (!SELF && k > 0 && !(good = wait_or_fail(&B.want, (k - 1) & 1, fail))) break;
         const Unit u = next_unit();
         const int q = k & (kQueue - 1);
-        if (k >= kQueue && !wait_or_fail(&B.unit_free[q], (k / kQueue - 1) & 1, fail)) return false;
+        if (k >= kQueue && !(good = wait_or_fail(&B.unit_free[q], (k / kQueue - 1) & 1, fail))) break;
         if (lane == 0) {
           B.unit[q] = u;
           mbar_arrive(&B.unit_full[q]);
         }
         __syncwarp();
-        ++k;
-        ahead[0] = look_up(u, 0, 0);
-        ahead[1] = u.kind == kHalves ? look_up(u, 1, 0) : ahead[0];
-        return true;
-      };
-      Src d1, d2;
-      d1.what = d2.what = 0;
-      good = publish();
-#pragma unroll 1
-      while (good) {
-        Unit u;
-        {
-          const Unit& e = B.unit[(k - 1) & (kQueue - 1)];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            u.n[x] = uniform(e.n[x]);
-            u.key0[x] = uniform(e.key0[x]);
-            u.g[x] = uniform(e.g[x]);
-          }
-          u.kind = uniform(e.kind);
-          u.b = uniform(e.b);
-          u.pos = uniform(e.pos);
-          u.seq = uniform(e.seq);
-        }
-        const int32_t steps = u.n[0];
-        if (steps == 0) break;
-        page[0] = ahead[0];
-        page[1] = ahead[1];
-        const int32_t at = max(0, steps - 5);  // the ring is full by then: looking ahead costs nothing
-#pragma unroll 1
-        for (int32_t j = 0; j < steps; ++j) {
-          if (j > 0 && (j & 31) == 0) {
-            page[0] = look_up(u, 0, j);
-            page[1] = u.kind == kHalves ? look_up(u, 1, j) : page[0];
-          }
-          Src s;
-          s.late = 0;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int32_t key = u.key0[x] + j * kStep;
-            s.tok[x] = __shfl_sync(0xffffffffu, page[x], j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
-            const int32_t y = max(0, min(u.pos + 1 - key, kStep)), z = max(0, min(u.seq - key, kStep));
-            s.late |= (y | z << 8) << (16 * x);
-          }
-          s.what = u.g[0] | u.g[1] << 8 | (u.kind == kShared ? 1 << 18 : 1 << 16 | (j < u.n[1] ? 1 << 17 : 0));
-          if (!(good = emit(&vmap, d2, true) && emit(&kmap, s, false))) break;
-          d2 = d1;
-          d1 = s;
-          if (j == at && !(good = publish())) break;
-        }
+        if (u.n[0] == 0) break;  // the end of the list
       }
       if (SELF && lane < 2 && !joins) store_join(p.joins + 2 * blockIdx.x + lane, JoinTile{});
-      good = good && emit(&vmap, d2, true) && emit(&vmap, d1, true);
-      if (good && lane == 0) {  // the late-row warps' end
-        B.late[late_n & (kLate - 1)] = {0, 0, -1, 0};
-        mbar_arrive(&B.late_full[late_n & (kLate - 1)]);
-      }
-      if (!good) {  // let the copies in flight land before the CTA leaves
-        for (int32_t q = max(0, used - kSlots); q < used; ++q)
-          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.kv_full[q % kSlots], (q / kSlots) & 1, 1000); ++x) {
-          }
-        for (int32_t q = max(0, late_n - kLate); q < late_n; ++q)
-          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.late_full[q % kLate], (q / kLate) & 1, 1000); ++x) {
-          }
-      }
     } else if (warp == 1) {
       // ============================================================== query tiles
+      // Tiles of at most 64 rows alternate between the halves of the lane's area, so that the next one's rows
+      // are there before the current one's last S.
       int32_t k = 0, done[2] = {0, 0};
+      bool alone[2] = {true, true};  // the lane's last tile fills the area
       Unit u;
       bool good = true;
 #pragma unroll 1
       while (good && take(k, u) && (u.n[0] | u.n[1]) != 0) {
+        const bool small = is_small(u);
 #pragma unroll
         for (int X = 0; X < 2; ++X) {
           if (u.n[X] == 0) continue;
-          if (done[X] > 0 && !(good = wait_or_fail(&B.q_empty[X], (done[X] - 1) & 1, fail))) break;
+          // the tile whose S must have completed before this one's rows may be overwritten
+          const int32_t after = done[X] - (small && !alone[X] ? 2 : 1);
+          if (after >= 0 && !(good = wait_or_fail(&B.q_empty[X][after & 1], (after >> 1) & 1, fail))) break;
           if (lane == 0) {
             // one token's rows for a decode row: the others of the tile may hold anything
             const bool single = u.tokens == 1;
-            const CUtensorMap* map = single ? &qmap_1 : &qmap_t;
-            uint8_t* dst = smem + X * kQTile;
+            const CUtensorMap* map = single ? &qmap_1 : (small ? &qmap_h : &qmap_t);
+            uint64_t* full = &B.q_full[X][done[X] & 1];
+            uint8_t* dst = smem + X * kQTile + (small ? (done[X] & 1) * (kQHalf / 2) : 0);
             const int32_t row = u.row + (u.kind == kShared ? X * p.tpt : 0);
-            mbar_expect_tx(&B.q_full[X], (single ? p.G : 128) * 256);
-            tma_load_5d(dst, map, &B.q_full[X], 0, 0, row, 0, u.g[X]);
-            tma_load_5d(dst + kQHalf, map, &B.q_full[X], 0, 0, row, 1, u.g[X]);
+            mbar_expect_tx(full, (single ? p.G : (small ? 64 : 128)) * 256);
+            tma_load_5d(dst, map, full, 0, 0, row, 0, u.g[X]);
+            tma_load_5d(dst + kQHalf, map, full, 0, 0, row, 1, u.g[X]);
           }
           __syncwarp();
           ++done[X];
+          alone[X] = !small;
         }
       }
-      if (!good || *fail)
-        for (int X = 0; X < 2; ++X)  // let the copies in flight land before the CTA leaves
-          for (int x = 0; x < 1000 && done[X] > 0 && !mbar_try_wait_hint(&B.q_full[X], (done[X] - 1) & 1, 1000); ++x) {
-          }
+      if (!good || *fail)  // let the copies in flight land before the CTA leaves
+        for (int X = 0; X < 2; ++X)
+          for (int32_t q = max(0, done[X] - 2); q < done[X]; ++q)
+            for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.q_full[X][q & 1], (q >> 1) & 1, 1000); ++x) {
+            }
     }
     __syncwarp();
   } else if (warp >= 12) {
@@ -898,7 +896,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
       const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
       const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
-      const uint64_t qd = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
+      const uint64_t qd0 = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
+      uint64_t qd = qd0;
       const uint64_t kd0 = umma_desc_sw128(sbase + kOffRing, 16, 1024);
       const uint64_t vd0 = umma_desc_sw128(sbase + kOffRing, kKvHalf, 1024);
       constexpr uint32_t kMine = 1, kTwo = 2, kOpens = 4, kAny = 8;  // of a step
@@ -942,7 +941,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const RingPos at = (d & kTwo) && X ? r.after(1) : r;
               const uint32_t buf = n_s & 1;
               if (j == 0) {
-                if (!(good = wait_or_fail(&B.q_full[X], tiles & 1, fail))) break;
+                if (!(good = wait_or_fail(&B.q_full[X][tiles & 1], (tiles >> 1) & 1, fail))) break;
+                qd = qd0 + (is_small(u) ? (tiles & 1) * (kQHalf / 2 >> 4) : 0);
                 ++tiles;
               }
               if (!(good = wait_or_fail(&B.kv_full[at.slot], at.phase, fail))) break;
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               issue_s(s_tmem + buf * 64, qd + (kQHalf >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
               umma_commit_elect(&B.s_full[X][buf]);
               umma_commit_elect(&B.kv_empty[us]);
-              if (j == mine - 1) umma_commit_elect(&B.q_empty[X]);
+              if (j == mine - 1) umma_commit_elect(&B.q_empty[X][(tiles - 1) & 1]);
               ++n_s;
             }
             r.advance((d & kTwo) ? 2 : 1);
@@ -978,22 +978,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (e.slot < 0) break;  // no more
         const uint32_t at = sbase + kOffRing + e.slot * kKvTile + h * kKvHalf + (lane & 7) * 16;
         bool odd = false;
+        // lanes 8 i .. 8 i + 7: one row
 #pragma unroll 1
-        for (int32_t x0 = e.y & ~3; x0 < kStep; x0 += 16) {  // lanes 8 i .. 8 i + 7: one row
+        for (int32_t x = e.z + (lane >> 3); x < kStep; x += 4) st_shared_v4(at + x * 128, make_uint4(0, 0, 0, 0));
+#pragma unroll 1
+        for (int32_t x0 = e.y + (lane >> 3); x0 < e.z; x0 += 16) {
           uint4 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int32_t x = x0 + 4 * i + (lane >> 3);
-            if (x < kStep) v[i] = ld_shared_v4(at + x * 128);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (x0 + 4 * i < e.z) v[i] = ld_shared_v4(at + (x0 + 4 * i) * 128);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int32_t x = x0 + 4 * i + (lane >> 3);
-            if (x < e.y || x >= kStep) continue;
-            if (x >= e.z) {
-              st_shared_v4(at + x * 128, make_uint4(0, 0, 0, 0));
-              continue;
-            }
+            const int32_t x = x0 + 4 * i;
+            if (x >= e.z) continue;
             const uint4 f = make_uint4(finite_bf16x2(v[i].x), finite_bf16x2(v[i].y), finite_bf16x2(v[i].z),
                                        finite_bf16x2(v[i].w));
             if (f.x != v[i].x || f.y != v[i].y || f.z != v[i].z || f.w != v[i].w) {
@@ -1155,20 +1152,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.ml[part + row] = make_float2(m_run, l);
       }
       const bool odd = *(volatile int32_t*)&B.odd[X] != 0;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float o[64];
+      // Sixteen channels at a time, not unrolled: a tile's end comes too rarely to keep long code in the
+      // instruction caches.
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t raw[16];
         if (act) {
-          tmem_ld32(o_tmem + c * 64, o);
-          tmem_ld32(o_tmem + c * 64 + 32, o + 32);
+          tmem_ld16(o_tmem + c * 16, raw);
           tmem_wait_ld();
         }
-        if (c == 1) {  // all of O is read: the next unit may overwrite it
+        if (c == 7) {  // all of O is read: the next unit may overwrite it
           tmem_fence_before();
           __syncwarp();
           mbar_arrive_if(&B.o_free[X], lane == 0);
         }
         if (!mine) continue;
+        float o[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = __uint_as_float(raw[x]);
         if (odd) {
           // rare: what is not finite in V of the late keys that the row sees (their weights are above 0, so
           // it is added as it is)
@@ -1178,9 +1179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int32_t page = p.page_table[(int64_t)u.b * p.max_blocks + key / MSA_BLOCK_TOKENS];
             if (page < 0 || page >= p.num_pages) page = 0;
             const int64_t cell = (int64_t)page * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
-            const uint2* v = reinterpret_cast<const uint2*>(p.v_cache + (cell * p.Hkv + g) * 128 + c * 64);
+            const uint2* v = reinterpret_cast<const uint2*>(p.v_cache + (cell * p.Hkv + g) * 128 + c * 16);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
+            for (int x = 0; x < 4; ++x) {
               const uint2 w = v[x], f = make_uint2(finite_bf16x2(w.x), finite_bf16x2(w.y));
               if (f.x != w.x || f.y != w.y) {
                 o[4 * x] += bf16_lo(w.x ^ f.x);
@@ -1194,34 +1195,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (halves) {
           if (X == 1) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              __stcg(half + (c * 16 + x) * 128, make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+            for (int x = 0; x < 4; ++x)
+              __stcg(half + (c * 4 + x) * 128, make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
             continue;
           }
 #pragma unroll
-          for (int x = 0; x < 64; ++x) o[x] *= f0;
-          if (f1 != 0.f)
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float4 h = __ldcg(half + (c * 16 + x) * 128);
-              o[4 * x] = fmaf(h.x, f1, o[4 * x]);
-              o[4 * x + 1] = fmaf(h.y, f1, o[4 * x + 1]);
-              o[4 * x + 2] = fmaf(h.z, f1, o[4 * x + 2]);
-              o[4 * x + 3] = fmaf(h.w, f1, o[4 * x + 3]);
-            }
+          for (int x = 0; x < 4; ++x) {
+            const float4 h = f1 != 0.f ? __ldcg(half + (c * 4 + x) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[4 * x] = fmaf(h.x, f1, o[4 * x] * f0);
+            o[4 * x + 1] = fmaf(h.y, f1, o[4 * x + 1] * f0);
+            o[4 * x + 2] = fmaf(h.z, f1, o[4 * x + 2] * f0);
+            o[4 * x + 3] = fmaf(h.w, f1, o[4 * x + 3] * f0);
+          }
         }
         if (part < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + out * 128 + c * 64);
+          uint4* dst = reinterpret_cast<uint4*>(p.o + out * 128 + c * 16);
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
+          for (int x = 0; x < 2; ++x)
             dst[x] = make_uint4(pack_bf16x2(o[8 * x] * scale, o[8 * x + 1] * scale),
                                 pack_bf16x2(o[8 * x + 2] * scale, o[8 * x + 3] * scale),
                                 pack_bf16x2(o[8 * x + 4] * scale, o[8 * x + 5] * scale),
                                 pack_bf16x2(o[8 * x + 6] * scale, o[8 * x + 7] * scale));
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.po + (int64_t)part * 128) + (int64_t)c * 16 * cap + row;
+          float4* dst = reinterpret_cast<float4*>(p.po + (int64_t)part * 128) + (int64_t)c * 4 * cap + row;
 #pragma unroll
-          for (int x = 0; x < 16; ++x)
+          for (int x = 0; x < 4; ++x)
             dst[(int64_t)x * cap] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
       }
@@ -1394,8 +1392,8 @@ Layout layout_of(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_bloc
 }
 
 template <bool SELF>
-cudaError_t launch_kernels(const CUtensorMap& qt, const CUtensorMap& q1, const CUtensorMap& km, const CUtensorMap& vm,
-                           const KParams& p, cudaStream_t stream) {
+cudaError_t launch_kernels(const CUtensorMap& qt, const CUtensorMap& qh, const CUtensorMap& q1, const CUtensorMap& km,
+                           const CUtensorMap& vm, const KParams& p, cudaStream_t stream) {
   cudaError_t e;
   static std::atomic<int> regs{0};  // of the kernel as built: the register split counts on it
   if (regs.load(std::memory_order_relaxed) == 0) {
@@ -1426,7 +1424,7 @@ cudaError_t launch_kernels(const CUtensorMap& qt, const CUtensorMap& q1, const C
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   e = launch_with_smem(chunk_attention_kernel<SELF>, kSmemBytes, raised,
-                       [&] { return cudaLaunchKernelEx(&cfg, chunk_attention_kernel<SELF>, qt, q1, km, vm, p); });
+                       [&] { return cudaLaunchKernelEx(&cfg, chunk_attention_kernel<SELF>, qt, qh, q1, km, vm, p); });
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(2 * p.ctas));
   cfg.blockDim = dim3(kJoinThreads);
@@ -1476,19 +1474,21 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
   p.lse = a.lse;
   // query rows as (channel half, head of the group, token row, half, group): a box is G heads of
   // consecutive token rows, one 128-byte line each
-  CUtensorMap qt, q1, km, vm;
+  CUtensorMap qt, qh, q1, km, vm;
   const uint64_t qd[5] = {64, (uint64_t)G, (uint64_t)a.T, 2, (uint64_t)a.Hkv};
   const uint64_t qs[4] = {256, (uint64_t)a.q_stride * 2, 128, (uint64_t)G * 256};
   const uint32_t bt[5] = {64, (uint32_t)G, (uint32_t)p.tpt, 1, 1};
+  const uint32_t bh[5] = {64, (uint32_t)G, (uint32_t)p.tpt / 2, 1, 1};
   const uint32_t b1[5] = {64, (uint32_t)G, 1, 1, 1};
   // cache cells as (channel half, token, half, group): a box is both halves of 64 tokens
   const uint64_t kd[4] = {64, (uint64_t)a.num_pages * 128, 2, (uint64_t)a.Hkv};
   const uint64_t ks[3] = {(uint64_t)a.Hkv * 256, 128, 256};
   const uint32_t bk[4] = {64, kStep, 2, 1};
-  if (!encode_bf16_map(&qt, a.q, 5, qd, qs, bt, true) || !encode_bf16_map(&q1, a.q, 5, qd, qs, b1, true) ||
+  if (!encode_bf16_map(&qt, a.q, 5, qd, qs, bt, true) || !encode_bf16_map(&qh, a.q, 5, qd, qs, bh, true) ||
+      !encode_bf16_map(&q1, a.q, 5, qd, qs, b1, true) ||
       !encode_bf16_map(&km, a.k_cache, 4, kd, ks, bk, true) || !encode_bf16_map(&vm, a.v_cache, 4, kd, ks, bk, true))
     return cudaErrorInvalidValue;
-  return y.self ? launch_kernels<true>(qt, q1, km, vm, p, stream) : launch_kernels<false>(qt, q1, km, vm, p, stream);
+  return y.self ? launch_kernels<true>(qt, qh, q1, km, vm, p, stream) : launch_kernels<false>(qt, qh, q1, km, vm, p, stream);
 }
 
 }  // namespace msa
