@@ -44,7 +44,7 @@ namespace {
 
 constexpr int kThreads = 512;                    // warpgroups: loads, softmax x 2, MMA issue
 constexpr int kLaunchRegs = 128;                 // registers per thread at launch, then split
-constexpr int kRegsLoad = 64, kRegsIssue = 64, kRegsSoftmax = 192;
+constexpr int kRegsLoad = 56, kRegsIssue = 56, kRegsSoftmax = 200;
 static_assert(128 * (kRegsLoad + kRegsIssue) + 256 * kRegsSoftmax == kThreads * kLaunchRegs, "register split");
 constexpr int kStep = 64;                        // keys per step
 constexpr uint32_t kQHalf = 128 * 128;           // 128 rows x 64 channels bf16

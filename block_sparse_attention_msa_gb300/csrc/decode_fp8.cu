@@ -33,7 +33,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <climits>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -54,7 +53,9 @@ constexpr uint32_t kTile = kTok * 128;         // K or V of a step
 constexpr uint32_t kStep = 2 * kTile;
 constexpr uint32_t kRing = kStages * kStep;    // of one warp: 24 KB
 constexpr uint32_t kScales = 2 * kTok;         // bytes per step
-constexpr int kWin = 4;                        // register windows of 4 x 32 entries
+// A score may exceed the softmax's reference by this much (log2) before the reference moves: weights stay
+// below 2^8, far within fp16.
+constexpr float kFar = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -71,72 +72,27 @@ struct KParams {
   const int32_t* fpt;
   const int32_t* lens;
   int32_t Hkv, hs, G, topk;
-  int64_t rows, units, num_pages;  // rows = R*Hkv, units = rows*topk
+  int32_t rows, units;             // rows = R*Hkv, units = rows*topk
+  int64_t num_pages;
   float* part_o;                   // [rows, topk, G, 128]
   float* part_lse;                 // [rows, topk, G]
 };
 
-// A warp-uniform, forward-moving view of a 32-bit array through registers: lane l holds
-// a[base + 32*j + l]; reading an index past the window reloads it from that index.
+// A warp-uniform, forward-moving view of a 32-bit array: lane l holds a[base + l].
 struct RegWindow {
-  int64_t base;
-  int32_t val[kWin];
-  __device__ __forceinline__ int32_t get(const int32_t* a, int64_t n, int64_t i, int lane) {
-    if (i < base || i >= base + 32 * kWin) {
+  int32_t base = INT32_MIN / 2, val = 0;
+  __device__ __forceinline__ int32_t get(const int32_t* a, int32_t n, int32_t i, int lane) {
+    if (i >= base + 32) {
       base = i;
-#pragma unroll
-      for (int j = 0; j < kWin; ++j) {
-        const int64_t k = i + 32 * j + lane;
-        val[j] = k < n ? __ldg(a + k) : 0;
-      }
+      val = i + lane < n ? __ldg(a + i + lane) : 0;
     }
-    const int o = (int)(i - base), j = o >> 5;
-    int32_t x = val[0];
-#pragma unroll
-    for (int t = 1; t < kWin; ++t) x = j == t ? val[t] : x;
-    return __shfl_sync(0xffffffffu, x, o & 31);
+    return __shfl_sync(0xffffffffu, val, i - base);
   }
 };
 
-// A warp's walk over its unit range [u, u1): unit u = f*topk + pi is page pi of row f; pages past
-// the row's visible length are skipped; each page is ceil(tokens/32) steps c.
-struct Walk {
-  int64_t u, u1, f;
-  int len, npg, c, nc;
-  bool valid;
-  RegWindow lw;
-  __device__ __forceinline__ void start(int64_t u0, int64_t uend) {
-    u = u0 - 1;
-    u1 = uend;
-    f = -1;
-    len = npg = c = nc = 0;
-    lw.base = LLONG_MIN / 2;
-  }
-  __device__ __forceinline__ void advance(const KParams& p, int lane) {
-    if (++c < nc) return;
-    for (;;) {
-      ++u;
-      if (u >= u1) {
-        valid = false;
-        return;
-      }
-      const int64_t fu = u / p.topk;
-      if (fu != f) {
-        f = fu;
-        len = min(max(lw.get(p.lens, p.rows, fu, lane), 0), p.topk * MSA_BLOCK_TOKENS);
-        npg = (len + MSA_BLOCK_TOKENS - 1) / MSA_BLOCK_TOKENS;
-      }
-      const int pi = (int)(u - f * p.topk);
-      if (pi >= npg) {  // the rest of this row has no visible tokens
-        u = (f + 1) * p.topk - 1;
-        continue;
-      }
-      c = 0;
-      nc = (min(MSA_BLOCK_TOKENS, len - pi * MSA_BLOCK_TOKENS) + kTok - 1) / kTok;
-      valid = true;
-      return;
-    }
-  }
+// A step of a warp's walk: row, page slot (row * topk + page), first token and the row's visible tokens.
+struct Step {
+  int32_t f, slot, n0, len;  // f < 0: the walk is over
 };
 
 // e4m3 pairs as fp16 pairs, exactly.
@@ -179,24 +135,62 @@ __device__ __forceinline__ uint32_t lds8(uint32_t at) {
   return v;
 }
 
-// Brings the step's 32 tokens of K and V, and their scales, of virtual page v from token t0 on. An
-// invalid page id is recorded and replaced by page 0, group 0.
-__device__ __forceinline__ void load_step(uint8_t* dst, uint8_t* scales, uint64_t* full, const CUtensorMap& kmap,
-                                          const CUtensorMap& vmap, const KParams& p, int32_t v, int t0, int lane) {
-  int32_t page = v >> (7 + p.hs), g = v & ((MSA_BLOCK_TOKENS << p.hs) - 1);
-  if (v < 0 || page >= p.num_pages || g >= p.Hkv) {
-    if (lane == 0) msa_record_error(kErrBadPage);
-    page = g = 0;
+// Walks a warp's unit range [u, u1): unit u = f*topk + pi is page pi of row f; pages past the row's
+// visible length are skipped; each page is ceil(tokens/32) steps. next() brings the step's 32 tokens of K
+// and V, and their scales, into a stage. An invalid page id is recorded and read as page 0, group 0.
+struct Walk {
+  int32_t u, u1, f, pi, len, npg, c, nc, row;
+  RegWindow lens, pages;
+  __device__ __forceinline__ void start(const KParams& p, int32_t u0, int32_t uend, int lane) {
+    u = u0;
+    u1 = uend;
+    f = u0 / p.topk;
+    pi = u0 - f * p.topk;
+    c = nc = 0;
+    if (u < u1) {  // both round trips at once
+      (void)pages.get(p.fpt, p.units, u, lane);
+      len = min(max(lens.get(p.lens, p.rows, f, lane), 0), p.topk * MSA_BLOCK_TOKENS);
+    }
+    npg = (len + MSA_BLOCK_TOKENS - 1) / MSA_BLOCK_TOKENS;
   }
-  const int32_t row = ((page << p.hs) + g) * MSA_BLOCK_TOKENS + t0;
-  if (lane == 0) {
-    mbar_expect_tx(full, kStep + kScales);
-    tma_load_2d(dst, &kmap, full, 0, row);
-    tma_load_2d(dst + kTile, &vmap, full, 0, row);
-    bulk_load(scales, p.k_scale + row, kTok, full);
-    bulk_load(scales + kTok, p.v_scale + row, kTok, full);
+  __device__ __forceinline__ Step next(const KParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                       uint8_t* dst, uint8_t* scales, uint64_t* full, int lane) {
+    while (c >= nc) {
+      if (u >= u1) return {-1, 0, 0, 0};
+      if (pi == p.topk) {
+        pi = 0;
+        ++f;
+        len = min(max(lens.get(p.lens, p.rows, f, lane), 0), p.topk * MSA_BLOCK_TOKENS);
+        npg = (len + MSA_BLOCK_TOKENS - 1) / MSA_BLOCK_TOKENS;
+      }
+      if (pi >= npg) {  // the rest of this row has no visible tokens
+        u += p.topk - pi;
+        pi = p.topk;
+        continue;
+      }
+      const int32_t v = pages.get(p.fpt, p.units, u, lane);
+      int32_t page = v >> (7 + p.hs), g = v & ((MSA_BLOCK_TOKENS << p.hs) - 1);
+      if (v < 0 || page >= p.num_pages || g >= p.Hkv) {
+        if (lane == 0) msa_record_error(kErrBadPage);
+        page = g = 0;
+      }
+      row = ((page << p.hs) + g) * MSA_BLOCK_TOKENS;
+      c = 0;
+      nc = (min(MSA_BLOCK_TOKENS, len - pi * MSA_BLOCK_TOKENS) + kTok - 1) / kTok;
+      ++u;
+      ++pi;
+    }
+    if (lane == 0) {
+      const int32_t at = row + c * kTok;
+      mbar_expect_tx(full, kStep + kScales);
+      tma_load_2d(dst, &kmap, full, 0, at);
+      tma_load_2d(dst + kTile, &vmap, full, 0, at);
+      bulk_load(scales, p.k_scale + at, kTok, full);
+      bulk_load(scales + kTok, p.v_scale + at, kTok, full);
+    }
+    return {f, u - 1, (pi - 1) * MSA_BLOCK_TOKENS + c++ * kTok, len};
   }
-}
+};
 
 // What a row segment leaves in a lane, for HT tiles of 8 heads: heads 8 h + 2 tig + {0, 1}, channels
 // 16 chunk + 0..15 (chunk: 4 (gid & 1) + gid / 2), O relative to 2^M.
@@ -210,41 +204,31 @@ struct Seg {
 // emit(f, slot_row, seg) with l summed over the warp. False after a wait that gave up.
 template <int HT, class Emit>
 __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                           uint8_t* ring, Bars& bars, int warp, int64_t u0, int64_t u1, int lane,
+                                           uint8_t* ring, Bars& bars, int warp, int32_t u0, int32_t u1, int lane,
                                            Emit&& emit) {
   const int gid = lane >> 2, tig = lane & 3, G = p.G;
   const uint32_t base = smem_u32(ring), sbase = smem_u32(bars.scale[warp]);
   // The rows of an 8-row tile are the tokens perm(0..7) = 0, 4, 1, 5, 2, 6, 3, 7, and lane gid reads
   // chunk perm(gid) of V: eight lanes of a load then meet eight different 16-byte columns.
   const uint32_t perm = ((gid & 1) << 2) | (gid >> 1);
-  Walk cur, pf;
-  cur.start(u0, u1);
-  pf.start(u0, u1);
-  RegWindow vw;
-  vw.base = LLONG_MIN / 2;
-  // the range's first page ids are requested before the row lengths that the walk needs first, so the
-  // two round trips overlap
-  if (u0 < u1) (void)vw.get(p.fpt, p.units, u0, lane);
-  cur.advance(p, lane);
-  pf.advance(p, lane);
+  Walk walk;
+  walk.start(p, u0, u1, lane);
   uint32_t issued = 0;
   auto prefetch = [&]() {
-    if (!pf.valid) return;
-    const int32_t v = vw.get(p.fpt, p.units, pf.u, lane);
     const uint32_t s = issued % kStages;
-    load_step(ring + s * kStep, bars.scale[warp][s], &bars.full[warp][s], kmap, vmap, p, v, pf.c * kTok, lane);
-    ++issued;
-    pf.advance(p, lane);
+    const Step x = walk.next(p, kmap, vmap, ring + s * kStep, bars.scale[warp][s], &bars.full[warp][s], lane);
+    issued += x.f >= 0;
+    return x;
   };
-#pragma unroll 1
-  for (int k = 0; k < kStages - 1; ++k) prefetch();
+  Step ahead[kStages - 1];
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) ahead[k] = prefetch();
 
   uint32_t it = 0;
 #pragma unroll 1
-  while (cur.valid) {
-    // ---- a row segment: row f from unit cur.u on
-    const int64_t f = cur.f, slot_row = cur.u;
-    const int len = cur.len;
+  while (ahead[0].f >= 0) {
+    // ---- a row segment
+    const int32_t f = ahead[0].f, slot_row = ahead[0].slot, len = ahead[0].len;
     // Q^T fragments (K index 16 x heads): k-step ks takes channels 64 (ks / 4) + 16 tig + 4 (ks % 4) + 0..3
     // of head 8 h + gid
     uint32_t qb[HT][8][2];
@@ -257,7 +241,7 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
       for (int x = 0; x < 4; ++x) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (head < G)
-          v = __ldg(reinterpret_cast<const uint4*>(p.q + (f * G + head) * 128 + (x >> 1) * 64 + tig * 16) + (x & 1));
+          v = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)f * G + head) * 128 + (x >> 1) * 64 + tig * 16) + (x & 1));
         w[4 * x] = v.x;
         w[4 * x + 1] = v.y;
         w[4 * x + 2] = v.z;
@@ -297,7 +281,11 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
 
 #pragma unroll 1
     do {
-      prefetch();  // into the stage that step it - 1 used
+      const int n0 = ahead[0].n0;
+      // the next step goes into the stage that the last one used
+#pragma unroll
+      for (int k = 0; k + 1 < kStages - 1; ++k) ahead[k] = ahead[k + 1];
+      ahead[kStages - 2] = prefetch();
       const uint32_t st = it % kStages;
       if (!mbar_wait(&bars.full[warp][st], (it / kStages) & 1)) {
         if (lane == 0) msa_record_error(kErrTimeout);
@@ -328,7 +316,6 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
         }
       }
       // ---- softmax statistics: token 16 mt + 8 r + perm, heads 2 tig + y
-      const int n0 = (int)(cur.u - f * p.topk) * MSA_BLOCK_TOKENS + cur.c * kTok;
       float ks[2][2], vs[2][2];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
@@ -356,31 +343,37 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
             mx[y] = fmaxf(mx[y], t);
             Mx[y] = fmaxf(Mx[y], w[mt][c]);
           }
+        // Any references near the maxima serve, so they move only when a score lies far above them.
+        bool far = false;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1)
+        for (int y = 0; y < 2; ++y) far |= mx[y] > s.m[h][y] + kFar || Mx[y] > s.M[h][y] + kFar;
+        if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
+              Mx[y] = fmaxf(Mx[y], __shfl_xor_sync(0xffffffffu, Mx[y], o));
+            }
+          float fo[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
-            Mx[y] = fmaxf(Mx[y], __shfl_xor_sync(0xffffffffu, Mx[y], o));
+            const float mn = fmaxf(s.m[h][y], mx[y]), Mn = fmaxf(s.M[h][y], Mx[y]);
+            s.l[h][y] *= mn == -INFINITY ? 1.f : ex2(s.m[h][y] - mn);
+            fo[y] = Mn == -INFINITY ? 1.f : ex2(s.M[h][y] - Mn);
+            s.m[h][y] = mn;
+            s.M[h][y] = Mn;
           }
-        float mref[2], Mref[2], fo[2];
-        bool moved = false;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float mn = fmaxf(s.m[h][y], mx[y]), Mn = fmaxf(s.M[h][y], Mx[y]);
-          mref[y] = mn == -INFINITY ? 0.f : mn;
-          Mref[y] = Mn == -INFINITY ? 0.f : Mn;
-          s.l[h][y] *= ex2(s.m[h][y] - mref[y]);
-          fo[y] = ex2(s.M[h][y] - Mref[y]);
-          moved |= Mn != s.M[h][y];
-          s.m[h][y] = mn;
-          s.M[h][y] = Mn;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
 #pragma unroll
             for (int c = 0; c < 4; ++c) s.o[h][x][c] *= fo[c & 1];
+        }
+        float mref[2], Mref[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          mref[y] = s.m[h][y] == -INFINITY ? 0.f : s.m[h][y];
+          Mref[y] = s.M[h][y] == -INFINITY ? 0.f : s.M[h][y];
         }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
@@ -422,8 +415,7 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
       }
       __syncwarp();  // every lane is done with the stage before it is refilled
       ++it;
-      cur.advance(p, lane);
-    } while (cur.valid && cur.f == f);
+    } while (ahead[0].f == f);
 
     // ---- the segment's sums over the lanes that hold the same heads
 #pragma unroll
@@ -479,13 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.G;
   const int64_t nw = (int64_t)gridDim.x * kWarps, wg = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t u0 = p.units * wg / nw, u1 = p.units * (wg + 1) / nw;
+  const int32_t u0 = (int32_t)(p.units * wg / nw), u1 = (int32_t)(p.units * (wg + 1) / nw);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // every slot of the range starts empty; a row segment's partial overwrites its first slot
-  for (int64_t i = u0 * G + lane; i < u1 * G; i += 32) p.part_lse[i] = -INFINITY;
+  for (int64_t i = (int64_t)u0 * G + lane; i < (int64_t)u1 * G; i += 32) p.part_lse[i] = -INFINITY;
   __syncwarp();
   walk_units<HT>(p, kmap, vmap, smem + warp * kRing, *bars, warp, u0, u1, lane,
-                 [&](int64_t, int64_t slot_row, const Seg<HT>& s) {
-                   store_partial<HT>(p.part_o + slot_row * G * 128, p.part_lse + slot_row * G, s, G, lane);
+                 [&](int32_t, int32_t slot_row, const Seg<HT>& s) {
+                   store_partial<HT>(p.part_o + (int64_t)slot_row * G * 128, p.part_lse + (int64_t)slot_row * G, s, G, lane);
                  });
 }
 
@@ -510,14 +504,16 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads,
   const int G = p.G;
   constexpr int kParts = kClusterCtas * kWarps;
   const int wi = rank * kWarps + warp;
-  const int64_t u0 = f * p.topk + (int64_t)p.topk * wi / kParts;
-  const int64_t u1 = f * p.topk + (int64_t)p.topk * (wi + 1) / kParts;
+  const int32_t u0 = (int32_t)(f * p.topk) + p.topk * wi / kParts;
+  const int32_t u1 = (int32_t)(f * p.topk) + p.topk * (wi + 1) / kParts;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // a warp's partial, once its walk is over: O [G][128] fp32, then its G LSEs
   float* part = reinterpret_cast<float*>(smem + warp * kRing);
   float* part_lse = part + 16 * 128;
   bool emitted = false;
   const bool good = walk_units<HT>(p, kmap, vmap, smem + warp * kRing, *bars, warp, u0, u1, lane,
-                                   [&](int64_t, int64_t, const Seg<HT>& s) {
+                                   [&](int32_t, int32_t, const Seg<HT>& s) {
                                      __syncwarp();  // the ring's last step is read: it becomes the partial's space
                                      store_partial<HT>(part, part_lse, s, G, lane);
                                      emitted = true;
@@ -565,9 +561,10 @@ __global__ void __launch_bounds__(kThreads) decode_fp8_merge_kernel(const __grid
                                                                     uint16_t* __restrict__ o_out,
                                                                     float* __restrict__ lse_out) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;  // row * G + head
-  if (item >= p.rows * p.G) return;
+  if (item >= (int64_t)p.rows * p.G) return;
   const int64_t f = item / p.G;
   const int e = (int)(item - f * p.G);
   float l[2], w[2];
@@ -614,11 +611,17 @@ __global__ void __launch_bounds__(kThreads) decode_fp8_merge_kernel(const __grid
 template <int HT>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const KParams& p, const DecodeFp8Args& a,
                    cudaStream_t stream) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  if (p.rows * kClusterCtas <= sm_count()) {  // few rows: one cluster per row, no partial in HBM, no merge kernel
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const int sms = sm_count();
+  if ((int64_t)p.rows * kClusterCtas <= sms) {  // few rows: one cluster per row, no partial in HBM, no merge kernel
     static std::atomic<size_t> raised[kMaxDevices];
     cfg.gridDim = dim3((unsigned)(p.rows * kClusterCtas));
     return launch_with_smem(paged_decode_fp8_cluster_kernel<HT>, kSmemBytes, raised, [&] {
@@ -626,17 +629,12 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const KPara
     });
   }
   static std::atomic<size_t> raised[kMaxDevices];
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>((p.units + kWarps - 1) / kWarps, sm_count()));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(((int64_t)p.units + kWarps - 1) / kWarps, sms));
   cudaError_t e = launch_with_smem(paged_decode_fp8_kernel<HT>, kSmemBytes, raised, [&] {
     return cudaLaunchKernelEx(&cfg, paged_decode_fp8_kernel<HT>, kmap, vmap, p);
   });
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)((p.rows * p.G + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3((unsigned)(((int64_t)p.rows * p.G + kWarps - 1) / kWarps));
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, decode_fp8_merge_kernel, p, a.o, a.lse);
   if (e != cudaSuccess) cudaGetLastError();
@@ -656,7 +654,7 @@ cudaError_t launch_paged_decode_fp8(const DecodeFp8Args& a, cudaStream_t stream)
   while ((1 << p.hs) < a.Hkv) ++p.hs;
   p.G = a.Hq / a.Hkv;
   p.topk = a.topk;
-  p.rows = (int64_t)a.R * a.Hkv;
+  p.rows = a.R * a.Hkv;
   p.units = p.rows * a.topk;
   p.num_pages = a.num_pages;
   p.part_o = a.part_o;
