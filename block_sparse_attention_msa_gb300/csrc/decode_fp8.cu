@@ -18,7 +18,9 @@
 // few instructions per byte.
 //  * A page of a group is 16 KB in one piece in this cache ([page][group][token][channel]), so a warp
 //    brings a step of 32 tokens (4 KB of K, 4 KB of V, 64 scales) with four bulk copies into its own
-//    3-stage ring, two steps ahead, and waits on its own barrier: no warp waits for another.
+//    ring, a step ahead, and waits on its own barrier: no warp waits for another. (Two stages of 8 KB
+//    in each of eight warps keep 64 KB a SM in flight beside what is worked on; three were slower, 55.9
+//    instead of 53.2 us, and so were ten or twelve warps, 56.7.)
 //  * The tokens are the M side of the MMAs (16 of them), the group's heads the N side (8, or two tiles
 //    of 8): S^T = K Q^T and O^T = V^T P^T, so 8 heads fill their tile (as the 16-row side they would be
 //    half of it: twice the MMAs, conversions alike). P^T goes from accumulator to operand layout by
@@ -47,11 +49,11 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kTok = 32;                       // tokens per step
 constexpr uint32_t kTile = kTok * 128;         // K or V of a step
 constexpr uint32_t kStep = 2 * kTile;
-constexpr uint32_t kRing = kStages * kStep;    // of one warp: 24 KB
+constexpr uint32_t kRing = kStages * kStep;    // of one warp: 16 KB
 constexpr uint32_t kScales = 2 * kTok;         // bytes per step
 // A score may exceed the softmax's reference by this much (log2) before the reference moves: weights stay
 // below 2^8, far within fp16.
@@ -61,8 +63,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct Bars {
   uint64_t full[kWarps][kStages];
-  uint8_t scale[kWarps][kStages][kScales];  // K, V; 64-byte lines: 16-byte aligned bulk copies
+  alignas(128) uint8_t scale[kWarps][kStages][kScales];  // K, V; 64-byte lines: 16-byte aligned bulk copies
 };
+static_assert(kTile % 1024 == 0 && kTok % 16 == 0, "alignment of the copies' targets");
 constexpr size_t kSmemBytes = 1024 + kWarps * kRing + sizeof(Bars);
 
 struct KParams {
@@ -486,10 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Few rows (a small batch at long context): a cluster of kClusterCtas CTAs per flattened row, as in the
 // bf16 form: its warps split the row's pages, leave their partials in their own ring, and the
 // cluster's CTAs merge a share of the row's outputs each through distributed shared memory.
-constexpr int kClusterCtas = 4;
+constexpr int kClusterCtas = 4, kClusterWarps = 8, kClusterThreads = kClusterWarps * 32;
+static_assert(kClusterWarps <= kWarps, "their rings fit");
 
 template <int HT>
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads, 1)
     paged_decode_fp8_cluster_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                     const __grid_constant__ KParams p, uint16_t* __restrict__ o_out,
                                     float* __restrict__ lse_out) {
@@ -502,8 +506,8 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads,
   const int rank = (int)cluster.block_rank();
   const int64_t f = blockIdx.x / kClusterCtas;  // flattened row (request, group)
   const int G = p.G;
-  constexpr int kParts = kClusterCtas * kWarps;
-  const int wi = rank * kWarps + warp;
+  constexpr int kParts = kClusterCtas * kClusterWarps;
+  const int wi = rank * kClusterWarps + warp;
   const int32_t u0 = (int32_t)(f * p.topk) + p.topk * wi / kParts;
   const int32_t u1 = (int32_t)(f * p.topk) + p.topk * (wi + 1) / kParts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -527,9 +531,9 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads,
   // empty range), kept in this CTA (behind warp 0's partial, which stays readable)
   float* wts = reinterpret_cast<float*>(smem + 12 * 1024);
   static_assert(kParts == 32, "one lane per partial");
-  for (int h = warp; h < G; h += kWarps) {
+  for (int h = warp; h < G; h += kClusterWarps) {
     const float* pl = cluster.map_shared_rank(
-        reinterpret_cast<float*>(smem + (lane % kWarps) * kRing) + 16 * 128, lane / kWarps);
+        reinterpret_cast<float*>(smem + (lane % kClusterWarps) * kRing) + 16 * 128, lane / kClusterWarps);
     const float l = pl[h];
     const float m = warp_max(l);
     const float e = (m == -INFINITY || l == -INFINITY) ? 0.f : __expf(l - m);
@@ -540,13 +544,13 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads,
   }
   __syncthreads();
   // (head, channel) outputs of the row, dealt over the cluster's threads: 32 independent remote loads each
-  for (int item = rank * kThreads + (int)threadIdx.x; item < G * 128; item += kClusterCtas * kThreads) {
+  for (int item = rank * kClusterThreads + (int)threadIdx.x; item < G * 128; item += kClusterCtas * kClusterThreads) {
     const int h = item >> 7, ch = item & 127;
     float acc = 0.f;
 #pragma unroll
     for (int j = 0; j < kParts; ++j) {
       const float* pj =
-          cluster.map_shared_rank(reinterpret_cast<float*>(smem + (j % kWarps) * kRing), j / kWarps);
+          cluster.map_shared_rank(reinterpret_cast<float*>(smem + (j % kClusterWarps) * kRing), j / kClusterWarps);
       acc = fmaf(wts[h * 32 + j], pj[h * 128 + ch], acc);
     }
     o_out[(f * G + h) * 128 + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(acc));
@@ -555,34 +559,39 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads,
 }
 
 // Joins the partials of a flattened row's slots, in their order: a warp per (row, head). Lane j weighs
-// slots j and j + 32 (at most 64 of them); the partials that carry weight then stream sixteen at a time,
-// all their loads in flight, four channels a lane.
-__global__ void __launch_bounds__(kThreads) decode_fp8_merge_kernel(const __grid_constant__ KParams p,
-                                                                    uint16_t* __restrict__ o_out,
-                                                                    float* __restrict__ lse_out) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+// slots j and j + 32 (at most 64 of them); the partials that carry weight then stream four at a time, all
+// their loads in flight, four channels a lane. Few registers, so that its CTAs stand beside the attention
+// kernel's and wait there.
+constexpr int kMergeWarps = 4;
+__global__ void __launch_bounds__(kMergeWarps * 32, 12) decode_fp8_merge_kernel(const __grid_constant__ KParams p,
+                                                                                uint16_t* __restrict__ o_out,
+                                                                                float* __restrict__ lse_out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + warp;  // row * G + head
-  if (item >= (int64_t)p.rows * p.G) return;
+  const int64_t item = (int64_t)blockIdx.x * kMergeWarps + warp;  // row * G + head
+  const bool mine = item < (int64_t)p.rows * p.G;
   const int64_t f = item / p.G;
   const int e = (int)(item - f * p.G);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!mine) return;
+  const float* lse = p.part_lse + f * p.topk * p.G + e;
+  const float4* part = reinterpret_cast<const float4*>(p.part_o + (f * p.topk * p.G + e) * 128) + lane;
   float l[2], w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int s = lane + 32 * h;
-    l[h] = s < p.topk ? __ldcs(p.part_lse + (f * p.topk + s) * p.G + e) : -INFINITY;
+    l[h] = s < p.topk ? __ldcs(lse + s * p.G) : -INFINITY;
   }
   const float m = warp_max(fmaxf(l[0], l[1]));
 #pragma unroll
   for (int h = 0; h < 2; ++h) w[h] = l[h] == -INFINITY ? 0.f : ex2((l[h] - m) * kLog2e);
-  const float total = warp_sum(w[0] + w[1]);
   // slots with a partial; a NaN among them reaches the output
-  uint64_t rest = (uint64_t)__ballot_sync(0xffffffffu, w[0] != 0.f) |
-                  ((uint64_t)__ballot_sync(0xffffffffu, w[1] != 0.f) << 32);
+  uint64_t rest = (uint64_t)__ballot_sync(0xffffffffu, l[0] != -INFINITY) |
+                  ((uint64_t)__ballot_sync(0xffffffffu, l[1] != -INFINITY) << 32);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
   while (rest) {
-    constexpr int kBatch = 16;
+    constexpr int kBatch = 4;
     float wk[kBatch];
     float4 v[kBatch];
 #pragma unroll
@@ -590,9 +599,9 @@ __global__ void __launch_bounds__(kThreads) decode_fp8_merge_kernel(const __grid
       const int s = rest ? __ffsll((long long)rest) - 1 : -1;
       rest &= rest - 1;
       wk[k] = __shfl_sync(0xffffffffu, s >= 32 ? w[1] : w[0], s & 31);
-      if (s < 0) wk[k] = 0.f;
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s >= 0) v[k] = __ldcs(reinterpret_cast<const float4*>(p.part_o + ((f * p.topk + s) * p.G + e) * 128) + lane);
+      if (s >= 0) v[k] = __ldcs(part + (int64_t)s * p.G * 32);
+      else wk[k] = 0.f;
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -602,6 +611,7 @@ __global__ void __launch_bounds__(kThreads) decode_fp8_merge_kernel(const __grid
       acc[3] = fmaf(wk[k], v[k].w, acc[3]);
     }
   }
+  const float total = warp_sum(w[0] + w[1]);
   const float inv = total == 0.f ? 0.f : 1.0f / total;
   *reinterpret_cast<uint2*>(o_out + item * 128 + lane * 4) =
       make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -624,6 +634,7 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const KPara
   if ((int64_t)p.rows * kClusterCtas <= sms) {  // few rows: one cluster per row, no partial in HBM, no merge kernel
     static std::atomic<size_t> raised[kMaxDevices];
     cfg.gridDim = dim3((unsigned)(p.rows * kClusterCtas));
+    cfg.blockDim = dim3(kClusterThreads);
     return launch_with_smem(paged_decode_fp8_cluster_kernel<HT>, kSmemBytes, raised, [&] {
       return cudaLaunchKernelEx(&cfg, paged_decode_fp8_cluster_kernel<HT>, kmap, vmap, p, a.o, a.lse);
     });
@@ -634,7 +645,8 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const KPara
     return cudaLaunchKernelEx(&cfg, paged_decode_fp8_kernel<HT>, kmap, vmap, p);
   });
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(((int64_t)p.rows * p.G + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3((unsigned)(((int64_t)p.rows * p.G + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, decode_fp8_merge_kernel, p, a.o, a.lse);
   if (e != cudaSuccess) cudaGetLastError();
