@@ -12,6 +12,11 @@
 // Both kernels copy: 385 bytes a row move either way, so HBM bounds long runs and the launch bounds
 // decode steps. Eight threads own a row, 16 channels each (two 16-byte loads of bf16, one 16-byte
 // store of e4m3, or the reverse); a row's largest magnitude takes three shuffles on packed bit patterns.
+// The 32 bytes of bf16 move in one access where they are aligned: two 16-byte stores half a sector each
+// cost the read-back a fifth of its rate (4.5 instead of 5.2 TB/s). Measured, replayed from a graph, Hkv 8:
+// 60032 rows read back in 56.5 us (370 MB, 6.5 TB/s, 96% of a copy), 32768 rows written and read back in
+// 64 us (404 MB, 6.3 TB/s), 8 rows in 4.1 us. Two rows of a thread: one 62.8 and 67.8 us, four 57.6 and
+// 64.7 us; a persistent grid 70.5 us for the first.
 #include "common.cuh"
 #include "host_util.h"
 #include "kernels.h"
@@ -22,8 +27,8 @@ namespace msa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // rows of a thread, all requested before the first store
+constexpr int kThreads = 128;
+constexpr int kUnroll = 2;  // rows of a thread, all requested before the first store
 
 struct QuantParams {
   const uint16_t* src[2];  // K, V rows
@@ -63,30 +68,55 @@ __device__ __forceinline__ float f16_hi(uint32_t x) {
 // NaN in the place of what is not finite, which e4m3 holds as NaN (it has no infinity).
 __device__ __forceinline__ float nan_or(float x) { return fabsf(x) <= 3.4028235e38f ? x : __int_as_float(0x7fffffff); }
 
+// 32 bytes in one access where the address allows it (WIDE), else in two.
+template <bool WIDE>
+__device__ __forceinline__ void load32(const uint4* at, uint32_t (&w)[8]) {
+  if constexpr (WIDE) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(at)
+                 : "memory");
+  } else {
+    const uint4 a = __ldcs(at), b = __ldcs(at + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store32(uint4* at, const uint32_t (&w)[8]) {
+  if constexpr (WIDE) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    __stcs(at, make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(at + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
+
 // (token, group) row `i` of a tensor of T << hs rows; eight lanes per row, c = channels 16 c .. + 15.
+template <bool WIDE>
 __global__ void __launch_bounds__(kThreads) append_kv_fp8_kernel(const __grid_constant__ QuantParams p) {
   const int x = blockIdx.y, c = threadIdx.x & 7;
   const int64_t rows = (int64_t)p.T << p.hs;
   const int64_t base = (int64_t)blockIdx.x * (kThreads / 8 * kUnroll) + (threadIdx.x >> 3);
   const uint16_t* src = p.src[x];
-  uint4 v[kUnroll][2];
+  uint32_t v[kUnroll][8];
   int32_t slot[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t i = base + u * (kThreads / 8), t = i >> p.hs;
     slot[u] = -1;
-    v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[u][k] = 0;
     if (i < rows) {
       slot[u] = p.slots[t];
-      const uint4* s = reinterpret_cast<const uint4*>(src + t * p.src_stride[x] + (i - (t << p.hs)) * 128) + 2 * c;
-      v[u][0] = __ldcs(s);
-      v[u][1] = __ldcs(s + 1);
+      load32<WIDE>(reinterpret_cast<const uint4*>(src + t * p.src_stride[x] + (i - (t << p.hs)) * 128) + 2 * c, v[u]);
     }
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t i = base + u * (kThreads / 8);
-    const uint32_t w[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+    const uint32_t(&w)[8] = v[u];
     uint32_t m2 = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m2 = max_mag2(m2, w[k]);
@@ -138,6 +168,7 @@ struct GatherParams {
   int64_t cells;
 };
 
+template <bool WIDE>
 __global__ void __launch_bounds__(kThreads) gather_kv_fp8_kernel(const __grid_constant__ GatherParams p) {
   const int x = blockIdx.y, c = threadIdx.x & 7;
   const int64_t rows = (int64_t)p.T << p.hs;
@@ -176,9 +207,7 @@ __global__ void __launch_bounds__(kThreads) gather_kv_fp8_kernel(const __grid_co
       r[2 * k] = pack_bf16x2(f16_lo(lo) * f, f16_hi(lo) * f);
       r[2 * k + 1] = pack_bf16x2(f16_lo(hi) * f, f16_hi(hi) * f);
     }
-    uint4* d = reinterpret_cast<uint4*>(p.dst[x] + i * 128) + 2 * c;
-    __stcs(d, make_uint4(r[0], r[1], r[2], r[3]));
-    __stcs(d + 1, make_uint4(r[4], r[5], r[6], r[7]));
+    store32<WIDE>(reinterpret_cast<uint4*>(p.dst[x] + i * 128) + 2 * c, r);
   }
 }
 
@@ -188,11 +217,12 @@ int32_t log2_of(int32_t x) {
   return s;
 }
 
+// K and V side by side.
 template <class P>
 cudaError_t launch_rows(void (*kernel)(P), const P& p, int64_t rows, cudaStream_t stream) {
   constexpr int64_t per = kThreads / 8 * kUnroll;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows + per - 1) / per), 2);  // K and V
+  cfg.gridDim = dim3((unsigned)((rows + per - 1) / per), 2);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   // the launch's own status: the thread's last error may be an older call's
@@ -217,7 +247,10 @@ cudaError_t launch_append_kv_fp8(const AppendFp8Args& a, cudaStream_t stream) {
   p.T = a.T;
   p.hs = log2_of(a.Hkv);
   p.cells = a.num_pages * MSA_BLOCK_TOKENS;
-  return launch_rows(append_kv_fp8_kernel, p, (int64_t)a.T * a.Hkv, stream);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                         (uintptr_t)(a.k_stride * 2) | (uintptr_t)(a.v_stride * 2);
+  return launch_rows((bits & 31) == 0 ? append_kv_fp8_kernel<true> : append_kv_fp8_kernel<false>, p,
+                     (int64_t)a.T * a.Hkv, stream);
 }
 
 cudaError_t launch_gather_kv_fp8(const GatherFp8Args& a, cudaStream_t stream) {
@@ -232,7 +265,9 @@ cudaError_t launch_gather_kv_fp8(const GatherFp8Args& a, cudaStream_t stream) {
   p.T = a.T;
   p.hs = log2_of(a.Hkv);
   p.cells = a.num_pages * MSA_BLOCK_TOKENS;
-  return launch_rows(gather_kv_fp8_kernel, p, (int64_t)a.T * a.Hkv, stream);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+  return launch_rows((bits & 31) == 0 ? gather_kv_fp8_kernel<true> : gather_kv_fp8_kernel<false>, p,
+                     (int64_t)a.T * a.Hkv, stream);
 }
 
 }  // namespace msa
