@@ -51,9 +51,9 @@ constexpr uint32_t kQHalf = 128 * 128;           // 128 rows x 64 channels bf16
 constexpr uint32_t kQTile = 2 * kQHalf;
 constexpr uint32_t kKvHalf = kStep * 128;        // 64 keys x 64 channels bf16
 constexpr uint32_t kKvTile = 2 * kKvHalf;        // K or V of one step: 16 KB, one slot of the ring
-constexpr int kSlots = 10;
-constexpr uint32_t kOffRing = 2 * kQTile;
-constexpr uint32_t kOffBar = kOffRing + kSlots * kKvTile;
+constexpr int kSlots = 5;                        // of K, and of V
+constexpr uint32_t kOffK = 2 * kQTile, kOffV = kOffK + kSlots * kKvTile;
+constexpr uint32_t kOffBar = kOffV + kSlots * kKvTile;
 constexpr uint32_t kTmemCols = 512;              // S buffers of lane X at 128 X, O at 256 + 128 X
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -382,7 +382,7 @@ static_assert(kLate > kSlots + 1, "an entry is not overwritten while it is open"
 constexpr int kQueue = 4;  // units that the feeder is ahead of the slowest reader at most
 
 struct Bars {
-  uint64_t kv_full[kSlots], kv_empty[kSlots];
+  uint64_t kv_full[2][kSlots], kv_empty[2][kSlots];  // K, V
   uint64_t q_full[2][2], q_empty[2][2];  // [lane][the lane's tile & 1]
   uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // [lane][the lane's step & 1]
   uint64_t o_free[2];
@@ -431,11 +431,9 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, vol
   *fail = 1;
   return false;
 }
-// wait_or_fail for two barriers at once: half of the warp tests either.
-__device__ __forceinline__ bool wait_two_or_fail(uint64_t* bar0, uint32_t par0, uint64_t* bar1, uint32_t par1,
-                                                 volatile int32_t* fail) {
-  const bool lo = (threadIdx.x & 16) == 0;
-  const uint32_t bar = smem_u32(lo ? bar0 : bar1), par = lo ? par0 : par1;
+// wait_or_fail for several barriers at once: each thread tests one (a completed wait takes 125 cycles).
+__device__ __forceinline__ bool wait_all_or_fail(uint64_t* mine, uint32_t par, volatile int32_t* fail) {
+  const uint32_t bar = smem_u32(mine);
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait_addr(bar, par))) return true;
     if (__any_sync(0xffffffffu, *fail != 0)) return false;
@@ -515,10 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 64) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&B.kv_full[i], 2);   // the producer twice, or the two late-row warps
-      mbar_init(&B.kv_empty[i], 2);  // both issuers, or one and the producer
-    }
+    for (int i = 0; i < kSlots; ++i)
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&B.kv_full[x][i], 2);   // the producer twice, or the two late-row warps
+        mbar_init(&B.kv_empty[x][i], 2);  // both issuers
+      }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&B.o_free[x], 4);
       mbar_init(&B.drained[x], 1);
@@ -532,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&B.unit_full[i], 1);
-      mbar_init(&B.unit_free[i], 12);  // readers: eight softmax warps, two issuers, the K/V and query loaders
+      mbar_init(&B.unit_free[i], 13);  // readers: eight softmax warps, two issuers, the K, V and query loaders
     }
     for (int i = 0; i < kLate; ++i) mbar_init(&B.late_full[i], 1);
     mbar_init(&B.want, 1);
@@ -640,28 +639,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
-    if (warp == 0) {
-      // ============================================================== K/V
-      // Loads the units' keys and values in the order in which the MMAs use them: V(i - 2), K(i) for each
-      // step i of the CTA's steps, a unit's behind the other's. A step of lanes with keys of their own has
-      // two slots for each.
+    if (warp == 0 || warp == 3) {
+      // ============================================================== K, V
+      // Warp 0 loads the units' keys and warp 3 their values, a unit's steps behind the other's; a slot takes
+      // a producer some 700 cycles, so one for both was what bounded the kernel. A step of lanes with keys of
+      // their own has a slot for each.
+      const int V = warp == 3;
+      const CUtensorMap* map = V ? &vmap : &kmap;
+      uint8_t* ring = smem + (V ? kOffV : kOffK);
       RingPos r{0, 0};
       int32_t used = 0;     // slots begun
       int32_t late_n = 0;   // late entries
-      bool good = true;
-      // A step's sources: token rows; late rows y and end z of either lane's V, 8 bits each; groups (8 bits
-      // each) and lanes (bit 16 + X: lane X has the step, bit 18: both read one slot; 0: no step).
-      struct Src {
-        int32_t tok[2], late, what;
-      };
-      // One slot: 64 rows of the map's tensor from token row tok on. `alone`: one lane reads it.
-      auto slot = [&](const CUtensorMap* map, int32_t tok, int32_t g, bool alone, bool late, int32_t y, int32_t z,
-                      int32_t lanes) {
-        if (used >= kSlots && !wait_or_fail(&B.kv_empty[r.slot], r.phase ^ 1u, fail)) return false;
+      // One slot: 64 rows from token row tok on. y, z: V's late rows and its end; lanes that read it.
+      auto slot = [&](int32_t tok, int32_t g, int32_t y, int32_t z, int32_t lanes) {
+        if (used >= kSlots && !wait_or_fail(&B.kv_empty[V][r.slot], r.phase ^ 1u, fail)) return false;
         const int32_t ut = uniform(tok), ug = uniform(g), us = uniform(r.slot);
+        const bool late = V && y < kStep;
         if (lane == 0) {
-          uint64_t* full = &B.kv_full[us];
-          if (alone) mbar_arrive(&B.kv_empty[us]);
+          uint64_t* full = &B.kv_full[V][us];
           if (late) {
             const int32_t q = late_n & (kLate - 1);
             B.late[q] = {y, z, us, lanes};
@@ -670,22 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(full);
           }
           mbar_expect_tx(full, kKvTile);
-          tma_load_4d(smem + kOffRing + us * kKvTile, map, full, 0, ut, 0, ug);
+          tma_load_4d(ring + us * kKvTile, map, full, 0, ut, 0, ug);
         }
         __syncwarp();
         if (late) ++late_n;
         ++used;
         r.advance(1);
-        return true;
-      };
-      auto emit = [&](const CUtensorMap* map, const Src& s, bool v) {
-        auto one = [&](int X, bool alone, int32_t lanes) {
-          const int32_t y = s.late >> (16 * X) & 255, z = s.late >> (16 * X + 8) & 255;
-          return slot(map, s.tok[X], s.what >> (8 * X) & 255, alone, v && y < kStep, y, z, lanes);
-        };
-        if (s.what >> 18 & 1) return one(0, false, 3);
-        if ((s.what >> 16 & 1) && !one(0, true, 1)) return false;
-        if ((s.what >> 17 & 1) && !one(1, true, 2)) return false;
         return true;
       };
       int32_t k = 0, page[2] = {0, 0};
@@ -699,9 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, bad) && lane == 0) msa_record_error(kErrBadPage);
         return at;
       };
-      Src d1, d2;
-      d1.what = d2.what = 0;
       Unit u;
+      bool good = true;
+#pragma unroll 1
       while (good && (good = take(k, u)) && u.n[0] > 0) {
         const int32_t steps = u.n[0];
 #pragma unroll 1
@@ -710,30 +695,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             page[0] = look_up(u, 0, j);
             page[1] = u.kind == kHalves ? look_up(u, 1, j) : page[0];
           }
-          Src s;
-          s.late = 0;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          auto one = [&](int x, int32_t lanes) {
             const int32_t key = u.key0[x] + j * kStep;
-            s.tok[x] = __shfl_sync(0xffffffffu, page[x], j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
-            const int32_t y = max(0, min(u.pos + 1 - key, kStep)), z = max(0, min(u.seq - key, kStep));
-            s.late |= (y | z << 8) << (16 * x);
-          }
-          s.what = u.g[0] | u.g[1] << 8 | (u.kind == kShared ? 1 << 18 : 1 << 16 | (j < u.n[1] ? 1 << 17 : 0));
-          if (!(good = emit(&vmap, d2, true) && emit(&kmap, s, false))) break;
-          d2 = d1;
-          d1 = s;
-          if (!SELF) mbar_arrive_if(&B.want, lane == 0 && j == max(0, steps - 6));
+            const int32_t tok = __shfl_sync(0xffffffffu, page[x], j & 31) * MSA_BLOCK_TOKENS + key % MSA_BLOCK_TOKENS;
+            return slot(tok, u.g[x], max(0, u.pos + 1 - key), max(0, min(u.seq - key, kStep)), lanes);
+          };
+          if (u.kind == kShared) good = one(0, 3);
+          else good = one(0, 1) && (j >= u.n[1] || one(1, 2));
+          if (!good) break;
+          if (!SELF && !V) mbar_arrive_if(&B.want, lane == 0 && j == max(0, steps - 6));
         }
       }
-      good = good && emit(&vmap, d2, true) && emit(&vmap, d1, true);
-      if (good && lane == 0) {  // the late-row warps' end
+      if (V && good && lane == 0) {  // the late-row warps' end
         B.late[late_n & (kLate - 1)] = {0, 0, -1, 0};
         mbar_arrive(&B.late_full[late_n & (kLate - 1)]);
       }
       if (!good) {  // let the copies in flight land before the CTA leaves
         for (int32_t q = max(0, used - kSlots); q < used; ++q)
-          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.kv_full[q % kSlots], (q / kSlots) & 1, 1000); ++x) {
+          for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.kv_full[V][q % kSlots], (q / kSlots) & 1, 1000); ++x) {
           }
         for (int32_t q = max(0, late_n - kLate); q < late_n; ++q)
           for (int x = 0; x < 1000 && !mbar_try_wait_hint(&B.late_full[q % kLate], (q / kLate) & 1, 1000); ++x) {
@@ -891,39 +870,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ================================================================ MMA issuers, one per lane
       // For each step i of the CTA: O(i - 2), S(i). O needs P and V; S(i) needs K(i) and overwrites the
       // tensor memory from which O(i - 2) reads P, which it may as the tensor pipe runs one thread's MMAs
-      // in issue order. The warp runs in lockstep, an elected lane issues.
+      // in issue order. The warp runs in lockstep, an elected lane issues. Either issuer waits for every
+      // slot and gives it back, the other lane's too: a slot's users change with the units, and a barrier's
+      // parity tells a use from the one before it only to a warp that has seen that one.
       const int X = warp - 12;
       const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
       const uint32_t idesc_s = umma_idesc_bf16(128, kStep, 0, 0);
       const uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1);
       const uint64_t qd0 = umma_desc_sw128(sbase + X * kQTile, 16, 1024);
       uint64_t qd = qd0;
-      const uint64_t kd0 = umma_desc_sw128(sbase + kOffRing, 16, 1024);
-      const uint64_t vd0 = umma_desc_sw128(sbase + kOffRing, kKvHalf, 1024);
+      const uint64_t kd0 = umma_desc_sw128(sbase + kOffK, 16, 1024);
+      const uint64_t vd0 = umma_desc_sw128(sbase + kOffV, kKvHalf, 1024);
       constexpr uint32_t kMine = 1, kTwo = 2, kOpens = 4, kAny = 8;  // of a step
       uint32_t d1 = 0, d2 = 0;
       Unit u;
       u.n[0] = u.n[1] = u.kind = 0;
       int32_t k = 0, j = 0, steps = 0, n_s = 0, n_o = 0, opened = 0, tiles = 0;
-      RingPos r{0, 0};
+      RingPos rk{0, 0}, rv{0, 0};
       bool good = true, more = true;
 #pragma unroll 1
       while (more || d1 || d2) {
         if (d2) {  // O of the step before the last
-          if (d2 & kMine) {
-            const RingPos at = (d2 & kTwo) && X ? r.after(1) : r;
-            const uint32_t buf = n_o & 1;
-            if ((d2 & kOpens) && opened++ > 0 && !(good = wait_or_fail(&B.o_free[X], opened & 1, fail))) break;
-            if (!(good = wait_two_or_fail(&B.kv_full[at.slot], at.phase, &B.p_full[X][buf], (n_o >> 1) & 1, fail)))
-              break;
+          const bool mine = d2 & kMine, two = d2 & kTwo;
+          const RingPos at = two && X ? rv.after(1) : rv, other = two ? (X ? rv : rv.after(1)) : at;
+          const uint32_t buf = n_o & 1;
+          if (mine && (d2 & kOpens) && opened++ > 0 && !(good = wait_or_fail(&B.o_free[X], opened & 1, fail))) break;
+          // own V, the other lane's, P
+          const int w = lane & 3;
+          if (!(good = wait_all_or_fail(w == 0 && mine ? &B.p_full[X][buf] : &B.kv_full[1][w == 1 ? other.slot : at.slot],
+                                        w == 0 && mine ? (n_o >> 1) & 1 : (w == 1 ? other.phase : at.phase), fail)))
+            break;
+          const int32_t us = uniform(at.slot);
+          if (mine) {
             tmem_fence_after();
-            const int32_t us = uniform(at.slot);
             issue_o(o_tmem, s_tmem + buf * 64, vd0 + us * (kKvTile >> 4), idesc_o, (d2 & kOpens) ? 0 : 1);
             umma_commit_elect(&B.o_full[X][buf]);
-            umma_commit_elect(&B.kv_empty[us]);
+            umma_commit_elect(&B.kv_empty[1][us]);
             ++n_o;
           }
-          r.advance((d2 & kTwo) ? 2 : 1);
+          mbar_arrive_if(&B.kv_empty[1][other.slot], lane == 0 && (two || !mine));
+          rv.advance(two ? 2 : 1);
         }
         uint32_t d = 0;
         if (more) {
@@ -934,29 +920,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             more = steps > 0;
           }
           if (more) {
-            const int32_t mine = X ? u.n[1] : u.n[0], other = X ? u.n[0] : u.n[1];
-            d = kAny | (j < mine ? kMine : 0u) | (u.kind != kShared && j < mine && j < other ? kTwo : 0u) |
-                (j == 0 && mine > 0 ? kOpens : 0u);
-            if (d & kMine) {
-              const RingPos at = (d & kTwo) && X ? r.after(1) : r;
+            const int32_t n_mine = X ? u.n[1] : u.n[0], n_other = X ? u.n[0] : u.n[1];
+            d = kAny | (j < n_mine ? kMine : 0u) | (u.kind != kShared && j < n_mine && j < n_other ? kTwo : 0u) |
+                (j == 0 && n_mine > 0 ? kOpens : 0u);
+            const bool mine = d & kMine, two = d & kTwo;
+            const RingPos at = two && X ? rk.after(1) : rk, other = two ? (X ? rk : rk.after(1)) : at;
+            const bool q = mine && j == 0;  // own K, the other lane's, the tile's queries
+            const int w = lane & 3;
+            if (!(good = wait_all_or_fail(
+                      w == 0 && q ? &B.q_full[X][tiles & 1] : &B.kv_full[0][w == 1 ? other.slot : at.slot],
+                      w == 0 && q ? (tiles >> 1) & 1 : (w == 1 ? other.phase : at.phase), fail)))
+              break;
+            if (q) {
+              qd = qd0 + (is_small(u) ? (tiles & 1) * (kQHalf / 2 >> 4) : 0);
+              ++tiles;
+            }
+            if (mine) {
               const uint32_t buf = n_s & 1;
-              if (j == 0) {
-                if (!(good = wait_or_fail(&B.q_full[X][tiles & 1], (tiles >> 1) & 1, fail))) break;
-                qd = qd0 + (is_small(u) ? (tiles & 1) * (kQHalf / 2 >> 4) : 0);
-                ++tiles;
-              }
-              if (!(good = wait_or_fail(&B.kv_full[at.slot], at.phase, fail))) break;
               tmem_fence_after();
               const int32_t us = uniform(at.slot);
               const uint64_t kd = kd0 + us * (kKvTile >> 4);
               issue_s(s_tmem + buf * 64, qd, kd, idesc_s, 0);
               issue_s(s_tmem + buf * 64, qd + (kQHalf >> 4), kd + (kKvHalf >> 4), idesc_s, 1);
               umma_commit_elect(&B.s_full[X][buf]);
-              umma_commit_elect(&B.kv_empty[us]);
-              if (j == mine - 1) umma_commit_elect(&B.q_empty[X][(tiles - 1) & 1]);
+              umma_commit_elect(&B.kv_empty[0][us]);
+              if (j == n_mine - 1) umma_commit_elect(&B.q_empty[X][(tiles - 1) & 1]);
               ++n_s;
             }
-            r.advance((d & kTwo) ? 2 : 1);
+            mbar_arrive_if(&B.kv_empty[0][other.slot], lane == 0 && (two || !mine));
+            rk.advance(two ? 2 : 1);
             ++j;
           }
         }
@@ -976,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_or_fail(&B.late_full[q], (k / kLate) & 1, fail)) break;
         const Late e = B.late[q];
         if (e.slot < 0) break;  // no more
-        const uint32_t at = sbase + kOffRing + e.slot * kKvTile + h * kKvHalf + (lane & 7) * 16;
+        const uint32_t at = sbase + kOffV + e.slot * kKvTile + h * kKvHalf + (lane & 7) * 16;
         bool odd = false;
         // lanes 8 i .. 8 i + 7: one row
 #pragma unroll 1
@@ -1005,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           if (odd && (e.lanes & 1)) *(volatile int32_t*)&B.odd[0] = 1;
           if (odd && (e.lanes & 2)) *(volatile int32_t*)&B.odd[1] = 1;
-          mbar_arrive(&B.kv_full[e.slot]);
+          mbar_arrive(&B.kv_full[1][e.slot]);
         }
         __syncwarp();
       }
