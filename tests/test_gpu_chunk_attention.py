@@ -169,6 +169,25 @@ def test_long(new, held, Hq, Hkv):
     check(run(w), reference(w, DEV))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(32, 4), (16, 1)])
+@pytest.mark.parametrize("pad", [0, 1 << 17])
+def test_units_of_all_kinds_in_turn_from_caches_beyond_l2(Hq, Hkv, pad):
+    """Decode rows, short chunks and long ones alternate, so that slots of K and V change between lanes
+    that share steps and lanes that do not, while loads take long (some 300 MB of cache). With many
+    padding rows the call is one that lists its work, else one that cuts it into equal runs."""
+    g = np.random.default_rng(Hq)
+    B = 48
+    new = [int(x) for x in g.choice([1, 1, 1, 3, 17, 40, 75], B)]
+    held = [int(x) for x in g.integers(0, 26000 // Hkv, B)]
+    w = make(new, held, Hq, Hkv, seed=90 + Hq, pad=0)
+    ref = reference(w, DEV)
+    if pad:
+        w["q"] = torch.cat([w["q"], torch.zeros((pad, Hq, D), dtype=torch.bfloat16)])
+    for _ in range(3):
+        o, lse = run(w)
+        check((o[:sum(new)], lse[:sum(new)]), ref)
+
+
 def test_large_scores_rescale_the_output():
     # scores that grow along the keys: the softmax's reference has to move many times
     w = make([40, 1], [600, 900], 16, 2, seed=3, scale=30.0)
@@ -414,6 +433,33 @@ def test_steps_of_a_scheduler():
         w = dict(q=q, kc=kc, vc=vc, table=table.clamp(min=0), seq=seq, cu=cu)
         check(got, reference({a: x.cpu() for a, x in w.items()}), slice(0, n))
         prev = seq
+
+
+FRESH = """
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import test_gpu_chunk_attention as t, torch, block_sparse_attention_msa_gb300 as msa
+for new, held in (([5, 1, 40], [300, 77, 0]), ([900], [100])):
+    w = t.make(new, held, 64, 8, seed=1)
+    d = {k: x.cuda() for k, x in w.items()}
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = msa.chunk_attention(d["q"], d["kc"], d["vc"], d["table"], d["seq"], d["cu"])
+    g.replay()
+    torch.cuda.synchronize()
+    assert msa.device_error() == 0
+    t.check(out, t.reference(w))
+"""
+
+
+def test_the_first_call_of_a_process_can_be_a_captured_one():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_refusals():

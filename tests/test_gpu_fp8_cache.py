@@ -142,6 +142,26 @@ def test_append_and_gather(T, Hkv, strided):
         assert torch.equal(a[live], b[live])
 
 
+@pytest.mark.parametrize("shift", [0, 8, 16, 24])
+def test_rows_at_every_16_byte_offset(shift):
+    # rows and outputs that are aligned to 16 bytes, not to 32
+    g = torch.Generator(device=DEV).manual_seed(shift)
+    T, Hkv = 300, 4
+    flat = torch.randn(2 * T * (Hkv * D + 8) + 64, generator=g, device=DEV).to(torch.bfloat16)
+    rows = flat[shift:shift + 2 * T * (Hkv * D + 8)].view(2, T, Hkv * D + 8)
+    k, v = (rows[i, :, :Hkv * D].unflatten(1, (Hkv, D)) for i in range(2))    # strides of 16-byte multiples
+    slots = torch.randperm(4 * PAGE, generator=g, device=DEV)[:T].to(torch.int32)
+    c = caches(4, Hkv)
+    msa.append_kv_fp8(k, v, slots, *c)
+    check_stored(c, slots.cpu().numpy(), k, v)
+    space = torch.zeros(2 * T * Hkv * D + 64, dtype=torch.bfloat16, device=DEV)
+    out = [space[shift + i * T * Hkv * D:shift + (i + 1) * T * Hkv * D].view(T, Hkv, D) for i in range(2)]
+    msa.gather_kv_fp8(*c, slots, out=out)
+    for x, back in ((k, out[0]), (v, out[1])):
+        assert np.array_equal(f64(back), ref_values(*ref_quantise(f64(x))))
+    assert not space[:shift].any() and not space[shift + 2 * T * Hkv * D:].any()
+
+
 def test_append_at_the_borders_of_the_format():
     """Every bf16 magnitude as a row's largest, ties, zeros, subnormals, NaN and infinities."""
     bits = torch.arange(0x7f80, dtype=torch.int32)                    # the finite magnitudes
