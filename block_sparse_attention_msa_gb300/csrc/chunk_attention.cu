@@ -11,14 +11,18 @@
 //    Tokens that fill one tile at most (decode rows, the rest of a chunk) give each of the CTA's two
 //    lanes a KV group, or half of the keys, of its own: their MMAs run far below their rate, but a step's
 //    keys take longer to arrive than the padded MMAs take.
-//  * Units. A tile pair (or tile) is cut along its keys into pieces of at most max(8 steps, an eighth
-//    of what is left per CTA... see piece_cost) so that the last units to start are short. A piece that is
-//    its whole tile writes the output itself; others leave partials that a second kernel joins in
-//    their order. The plan kernel makes the list of units from the lengths on the GPU, so a call can be
-//    captured once and replayed with other lengths. CTAs take units from the list one after the other;
-//    which CTA takes which changes no result.
+//  * Units. A tile pair (or tile) is cut along its keys into runs of steps. A run that is its whole tile
+//    writes the output itself; others leave partials that a second kernel joins in their order. The runs
+//    are made from the lengths on the GPU, so a call can be captured once and replayed with other lengths,
+//    in one of two ways that the host chooses by what the sizes allow (see the launch):
+//      - equal runs: every CTA walks the lengths itself and takes its share of all steps, without another
+//        launch. For few tiles, where the launch and the reading of a list would be most of the time;
+//      - a list: a plan kernel writes units of at most half of a CTA's share of what is left (kMinPiece
+//        steps at least), so that the last ones to start are short, and CTAs take one after the other.
+//        Which CTA takes which changes no result. Tiles need different times (causal ends, kinds), which
+//        evens out this way.
 //  * The order (request, group, last tiles first, pieces) lets the CTAs that run at the same time read
-//    the same keys, and DRAM once.
+//    the same keys, and DRAM once (4096 tokens on 16384: 152 MB read, as many as the caches and Q hold).
 //  * V cells that a row must not use (later tokens of its request, what lies behind its last token) are
 //    multiplied by weights of 0, and 0 * NaN is NaN. So in steps that hold such cells two warps
 //    look through V in shared memory before the MMAs: rows behind the request's end become zeros, and so
@@ -28,7 +32,20 @@
 // softmax warpgroup per lane keeps the running reference and sum in fp32. P is rounded to bf16 for its
 // product, as tensor cores take it beside V in bf16 (2^-9 of each weight at most); its sum l is taken
 // before that rounding. A step is 64 keys because then S has two buffers per lane next to O (2 lanes x
-// (2 x 64 + 128) = 512 columns): S(i+1) is ready when the softmax of step i ends.
+// (2 x 64 + 128) = 512 columns): S(i+1) is ready when the softmax of step i ends. K and V come through a
+// ring and a producer warp each: one warp for both needs 1.4 us a step, as long as the decode rows' step.
+//
+// What bounds it, Hq/Hkv/D = 64/8/128 and 1.87 PFLOP/s bf16, 6.79 TB/s measured:
+//   one prompt of 16384             3.00-3.15 ms  (1.40-1.47 PFLOP/s, 75-78 % of the burst rate)
+//   2048 tokens on 60032 keys       2.82-2.93 ms  (1.40-1.46 PFLOP/s)
+//   64 decode rows, 8k-128k keys    0.386-0.391 ms (the copy rate: HBM)
+//   64 chunks of 64 tokens          0.144 ms; 1 row on 2048 keys 13 us (latency, two launches)
+// Long chunks are bound by the S products. An N = 64 product reads its 128 x 16 Q operand from shared
+// memory again at every instruction: 48 cycles measured where its arithmetic takes 32 (N = 128: 64 of 64; P
+// from tensor memory, N = 128: 64 of 64). Without the S products 3.09 ms became 2.22, without the O products
+// 2.88, without the softmax's arithmetic 2.94. Steps of 128 keys do away with that, but leave one
+// S buffer per lane, so a lane's softmax and its S product take turns: 3.31 ms.
+// Also slower: both lanes' issue strictly in turn (4.76 ms), the softmax in scalar instead of paired fp32.
 #include <math.h>
 
 #include "common.cuh"
