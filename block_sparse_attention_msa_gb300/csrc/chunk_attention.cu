@@ -17,7 +17,7 @@
 //    in one of two ways that the host chooses by what the sizes allow (see the launch):
 //      - equal runs: every CTA walks the lengths itself and takes its share of all steps, without another
 //        launch. For few tiles, where the launch and the reading of a list would be most of the time;
-//      - a list: a plan kernel writes units of at most half of a CTA's share of what is left (kMinPiece
+//      - a list: a plan kernel writes units of at most two thirds of a CTA's share of what is left (kMinPiece
 //        steps at least), so that the last ones to start are short, and CTAs take one after the other.
 //        Which CTA takes which changes no result. Tiles need different times (causal ends, kinds), which
 //        evens out this way.
@@ -37,9 +37,9 @@
 //
 // What bounds it, Hq/Hkv/D = 64/8/128 and 1.87 PFLOP/s bf16, 6.79 TB/s measured:
 //   one prompt of 16384             3.00-3.15 ms  (1.40-1.47 PFLOP/s, 75-78 % of the burst rate)
-//   2048 tokens on 60032 keys       2.82-2.93 ms  (1.40-1.46 PFLOP/s)
+//   2048 tokens on 60032 keys       2.83-2.87 ms  (1.43-1.45 PFLOP/s)
 //   64 decode rows, 8k-128k keys    0.386-0.391 ms (the copy rate: HBM)
-//   64 chunks of 64 tokens          0.144 ms; 1 row on 2048 keys 13 us (latency, two launches)
+//   64 chunks of 64 tokens          0.117 ms; 1 row on 2048 keys 13 us (latency, two launches)
 // Long chunks are bound by the S products. An N = 64 product reads its 128 x 16 Q operand from shared
 // memory again at every instruction: 48 cycles measured where its arithmetic takes 32 (N = 128: 64 of 64; P
 // from tensor memory, N = 128: 64 of 64). Without the S products 3.09 ms became 2.22, without the O products
@@ -78,7 +78,7 @@ constexpr float kFarSum = 16384.f;  // of a step's P: beyond it the softmax's re
 // s log2(e) - m in one fma is off by what m was rounded by, the same for all keys of a row: a common
 // factor of P and l. Beyond this magnitude of m it would leave fp32's range, and m is subtracted first.
 constexpr float kFarRef = 16777216.f;
-constexpr int kMinPiece = 8;        // steps of a piece, where the whole call has as many per CTA
+constexpr int kMinPiece = 16;       // steps of a piece, where the whole call has as many per CTA
 // Of the cut into equal runs: relative time of a step of a shared unit and of lanes with keys of their own
 // (which HBM feeds at the copy rate when all CTAs have such), and what a tile's end and beginning take.
 constexpr int32_t kSharedCost = 4, kOwnCost = 7, kTileCost = 7;
@@ -278,9 +278,11 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums, int64_t&
 static_assert(kPlanThreads == 1024, "block_scan: 32 warps");
 
 // Pieces of an item at which `left` steps of the whole call, its own among them, are still to come:
-// half of a CTA's share of them each, so that the CTAs end together.
+// two thirds of a CTA's share of them each, so that the CTAs end together. (kMinPiece 8 and half of the share
+// left 3.5 partials per row of 2048 tokens on 60032 and took 1 % longer there, 64 chunks of 64 tokens 145 instead of
+// 117 us; the whole share 2 % longer.)
 __device__ __forceinline__ int32_t pieces_of(const KParams& p, int32_t cost, int64_t left, int32_t least) {
-  const int32_t most = (int32_t)max((int64_t)least, (left + 2 * p.ctas - 1) / (2 * p.ctas));
+  const int32_t most = (int32_t)max((int64_t)least, (2 * left + 3 * p.ctas - 1) / (3 * p.ctas));
   return (cost + most - 1) / most;
 }
 
@@ -1250,9 +1252,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------------------ join
-// A CTA joins a tile: four groups of 256 threads take eight rows each, a thread four channels of one row, so
-// a warp reads whole 128-byte lines of the partials' [channel quad][row][4] layout. With fewer rows the
-// groups deal a row's pieces among them, four loads in flight each, and join through shared memory.
+// A CTA joins rows of a tile: four groups of 256 threads take eight rows each, a thread four channels of one
+// row, so a warp reads whole 128-byte lines of the partials' [channel quad][row][4] layout. Of more than four
+// pieces the groups share them, for fewer rows at a time, four loads in flight each, and join through shared
+// memory. A tile's slices of rows go to different CTAs, since the last tiles are cut into the most pieces
+// (2048 tokens on 60032: 120 of them; a CTA per tile took 147 us).
 constexpr int kJoinRows = 8;
 constexpr int kJoinSplit = 4;
 constexpr int kJoinThreads = kJoinRows * 32 * kJoinSplit;
@@ -1291,19 +1295,41 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
   __shared__ float4 s_o[kJoinSplit][kJoinRows * 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int t = threadIdx.x % (kJoinRows * 32), group = threadIdx.x / (kJoinRows * 32);
+  const int t = threadIdx.x % (kJoinRows * 32), group = threadIdx.x / (kJoinRows * 32), lane = threadIdx.x & 31;
   const int32_t quad = t / kJoinRows;
-  if (tiles == 0) tiles = p.head->joins;
+  // In the list the most pieces are behind. Of equal runs the first CTAs have what few there are, and the join's
+  // first CTAs start first.
+  const bool listed = tiles == 0;
+  if (listed) tiles = p.head->joins;
+  const int32_t slices = p.tile_rows / kJoinRows, step = 2 * p.tile_rows;
+  const uint32_t units = (uint32_t)(tiles * slices);  // in 32 bits: tiles are a few thousand at most
 #pragma unroll 1
-  for (int32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const JoinTile e = p.joins[tile];
-    if (e.rows <= 0) continue;
-    const int32_t split = e.rows <= kJoinRows ? 4 : (e.rows <= 2 * kJoinRows ? 2 : 1);
-    const int32_t step = 2 * p.tile_rows;
+  for (uint32_t u0 = blockIdx.x; u0 < units; u0 += 32 * gridDim.x) {
+    // a lane reads one of the CTA's next 32 units
+    const uint32_t unit = u0 + lane * gridDim.x;
+    JoinTile mine{};
+    int32_t my_split = 1;  // 1, 2 or 4
+    int32_t my_r0 = 0;
+    if (unit < units) {
+      int32_t at = (int32_t)unit;
+      if (slices > 1) {
+        const int32_t slice = (int32_t)(unit / (uint32_t)tiles);
+        at += slice * ((int32_t)((uint32_t)tiles / (uint32_t)slices) - tiles);
+        if (at >= tiles) at -= tiles;
+        my_r0 = slice * kJoinRows;
+      }
+      mine = p.joins[listed ? tiles - 1 - at : at];
+      my_split = mine.pieces <= 4 ? 1 : (mine.pieces <= 8 ? 2 : 4);
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, my_r0 < mine.rows && (my_r0 & (kJoinRows * kJoinSplit / my_split - 1)) == 0);
 #pragma unroll 1
-    for (int32_t r0 = 0; r0 < e.rows; r0 += kJoinRows * kJoinSplit / split) {
-      const int32_t part = group % split;
-      const int32_t r = r0 + group / split * kJoinRows + (t & (kJoinRows - 1));
+    for (; todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      auto get = [&](int32_t x) { return __shfl_sync(0xffffffffu, x, src); };
+      const JoinTile e{get(mine.row), get(mine.rows), get(mine.g), get(mine.first), get(mine.rest),
+                       get(mine.pieces), get(mine.cap), 0};
+      const int32_t split = get(my_split), part = group & (split - 1);
+      const int32_t r = get(my_r0) + (group >> (split >> 1)) * kJoinRows + (t & (kJoinRows - 1));
       const bool valid = r < e.rows;
       Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       if (valid) {
@@ -1376,11 +1402,11 @@ Layout layout_of(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_bloc
     y.cap_pieces = 2 * ctas;  // of a run's first and last item
   } else {
     // Pieces of the items that are cut: an item of c steps with r still to come, itself included, has
-    // ceil(c / max(8, r / 2 ctas)) pieces, at most 2 c / that for more than one. r falls to 0 over the call,
-    // so the sum is at most 2 * 2 ctas * (1 + log(most steps / 8)); with less than 8 steps per CTA pieces
+    // ceil(c / max(16, 2 r / 3 ctas)) pieces, at most 2 c / that for more than one. r falls to 0 over the call,
+    // so the sum is at most 2 * 1.5 ctas * (1 + log(most steps / 16)); with less than 16 steps per CTA pieces
     // are as short as these, and at most 2 * ctas.
     const double most = 2.0 * max_blocks / kMinPiece;
-    const int64_t cut = (int64_t)(4.0 * ctas * (1.0 + (most > 1 ? log(most) : 0.0))) + 16;
+    const int64_t cut = (int64_t)(3.0 * ctas * (1.0 + (most > 1 ? log(most) : 0.0))) + 16;
     y.cap_units = (int32_t)(items + cut);
     y.cap_joins = (int32_t)(2 * cut);
     y.cap_pieces = (int32_t)cut;

@@ -497,8 +497,8 @@ MSA_API int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache,
  *   T * Hq / Hkv) rows a piece. Where T <= B * 128 * Hkv / Hq (one tile of query rows per request on
  *   average) or few pairs of tiles come together, CTAs cut the keys into equal runs, at most two pieces per
  *   SM: 40 MB with 152 SMs (2.5 MB for one row of G 8); else, for long prompts, it also holds the list of
- *   work, and the most pieces that any lengths lead to, 600 * (1 + log(max_blocks / 4)): 0.46 GB for 2048
- *   rows of one request with G 8 and 485 blocks, 0.53 GB for 1024 blocks.
+ *   work, and the most pieces that any lengths lead to, 456 * (1 + log(max_blocks / 8)): 0.30 GB for 2048
+ *   rows of one request with G 8 and 485 blocks, 0.35 GB for 1024 blocks.
  * B <= 16384, T*Hq in int32. Lengths and tables are read on the device: a captured call can be
  * replayed with other values in the same buffers. cu_tokens out of order or outside [0, T], lengths
  * below n_b or above max_blocks*128 are clamped and set bit 1 of the device error word, a page id
