@@ -110,7 +110,7 @@ def test_chunk_workspace_size(lib):
     assert size(1, 1, 8, 1, 128) < size(1, 16, 8, 1, 128)
     # the stated number of pieces, 520 bytes a row, 2 * 128 rows a piece
     for mb in (485, 1024):
-        stated = 600 * (1 + math.log(mb / 4)) * 2 * 128 * 520
+        stated = 456 * (1 + math.log(mb / 8)) * 2 * 128 * 520
         assert 0.95 * stated < size(1, 2048, 64, 8, mb) < 1.05 * stated
     for bad in ((0, 4, 64, 8, 4), (4, 0, 64, 8, 4), (4, 4, 60, 8, 4), (4, 4, 0, 8, 4), (4, 4, 96, 3, 4), (4, 4, 64, 8, 0),
                 (16385, 4, 64, 8, 4), (4, 1 << 30, 64, 8, 4)):
