@@ -38,7 +38,7 @@
 // What bounds it, Hq/Hkv/D = 64/8/128 and 1.87 PFLOP/s bf16, 6.79 TB/s measured:
 //   one prompt of 16384             3.00-3.15 ms  (1.40-1.47 PFLOP/s, 75-78 % of the burst rate)
 //   2048 tokens on 60032 keys       2.83-2.87 ms  (1.43-1.45 PFLOP/s)
-//   64 decode rows, 8k-128k keys    0.386-0.391 ms (the copy rate: HBM)
+//   64 decode rows, 4k-16k keys     0.381-0.391 ms (the copy rate: HBM)
 //   64 chunks of 64 tokens          0.117 ms; 1 row on 2048 keys 13 us (latency, two launches)
 // Long chunks are bound by the S products. An N = 64 product reads its 128 x 16 Q operand from shared
 // memory again at every instruction: 48 cycles measured where its arithmetic takes 32 (N = 128: 64 of 64; P
