@@ -361,14 +361,10 @@ def sparse_prefill_paged(q, k_cache, v_cache, page_table, block_ids, S_kv: int,
 # checks), page tables 21 to 25 us (30; five outputs to allocate), shared-prefix decode 25 to 29 us
 # (two launches, eleven tensor maps).
 
-def _ok(t, dtype, ndim: int, dev) -> bool:
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
-            and t.device == dev)
-
-
 def _check(name: str, t, dtype, ndim: int, dev):
     """A contiguous CUDA tensor of that type and rank on `dev`; the errors of ``_need``."""
-    if not _ok(t, dtype, ndim, dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+            and t.device == dev):
         _need(t, name, dtype, ndim)
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
 
@@ -386,6 +382,24 @@ def _call(dev, fn, *args):
         return fn(*args, stream)
     with torch.cuda.device(dev):
         return fn(*args, stream)
+
+
+def _scratch_call(dev, workspace: Workspace | None, key: str, size, fn):
+    """fn(pointer, bytes, stream) with `dev` current and size() bytes of scratch, from `workspace` or, for
+    this call alone, from the caching allocator: in the stream's order, as a tensor's memory would be, but
+    without the tensor (3 us of a call of 22)."""
+    def run(stream):
+        nbytes = max(256, size())
+        if workspace is not None:
+            buf = workspace.get(key, nbytes, dev)
+            return fn(buf.data_ptr(), buf.numel(), stream)
+        ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+        try:
+            return fn(ptr, nbytes, stream)
+        finally:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ptr)
+
+    return _call(dev, run)
 
 
 def build_page_tables(prev_lens, new_lens, page_table, free_pages, pages_used, T: int,
@@ -594,19 +608,13 @@ def chunk_attention(q, k_cache, v_cache, page_table, seq_lens, cu_tokens, with_l
         if o.shape != q.shape or (lse is not None and lse.shape != (T, Hq)):
             raise ValueError("chunk_attention: output shapes do not match")
     lib = load()
-
-    def run(stream):
-        # on the device: the size goes with its SM count
-        nbytes = max(256, lib.msa_chunk_attention_workspace_size(B, T, Hq, Hkv, max_blocks))
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None \
-            else workspace.get("chunk", nbytes, dev)
-        return lib.msa_chunk_attention(
-            qp, q_stride, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-            seq_lens.data_ptr(), cu_tokens.data_ptr(), B, T, Hq, Hkv, D, max_blocks, P, o.data_ptr(),
-            None if lse is None else lse.data_ptr(), buf.data_ptr(), nbytes if workspace is None
-            else buf.numel(), stream)
-
-    _lib.check("msa_chunk_attention", _call(dev, run))
+    rc = _scratch_call(  # the size goes with the device's SM count
+        dev, workspace, "chunk", lambda: lib.msa_chunk_attention_workspace_size(B, T, Hq, Hkv, max_blocks),
+        lambda ws, nbytes, stream: lib.msa_chunk_attention(
+            qp, q_stride, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+            cu_tokens.data_ptr(), B, T, Hq, Hkv, D, max_blocks, P, o.data_ptr(),
+            None if lse is None else lse.data_ptr(), ws, nbytes, stream))
+    _lib.check("msa_chunk_attention", rc)
     return o, lse
 
 
@@ -695,7 +703,7 @@ def paged_sparse_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, flat_page_tab
         raise ValueError("paged_sparse_decode_fp8: inconsistent shapes")
     _sizes("paged_sparse_decode_fp8", R, Hq, topk)
     if out is None:
-        o = torch.empty((R, Hq, D), dtype=bf16, device=dev)
+        o = torch.empty_like(q)
         lse = torch.empty((R, Hq), dtype=torch.float32, device=dev) if with_lse else None
     else:
         o, lse = out
@@ -705,13 +713,12 @@ def paged_sparse_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, flat_page_tab
         if o.shape != q.shape or (lse is not None and lse.shape != (R, Hq)):
             raise ValueError("paged_sparse_decode_fp8: output shapes do not match")
     lib = load()
-    nbytes = max(256, lib.msa_paged_sparse_decode_workspace_size(R, Hq, Hkv, topk))
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None \
-        else workspace.get("decode_fp8", nbytes, dev)
-    rc = _call(dev, lib.msa_paged_sparse_decode_fp8, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-               k_scale.data_ptr(), v_scale.data_ptr(), flat_page_table.data_ptr(), flat_kv_lens.data_ptr(),
-               R, Hq, Hkv, D, topk, P, o.data_ptr(), None if lse is None else lse.data_ptr(),
-               buf.data_ptr(), buf.numel())
+    rc = _scratch_call(
+        dev, workspace, "decode_fp8", lambda: lib.msa_paged_sparse_decode_workspace_size(R, Hq, Hkv, topk),
+        lambda ws, nbytes, stream: lib.msa_paged_sparse_decode_fp8(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            flat_page_table.data_ptr(), flat_kv_lens.data_ptr(), R, Hq, Hkv, D, topk, P, o.data_ptr(),
+            None if lse is None else lse.data_ptr(), ws, nbytes, stream))
     _lib.check("msa_paged_sparse_decode_fp8", rc)
     return o, lse
 
