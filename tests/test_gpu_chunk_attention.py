@@ -169,6 +169,22 @@ def test_long(new, held, Hq, Hkv):
     check(run(w), reference(w, DEV))
 
 
+@pytest.mark.parametrize("new", [1, 2, 5, 9, 16, 23])
+@pytest.mark.parametrize("pad", [0, 1 << 14])
+def test_a_tile_in_any_number_of_pieces(new, pad):
+    """Tiles of 8 to 128 rows (and a pair) whose keys are cut into few, several and many pieces, by calls
+    that cut equal runs and by calls that list their work (many
+    padding rows)."""
+    Hq, Hkv = 16, 2
+    for held in (64, 190, 330, 500, 640, 1000, 1500, 2600):
+        w = make([new], [held], Hq, Hkv, seed=held + new)
+        ref = reference(w, DEV)
+        if pad:
+            w["q"] = torch.cat([w["q"], torch.zeros((pad, Hq, D), dtype=torch.bfloat16)])
+        o, lse = run(w)
+        check((o[:new], lse[:new]), ref)
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(32, 4), (16, 1)])
 @pytest.mark.parametrize("pad", [0, 1 << 17])
 def test_units_of_all_kinds_in_turn_from_caches_beyond_l2(Hq, Hkv, pad):
