@@ -542,7 +542,8 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
         reinterpret_cast<float*>(smem + (lane % kClusterWarps) * kRing) + 16 * 128, lane / kClusterWarps);
     const float l = pl[h];
     const float m = warp_max(l);
-    const float e = (m == -INFINITY || l == -INFINITY) ? 0.f : __expf(l - m);
+    // the lane's own part alone says whether it is empty: a NaN, which the maximum passes over, stays one
+    const float e = l == -INFINITY ? 0.f : __expf(l - m);
     const float total = warp_sum(e);
     wts[h * 32 + lane] = total == 0.f ? 0.f : e / total;
     if (lane == 0 && lse_out && rank == (h % kClusterCtas))

@@ -1,0 +1,86 @@
+"""GPU tests: a row that sees a NaN gives NaN, in o and in lse, whatever form of a kernel takes it: one
+cluster per row or partials with a merge, whole rows or halves of their keys. An lse of -inf says that a row
+saw no key, and a later merge drops such a row."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_msa_gb300 as msa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+PAGE = 128
+D = 128
+NAN = float("nan")
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_sparse_attention_msa_gb300 import build
+    build.build()
+    msa.load()
+    assert msa.device_error() == 0
+
+
+@pytest.fixture(autouse=True)
+def no_error_left():
+    yield
+    assert msa.device_error() == 0
+
+
+def i32(x):
+    return torch.from_numpy(np.array(x, dtype=np.int32))
+
+
+def sparse_rows(R, Hq, Hkv, n, topk, seed):
+    """R rows of n visible tokens, every row on pages of its own."""
+    g = torch.Generator().manual_seed(seed)
+    m = (n + PAGE - 1) // PAGE
+    pages = R * m
+    fpt = torch.full((R * Hkv, topk), -1, dtype=torch.int64)
+    for f in range(R * Hkv):
+        fpt[f, :m] = (f // Hkv * m + torch.arange(m)) * PAGE * Hkv + f % Hkv
+    return dict(q=(torch.randn((R, Hq, D), generator=g) * D ** -0.5).to(torch.bfloat16).to(DEV),
+                k=torch.randn((pages, PAGE, Hkv, D), generator=g).to(torch.bfloat16).to(DEV),
+                v=torch.randn((pages, PAGE, Hkv, D), generator=g).to(torch.bfloat16).to(DEV),
+                fpt=fpt.to(torch.int32).to(DEV), lens=torch.full((R * Hkv,), n, dtype=torch.int32, device=DEV), m=m)
+
+
+def decode_fp8(w):
+    P, _, Hkv, _ = w["k"].shape
+    c = [torch.zeros((P, Hkv, PAGE, D), dtype=torch.uint8, device=DEV).view(F8) for _ in range(2)]
+    c += [torch.zeros((P, Hkv, PAGE), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    slots = torch.arange(P * PAGE, dtype=torch.int32, device=DEV)
+    msa.append_kv_fp8(w["k"].view(-1, Hkv, D), w["v"].view(-1, Hkv, D), slots, *c)
+    return msa.paged_sparse_decode_fp8(w["q"], *c, w["fpt"], w["lens"])
+
+
+def decode_bf16(w):
+    return msa.paged_sparse_decode(w["q"], w["k"], w["v"], w["fpt"], w["lens"])
+
+
+DECODES = [pytest.param(decode_fp8, id="e4m3")]
+
+
+# rows: one cluster each where there are few, else partials and a merge kernel
+@pytest.mark.parametrize("decode", DECODES)
+@pytest.mark.parametrize("R", [1, 40])
+@pytest.mark.parametrize("n,topk", [(1, 2), (100, 4), (128, 4), (500, 4), (700, 40)])
+@pytest.mark.parametrize("what", ["query", "key"])
+def test_decode_rows_that_see_a_nan(decode, R, n, topk, what):
+    Hq, Hkv = 16, 2
+    w = sparse_rows(R, Hq, Hkv, n, topk, seed=n)
+    clean = decode(w)
+    r = R // 2
+    if what == "query":
+        w["q"][r, 9, 77] = NAN                      # one head of group 1
+        heads = slice(9, 10)
+    else:
+        for page in range(w["m"]):                  # one visible key of every page of group 1
+            w["k"][r * w["m"] + page, min(PAGE, n - page * PAGE) // 2, 1, 5] = NAN
+        heads = slice(8, 16)
+    o, lse = decode(w)
+    assert torch.isnan(o[r, heads]).all() and torch.isnan(lse[r, heads]).all()
+    o[r, heads], lse[r, heads] = clean[0][r, heads], clean[1][r, heads]
+    assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
