@@ -327,12 +327,12 @@ __device__ __forceinline__ void store_partial(float* dst, float* lse_dst, const 
   for (int r = 0; r < 2; ++r) {
     const int row = gid + 8 * r;
     if (row >= G) continue;
-    const float inv = lrow[r] > 0.f ? 1.0f / lrow[r] : 0.f;
+    const float inv = lrow[r] == 0.f ? 0.f : 1.0f / lrow[r];  // a NaN sum stays one, here and in the LSE
 #pragma unroll
     for (int nd = 0; nd < 16; ++nd)
       *reinterpret_cast<float2*>(dst + row * 128 + nd * 8 + tig * 2) =
           make_float2(o[nd][2 * r] * inv, o[nd][2 * r + 1] * inv);
-    if (tig == 0) lse_dst[row] = lrow[r] > 0.f ? mrow[r] + __logf(lrow[r]) : -INFINITY;
+    if (tig == 0) lse_dst[row] = lrow[r] == 0.f ? -INFINITY : mrow[r] + __logf(lrow[r]);
   }
 }
 
@@ -410,11 +410,12 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads,
         reinterpret_cast<float*>(smem + (lane % kWarps) * kWarpBytes) + 16 * 128, lane / kWarps);
     const float l = pl[h];
     const float m = warp_max(l);
-    const float e = (m == -INFINITY || l == -INFINITY) ? 0.f : __expf(l - m);
+    // the lane's own part alone says whether it is empty: a NaN, which the maximum passes over, stays one
+    const float e = l == -INFINITY ? 0.f : __expf(l - m);
     const float total = warp_sum(e);
-    wts[h * 32 + lane] = total > 0.f ? e / total : 0.f;
+    wts[h * 32 + lane] = total == 0.f ? 0.f : e / total;
     if (lane == 0 && lse_out && rank == (h % kClusterCtas))
-      lse_out[f * G + h] = total > 0.f ? m + __logf(total) : -INFINITY;
+      lse_out[f * G + h] = total == 0.f ? -INFINITY : m + __logf(total);
   }
   __syncthreads();
   // (head, channel) outputs of the row, dealt over the cluster's threads: 32 independent

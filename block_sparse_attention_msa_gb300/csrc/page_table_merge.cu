@@ -71,10 +71,10 @@ __global__ void __launch_bounds__(256)
   float wts[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    wts[h] = (m == -INFINITY || my_l[h] == -INFINITY) ? 0.f : __expf(my_l[h] - m);
+    wts[h] = my_l[h] == -INFINITY ? 0.f : __expf(my_l[h] - m);  // a NaN, which m passes over, stays one
   const float my_w = wts[0];
   const float total = warp_sum(wts[0] + wts[1]);
-  const float inv = total > 0.f ? 1.0f / total : 0.f;
+  const float inv = total == 0.f ? 0.f : 1.0f / total;
   const int64_t orow = (u * G + e) * (int64_t)D;
   if (BF16 && D == 128 && S <= 32) {
     const int half = lane >> 4, c = lane & 15;  // channels c*8 .. c*8+7
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256)
       }
     }
   }
-  if (lse && lane == 0) lse[u * G + e] = total > 0.f ? m + __logf(total) : -INFINITY;
+  if (lse && lane == 0) lse[u * G + e] = total == 0.f ? -INFINITY : m + __logf(total);
 }
 
 // Prefill merge over chunk-major partials: part_o[c][row][8] bf16 with c = 16 channel chunks

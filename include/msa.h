@@ -310,7 +310,8 @@ MSA_API int msa_prefill_bucket(const int32_t* block_ids, int32_t T, int32_t Hkv,
  *
  * For unit u < U and head e < G:  lse = log sum_s exp(lse_parts[u,s,e]);
  *   o[u,e,:] = sum_s exp(lse_parts[u,s,e] - lse) * o_parts[u,s,e,:]; partials whose lse is
- *   -inf carry no weight; a unit with no finite partial gives o = 0, lse = -inf.
+ *   -inf carry no weight; a unit with no other partial gives o = 0, lse = -inf. A partial whose lse is
+ *   NaN makes o and lse NaN.
  *   o_parts   [U, S, G, D], bf16 when parts_bf16 != 0 else fp32; lse_parts [U, S, G] fp32
  *   o         [U, G, D] bf16 (out); lse [U, G] fp32 (out, may be NULL)
  * With U = T*Hkv and G = Hq/Hkv the output is exactly the [T, Hq, D] layout.

@@ -60,7 +60,7 @@ def decode_bf16(w):
     return msa.paged_sparse_decode(w["q"], w["k"], w["v"], w["fpt"], w["lens"])
 
 
-DECODES = [pytest.param(decode_fp8, id="e4m3")]
+DECODES = [pytest.param(decode_fp8, id="e4m3"), pytest.param(decode_bf16, id="bf16")]
 
 
 # rows: one cluster each where there are few, else partials and a merge kernel
@@ -84,3 +84,23 @@ def test_decode_rows_that_see_a_nan(decode, R, n, topk, what):
     assert torch.isnan(o[r, heads]).all() and torch.isnan(lse[r, heads]).all()
     o[r, heads], lse[r, heads] = clean[0][r, heads], clean[1][r, heads]
     assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("S", [1, 3, 40])
+def test_a_merge_of_parts_one_of_which_is_nan(bf16, S):
+    g = torch.Generator().manual_seed(S)
+    U, G = 5, 4
+    parts = torch.randn((U, S, G, D), generator=g).to(torch.bfloat16 if bf16 else torch.float32).to(DEV)
+    lse = torch.randn((U, S, G), generator=g).to(DEV)
+    lse[1, 1:] = lse[3] = -float("inf")       # one part; none
+    clean = msa.lse_merge(parts, lse)
+    assert (clean[0][3] == 0).all() and torch.isneginf(clean[1][3]).all()
+    lse[1, 0, 2] = lse[2, S // 2, 1] = NAN
+    lse[4, :, 0] = -float("inf")
+    lse[4, S - 1, 0] = NAN                    # beside empty parts
+    o, z = msa.lse_merge(parts, lse)
+    for u, e in ((1, 2), (2, 1), (4, 0)):
+        assert torch.isnan(o[u, e]).all() and torch.isnan(z[u, e])
+        o[u, e], z[u, e] = clean[0][u, e], clean[1][u, e]
+    assert torch.equal(o, clean[0]) and torch.equal(z, clean[1])
