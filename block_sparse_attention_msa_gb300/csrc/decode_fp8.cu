@@ -241,7 +241,9 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
     // Q^T fragments (K index 16 x heads): k-step ks takes channels 64 (ks / 4) + 16 tig + 4 (ks % 4) + 0..3
     // of head 8 h + gid
     uint32_t qb[HT][8][2];
-    float qf[HT][2];  // 2^eq * log2(e) of this lane's heads as columns of S^T
+    // Of this lane's heads as columns of S^T: qf * qw = 2^eq * log2(e), qw the part of 2^eq above 1. A score is
+    // (sc * (2^a * qf)) * qw: factors below 1 come together, so that nothing leaves fp32 but what the score does.
+    float qf[HT][2], qw[HT][2];
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
       const int head = 8 * h + gid;
@@ -273,7 +275,9 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int32_t ey = __shfl_sync(0xffffffffu, e, (2 * tig + y) * 4);
-        qf[h][y] = kLog2e * __int_as_float((ey - 14) << 23);  // 2^(e - 141), exponent field e - 14 >= 1
+        // 2^(e - 141): exponent field e - 14 >= 1
+        qf[h][y] = kLog2e * __int_as_float(min(ey - 14, 127) << 23);
+        qw[h][y] = __int_as_float(max(ey - 14, 127) << 23);
       }
     }
     Seg<HT> s;
@@ -345,7 +349,7 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int r = c >> 1, y = c & 1;
-            float t = sc[h][mt][c] * ks[mt][r] * qf[h][y];
+            float t = sc[h][mt][c] * (ks[mt][r] * qf[h][y]) * qw[h][y];
             if (n0 + mt * 16 + r * 8 + (int)perm >= len) t = -INFINITY;
             sc[h][mt][c] = t;
             w[mt][c] = t + vs[mt][r];

@@ -523,8 +523,9 @@ MSA_API int msa_chunk_attention(const uint16_t* q, int64_t q_stride, const uint1
  * A row is one token of one KV group. Its 128 channels are e4m3 numbers (no infinity; 448 the
  * largest) with one power of two: k_cache, v_cache [num_pages, Hkv, 128, D] e4m3 bytes (a page of a
  * group is 16 KB in one piece) and k_scale, v_scale [num_pages, Hkv, 128] bytes e + 127. The value of a
- * channel is number * 2^e. Slots (page*128 + offset) and virtual pages (page*128*Hkv + group) are those
- * of the bf16 caches, so one set of tables serves both.
+ * channel is number * 2^e (bytes 0 to 254; 255, which msa_append_kv_fp8 never writes, stands for no
+ * power). Slots (page*128 + offset) and virtual pages (page*128*Hkv + group) are those of the bf16
+ * caches, so one set of tables serves both.
  *
  * msa_append_kv_fp8: for every token row t with slot_map[t] >= 0 and every group, e is the smallest
  *   integer in [-127, 119] for which every finite |x| <= 448 * 2^e (119: rows beyond are held at
