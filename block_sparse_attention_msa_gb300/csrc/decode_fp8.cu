@@ -6,13 +6,16 @@
 //   m = max t_n,  l = sum 2^(t_n - m),  M = max (t_n + b_n),  O = sum 2^(t_n + b_n - M) v'_n
 //   o = O 2^(M - m) / l,  lse = (m + log2 l) ln 2.
 // The values' powers of two are part of the weights, so the products run on the stored numbers as they
-// are. The weights have a maximum of their own, M: they stay in (0, 1] however the magnitudes of V
-// differ from token to token, and l, without the powers, keeps m.
+// are. The weights have a maximum of their own, M: they stay in (0, 2^8] of it (see kFar) however the
+// magnitudes of V differ from token to token, and l, without the powers, keeps m.
 //
 // e4m3 becomes fp16 in one instruction per pair, exactly, so both products are fp16 MMAs with fp32
 // sums. The other operands are rounded to fp16: q after a power of two that brings its head's largest
-// magnitude to [2^14, 2^15) (exact down to 2^-28 of that, then 2^-39 of it), the weights in (0, 1]
-// at 2^-11 of their value (2^-25 below 2^-14). bf16 weights, as beside bf16 values, would be at 2^-8.
+// magnitude to [2^14, 2^15) (exact down to 2^-28 of that, then 2^-39 of it), the weights at 2^-11 of
+// their value. fp16 keeps that to 2^-14, and a weight carries its value's power of two, so beside one token
+// of far larger values the others' weights lie far below the largest. The weights are therefore taken times
+// 2^7, to 2^15 at most, just within fp16: 2^-11 of their value down to 2^-21 of the largest, and 2^-32 of the
+// largest below. bf16 weights, as beside bf16 values, would be at 2^-8.
 //
 // GB300 design. HBM-bound: 2 * 129 bytes per (row, group, token), so what counts is loads in flight and
 // few instructions per byte.
@@ -61,9 +64,10 @@ constexpr uint32_t kTile = kTok * 128;         // K or V of a step
 constexpr uint32_t kStep = 2 * kTile;
 constexpr uint32_t kRing = kStages * kStep;    // of one warp: 16 KB
 constexpr uint32_t kScales = 2 * kTok;         // bytes per step
-// A score may exceed the softmax's reference by this much (log2) before the reference moves: weights stay
-// below 2^8, far within fp16.
+// A score may exceed the softmax's reference by this much (log2) before the reference moves, and weights are
+// taken times 2^kLift: they stay at 2^15 at most, within fp16 (65504).
 constexpr float kFar = 8.f;
+constexpr float kLift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -202,7 +206,7 @@ struct Walk {
 };
 
 // What a row segment leaves in a lane, for HT tiles of 8 heads: heads 8 h + 2 tig + {0, 1}, channels
-// 16 chunk + 0..15 (chunk: 4 (gid & 1) + gid / 2), O relative to 2^M.
+// 16 chunk + 0..15 (chunk: 4 (gid & 1) + gid / 2), O relative to 2^(M - kLift).
 template <int HT>
 struct Seg {
   float o[HT][8][4];  // [.][channel pair][channel 2x: heads 0, 1; channel 2x + 1: heads 0, 1]
@@ -386,7 +390,7 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           mref[y] = s.m[h][y] == -INFINITY ? 0.f : s.m[h][y];
-          Mref[y] = s.M[h][y] == -INFINITY ? 0.f : s.M[h][y];
+          Mref[y] = (s.M[h][y] == -INFINITY ? 0.f : s.M[h][y]) - kLift;
         }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
@@ -454,8 +458,8 @@ __device__ __forceinline__ void store_partial(float* dst, float* lse_dst, const 
       const int head = 8 * h + 2 * tig + y;
       if (head >= G) continue;
       const float l = s.l[h][y];
-      // O 2^(M - m) / l, the power in two halves: it may leave fp32's range where O's product does not
-      const float half = l == 0.f ? 0.f : ex2(0.5f * (s.M[h][y] - s.m[h][y])), inv = l == 0.f ? 0.f : 1.0f / l;
+      // O 2^(M - kLift - m) / l, the power in two halves: it may leave fp32's range where O's product does not
+      const float half = l == 0.f ? 0.f : ex2(0.5f * (s.M[h][y] - kLift - s.m[h][y])), inv = l == 0.f ? 0.f : 1.0f / l;
       float4* d = reinterpret_cast<float4*>(dst + head * 128 + chunk * 16);
 #pragma unroll
       for (int x = 0; x < 4; ++x)

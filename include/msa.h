@@ -539,7 +539,8 @@ MSA_API int msa_chunk_attention(const uint16_t* q, int64_t q_stride, const uint1
  * msa_paged_sparse_decode_fp8: msa_paged_sparse_decode on the values of the quantised cache, with the
  *   same tables and the same workspace size. e4m3 numbers are multiplied as they are; q and the softmax
  *   weights are rounded to fp16 for it (q after a power of two for its head, so at 2^-39 of the
- *   head's largest magnitude at most; weights at 2^-11 of their value).
+ *   head's largest magnitude at most; weights, each taken times the power of its row of V, at 2^-11 of
+ *   their value, or 2^-32 of the row's largest such weight where that is more).
  * Tensors are 16-byte aligned. num_pages*128*Hkv must fit int32. A slot of num_pages*128 or more is
  * skipped, a virtual page out of range read as page 0, group 0; both set bit 0 of the device error word.
  * ------------------------------------------------------------------------------------ */

@@ -42,3 +42,42 @@ def test_scores_of_large_keys_and_small_queries_and_the_reverse(R, Hq, a, c):
     ref = reference(w)
     assert torch.isfinite(ref[0]).all()
     check(run(w), ref)
+
+
+@pytest.mark.parametrize("R,Hq", [(1, 8), (24, 8), (1, 32), (24, 32)])
+@pytest.mark.parametrize("power", [12, 18, 22, 25])
+@pytest.mark.parametrize("n", [2, 3, 40, 700])
+def test_values_beside_one_token_of_far_larger_values(R, Hq, power, n):
+    """One token's values are 2^power larger, in channel 0 alone: the other channels' outputs are the other
+    tokens', whose weights (with their values' powers of two) lie as far below the largest.
+
+    Tolerance: each weight is rounded to fp16 at 2^-11 of its value or at 2^-32 of the row's largest, whichever
+    is more; the rest as in the other decode tests."""
+    Hkv, topk = 2, 6
+    w = base.make([n] * (R * Hkv), topk, Hq, Hkv, seed=power + n, spread=0.0, pages=64)
+    first = w["fpt"][:, 0].long()
+    page, g = first // (PAGE * Hkv), first % (PAGE * Hkv)
+    code, e = base.ref_quantise(np.concatenate([[2.0 ** power], np.zeros(D - 1)])[None])
+    at = n // 2 if n < PAGE else 77
+    w["vc"][page, g, at], w["vs"][page, g, at] = torch.from_numpy(code), torch.from_numpy(e)
+    o, lse, to, tl = reference(w)
+    fpt = w["fpt"].long()
+    tight = torch.zeros_like(to)
+    G = Hq // Hkv
+    for f in range(R * Hkv):
+        r, h = f // Hkv, slice(f % Hkv * G, (f % Hkv + 1) * G)
+        vp = fpt[f, :(n + PAGE - 1) // PAGE]
+        pg, gg = vp // (PAGE * Hkv), vp % (PAGE * Hkv)
+        k, v = (torch.from_numpy(base.ref_values(w[x + "c"][pg, gg].numpy(), w[x + "s"][pg, gg].numpy())).flatten(0, 1)[:n]
+                for x in "kv")
+        b = torch.exp2(w["vs"][pg, gg].double().flatten()[:n] - 127)
+        qi = w["q"][r, h].double()
+        s = qi @ k.T
+        p = torch.softmax(s, -1)
+        big = (p * b).amax(-1, keepdim=True)
+        step = torch.maximum(2.0 ** -11 * (1 + 2.0 ** -7) * p, 2.0 ** -32 * (1 + 2.0 ** -7) * big / b)   # of a weight
+        ds = 2.0 ** -23 * 128 * (qi.abs() @ k.abs().T).amax(-1, keepdim=True) + 2.0 ** -21 * s.abs().amax(-1, keepdim=True) \
+            + 2.0 ** -39 * qi.abs().amax(-1, keepdim=True) * k.abs().sum(-1).max()
+        A = p @ v.abs()
+        tight[r, h] = 2.0 ** -8 * (p @ v).abs() * (1 + 2.0 ** -7) + step @ v.abs() + (2 * ds + 2.0 ** -20 + n * 2.0 ** -24) * A
+    check(run(w), (o, lse, tight, tl))
