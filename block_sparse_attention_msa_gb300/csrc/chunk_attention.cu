@@ -1138,6 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(good = wait_or_fail(&B.o_full[X][(n - 1) & 1], ((n - 1) >> 1) & 1, fail))) break;
       tmem_fence_after();
       float f0 = 1.f, f1 = 0.f;  // weights of the lanes' parts
+      bool later = false;
       float4* half = nullptr;    // lane 1's part, for which lane 0 waits
       if (halves) {
         half = reinterpret_cast<float4*>(p.half_po) + (int64_t)blockIdx.x * 128 * 32 + row;
@@ -1148,10 +1149,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(good = wait_or_fail(&B.half_full, halved & 1, fail))) break;
           const float2 o = B.half_ml[row];
           const float m = fmaxf(m_run, o.x);
-          if (o.x != -INFINITY || o.y != 0.f) f1 = ex2(o.x - m);  // lane 1's keys count for the row
+          // whether the row sees keys of lane 1. Their weight may be 0 all the same, beside far larger scores
+          // or where all that is left of them is a NaN: 0 times what is not finite then shows it
+          later = o.x != -INFINITY || o.y != 0.f;
+          if (later) f1 = ex2(o.x - m);
           if (m_run != m) f0 = ex2(m_run - m);
           m_run = m;
-          l = l * f0 + (f1 != 0.f ? o.y * f1 : 0.f);
+          l = l * f0 + (later ? o.y * f1 : 0.f);
         }
         ++halved;
       }
@@ -1212,7 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float4 h = f1 != 0.f ? __ldcg(half + (c * 4 + x) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 h = later ? __ldcg(half + (c * 4 + x) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
             o[4 * x] = fmaf(h.x, f1, o[4 * x] * f0);
             o[4 * x + 1] = fmaf(h.y, f1, o[4 * x + 1] * f0);
             o[4 * x + 2] = fmaf(h.z, f1, o[4 * x + 2] * f0);

@@ -104,3 +104,30 @@ def test_a_merge_of_parts_one_of_which_is_nan(bf16, S):
         assert torch.isnan(o[u, e]).all() and torch.isnan(z[u, e])
         o[u, e], z[u, e] = clean[0][u, e], clean[1][u, e]
     assert torch.equal(o, clean[0]) and torch.equal(z, clean[1])
+
+
+@pytest.mark.parametrize("n,at", [(65, 64), (33, 32), (129, 128), (200, 64)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_a_nan_in_the_later_half_of_a_single_group_s_keys(n, at, what):
+    """One KV group: the keys of a tile are halved between two lanes. The NaN key is the only one that the row
+    sees in the later half, or its values are NaN and its weight vanishes beside the earlier half's."""
+    Hq = 8
+    g = torch.Generator().manual_seed(n)
+    bf = torch.bfloat16
+    P = (n + PAGE - 1) // PAGE
+    kc, vc = (torch.randn((P, PAGE, 1, D), generator=g).to(bf).to(DEV) for _ in range(2))
+    q = torch.ones((1, Hq, D), dtype=bf, device=DEV)
+    table = torch.arange(P, dtype=torch.int32, device=DEV)[None]
+    call = lambda: msa.chunk_attention(q, kc, vc, table, i32([n]).to(DEV), i32([0, 1]).to(DEV))
+    page, off = at // PAGE, at % PAGE
+    if what == "k":
+        kc[page, off] = NAN
+        o, lse = call()
+        assert torch.isnan(o).all() and torch.isnan(lse).all()
+    else:
+        vc[page, off] = NAN
+        kc[page, off] = -200.0        # a score of -25600: no weight is left of it in fp32
+        if n == 200:                  # every key of the later half
+            kc.view(-1, 1, D)[at:n] = -200.0
+        o, lse = call()
+        assert torch.isnan(o).all() and torch.isfinite(lse).all()
