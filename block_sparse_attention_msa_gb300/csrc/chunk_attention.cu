@@ -1109,6 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (m_run != -INFINITY)
 #pragma unroll
                 for (int x = 0; x < kStep; ++x) v[x] -= m_nat;
+              __syncwarp();  // threads part here, and tensor memory is accessed by whole warps
             }
             l4[0] = l4[1] = l4[2] = l4[3] = 0.f;
 #pragma unroll
@@ -1172,6 +1173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t raw[16];
+        __syncwarp();  // threads of padding rows part from the others below, and tcgen05.ld takes a whole warp
         if (act) {
           tmem_ld16(o_tmem + c * 16, raw);
           tmem_wait_ld();
