@@ -1025,6 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float o[64];
+        __syncwarp();  // live rows alone store below, and tcgen05.ld takes a whole warp
         if (act) {
           tmem_ld32(o_tmem + c * 64, o);
           tmem_ld32(o_tmem + c * 64 + 32, o + 32);

@@ -67,3 +67,18 @@ def test_rows_without_a_finite_score_beside_rows_of_far_scores(Hq, Hkv, held):
     score = float(torch.tensor(-2.5e38).to(torch.bfloat16)) * 2.0 ** -80
     assert ((lse[~none].double() - score).abs() <= 2.0 ** -22 * abs(score)).all()
     assert n <= w["table"].shape[1] * PAGE
+
+
+@pytest.mark.parametrize("Hq,Hkv,N", [(8, 8, 7), (8, 4, 3), (16, 1, 2), (32, 2, 3), (64, 8, 1)])
+@pytest.mark.parametrize("held", [0, 900])
+def test_the_same_rows_in_the_shared_prefix_decode(Hq, Hkv, N, held):
+    w = make([N, N], [held, 3], Hq, Hkv, seed=held + N)
+    clean = reference(w)
+    pos = held + N - 1
+    w["vc"][w["table"][0, pos // PAGE], pos % PAGE, :, 17] = NAN
+    d = {k: x.to(DEV) for k, x in w.items()}
+    o, lse = msa.shared_prefix_decode(d["q"], d["kc"], d["vc"], d["table"], d["seq"],
+                                      torch.zeros(1, dtype=torch.int32, device=DEV), N=N)
+    assert torch.isnan(o[N - 1, :, 17]).all()
+    o[N - 1, :, 17] = clean[0][N - 1, :, 17].to(torch.bfloat16).to(DEV)
+    check((o, lse), clean)
