@@ -304,7 +304,8 @@ __device__ __forceinline__ bool walk_units(const KParams& p, const CUtensorMap& 
       for (int k = 0; k + 1 < kStages - 1; ++k) ahead[k] = ahead[k + 1];
       ahead[kStages - 2] = prefetch();
       const uint32_t st = it % kStages;
-      if (!mbar_wait(&bars.full[warp][st], (it / kStages) & 1)) {
+      // each thread waits for itself; the vote brings the warp together, as the products take it, with one answer
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[warp][st], (it / kStages) & 1))) {
         if (lane == 0) msa_record_error(kErrTimeout);
         for (uint32_t k = it + 1; k < issued; ++k)  // the copies in flight land before the CTA leaves
           mbar_wait(&bars.full[warp][k % kStages], (k / kStages) & 1);
