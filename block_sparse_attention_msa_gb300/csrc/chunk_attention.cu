@@ -83,6 +83,7 @@ constexpr int kMinPiece = 16;       // steps of a piece, where the whole call ha
 // (which HBM feeds at the copy rate when all CTAs have such), and what a tile's end and beginning take.
 constexpr int32_t kSharedCost = 4, kOwnCost = 7, kTileCost = 7;
 constexpr int32_t kLeastRun = 2 * kOwnCost;
+constexpr uint32_t kMostCost = 2147483647;  // of a call
 
 // What the two lanes of a unit have.
 enum : int32_t {
@@ -585,34 +586,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (SELF) {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int32_t sum = 0;
+    // The layout holds the sums of token ranges in order below kMostCost. Ranges that overlap can pass it by far:
+    // the sums stop there, and such a call has no work.
+    uint32_t sum = 0;
     bool any_bad = false;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       bool bad;
-      sum += request_cost(p, request_of(p, b, bad));
+      sum = min(sum + (uint32_t)request_cost(p, request_of(p, b, bad)), kMostCost);
       any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) msa_record_error(kErrBadBlock);
-    int32_t before = sum;
+    uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = min(incl + y, kMostCost);
     }
-    if (lane == 31) B.w_sum[warp] = before;
+    if (lane == 31) B.w_sum[warp] = (int32_t)incl;
     if (tid == 0) B.start_b = p.B;
     __syncthreads();
-    before -= sum;
-    int32_t total = 0;
+    uint32_t at = incl - sum, all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += B.w_sum[w];
-      total += B.w_sum[w];
+      if (w < warp) at = min(at + (uint32_t)B.w_sum[w], kMostCost);
+      all = min(all + (uint32_t)B.w_sum[w], kMostCost);
     }
+    const int32_t total = all < kMostCost ? (int32_t)all : 0, before = (int32_t)at;
     const int32_t workers = max(1, min((int32_t)gridDim.x, total / kLeastRun));
     const int32_t x0 = (int32_t)((int64_t)total * min((int32_t)blockIdx.x, workers) / workers);
-    if (before <= x0 && x0 < before + sum) {  // this CTA starts in one of the thread's requests
+    if (before <= x0 && x0 - before < (int32_t)sum && total > 0) {  // this CTA starts in one of the thread's requests
       int32_t off = x0 - before;
       int b = b0;
 #pragma unroll 1
@@ -1402,7 +1405,7 @@ Layout layout_of(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_bloc
   // Equal runs where tokens fill one tile per request on average, or there are few pairs: keys are then read
   // by few CTAs each, and what counts is that all CTAs have work, without the plan kernel's time.
   y.self = (T <= B * tpt || pairs <= 2 * ctas) &&
-           items * ((2 * (int64_t)max_blocks + 1) * kOwnCost + kTileCost) <= 2147483647;
+           items * ((2 * (int64_t)max_blocks + 1) * kOwnCost + kTileCost) <= kMostCost;
   if (y.self) {
     y.cap_joins = 2 * ctas;
     y.cap_pieces = 2 * ctas;  // of a run's first and last item

@@ -502,8 +502,9 @@ MSA_API int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache,
  *   rows of one request with G 8 and 485 blocks, 0.35 GB for 1024 blocks.
  * B <= 16384, T*Hq in int32. Lengths and tables are read on the device: a captured call can be
  * replayed with other values in the same buffers. cu_tokens out of order or outside [0, T], lengths
- * below n_b or above max_blocks*128 are clamped and set bit 1 of the device error word, a page id
- * out of range is read as page 0 and sets bit 0. The result depends only on the inputs and the
+ * below n_b or above max_blocks*128 are clamped and set bit 1 of the device error word (where ranges out
+ * of order overlap, what the rows hold is not defined); a page id out of range is read as page 0 and
+ * sets bit 0. The result depends only on the inputs and the
  * device's SM count (no run-to-run variation). Sums and lse are fp32; the softmax weights are rounded to
  * bf16 for their product with V, as in the library's other attention calls.
  * ------------------------------------------------------------------------------------ */
