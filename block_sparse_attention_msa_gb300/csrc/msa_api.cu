@@ -563,6 +563,23 @@ int msa_paged_sparse_decode_fp8(const uint16_t* q, const uint8_t* k_cache, const
 }
 
 // ------------------------------------------------------------------------------ chunk attention
+struct ByteRange {
+  const void* at;
+  int64_t bytes;
+};
+static bool overlaps(const ByteRange& x, const ByteRange& y) {
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.at), y0 = reinterpret_cast<uintptr_t>(y.at);
+  return x.bytes > 0 && y.bytes > 0 && x0 < y0 + y.bytes && y0 < x0 + x.bytes;
+}
+// ... one of n rows of `row` bytes, `step` bytes apart; what lies between them may be another tensor's.
+static bool overlaps_rows(const ByteRange& x, const void* rows, int64_t n, int64_t step, int64_t row) {
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.at), r0 = reinterpret_cast<uintptr_t>(rows);
+  if (!overlaps(x, {rows, (n - 1) * step + row})) return false;
+  if (n == 1 || x0 < r0 + row) return true;  // up to the first row's end
+  const int64_t i = (int64_t)(x0 - r0) / step;  // the last row that begins at or before x
+  return overlaps(x, {reinterpret_cast<const void*>(r0 + i * step), row}) ||
+         (i + 1 < n && overlaps(x, {reinterpret_cast<const void*>(r0 + (i + 1) * step), row}));
+}
 // Work items of a call: pairs of query tiles and single tiles, per KV group.
 static int64_t chunk_items(int32_t B, int32_t T, int32_t Hq, int32_t Hkv) {
   return (int64_t)Hkv * (T / (2 * (128 / (Hq / Hkv))) + (B < T ? B : T));
@@ -604,6 +621,17 @@ int msa_chunk_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_c
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return fail(MSA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", name,
                 workspace, workspace_bytes, need);
+  // outputs and workspace: written while the inputs, of which q's rows may stand apart, are read
+  const int64_t rows = (int64_t)T * Hq, cells = num_pages * 128 * Hkv * 256;
+  const ByteRange written[] = {{o, rows * 256}, {lse, lse ? rows * 4 : 0}, {workspace, (int64_t)need}};
+  const ByteRange read[] = {{k_cache, cells}, {v_cache, cells}, {page_table, (int64_t)B * max_blocks * 4},
+                            {seq_lens, (int64_t)B * 4}, {cu_tokens, ((int64_t)B + 1) * 4}};
+  for (int x = 0; x < 3; ++x) {
+    bool bad = overlaps_rows(written[x], q, T, T > 1 ? q_stride * 2 : 0, (int64_t)Hq * 256);
+    for (const ByteRange& r : read) bad |= overlaps(written[x], r);
+    for (int y = 0; y < x; ++y) bad |= overlaps(written[x], written[y]);
+    if (bad) return fail(MSA_ERR_ARG, "%s: an output or the workspace overlaps an input or another output", name);
+  }
   msa::ChunkArgs a{};
   a.q = q;
   a.q_stride = T > 1 ? q_stride : (int64_t)Hq * 128;

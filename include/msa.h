@@ -491,7 +491,8 @@ MSA_API int msa_shared_prefix_decode(const uint16_t* q, const uint16_t* k_cache,
  *   of 8; a slice of a fused projection needs no copy)
  *   k_cache, v_cache [num_pages, 128, Hkv, D] bf16; page_table [B, max_blocks] int32
  *   seq_lens [B], cu_tokens [B+1] int32
- *   o [T, Hq, D] bf16, lse [T, Hq] fp32 or NULL (out; neither may overlap an input)
+ *   o [T, Hq, D] bf16, lse [T, Hq] fp32 or NULL (out). No output may overlap an input, the workspace or
+ *   the other output (MSA_ERR_ARG); o may lie between the rows of q
  *   workspace >= msa_chunk_attention_workspace_size(B, T, Hq, Hkv, max_blocks) bytes, 256-byte
  *   aligned, any contents (its size goes with the current device's SM count). Calls that may run
  *   concurrently need separate workspaces. It holds fp32 partials, 520 bytes per row of 2 * min(128,
