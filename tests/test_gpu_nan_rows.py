@@ -131,3 +131,19 @@ def test_a_nan_in_the_later_half_of_a_single_group_s_keys(n, at, what):
             kc.view(-1, 1, D)[at:n] = -200.0
         o, lse = call()
         assert torch.isnan(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("new,held,Hq,Hkv", [([40, 1], [700, 90], 32, 4), ([9, 2], [0, 400], 8, 1), ([1, 1, 1], [5, 64, 900], 8, 2)])
+@pytest.mark.parametrize("junk", [NAN, float("inf")])
+def test_queries_that_are_not_finite_beside_others_in_a_tile(new, held, Hq, Hkv, junk):
+    from test_gpu_chunk_attention import make, reference, run, check
+    w = make(new, held, Hq, Hkv, seed=Hq + len(new))
+    clean = reference(w)
+    T = sum(new)
+    bad = torch.zeros((T, Hq), dtype=torch.bool)
+    bad[::3, 1::4] = True
+    w["q"][:T][bad] = junk              # infinity: scores of both signs, or infinity times 0
+    o, lse = run(w)
+    assert torch.isnan(o.cpu()[bad]).all() and torch.isnan(lse.cpu()[bad]).all()
+    o[bad.to(DEV)], lse[bad.to(DEV)] = clean[0][bad].to(torch.bfloat16).to(DEV), clean[1][bad].float().to(DEV)
+    check((o, lse), clean)
