@@ -387,7 +387,8 @@ def _call(dev, fn, *args):
 def _scratch_call(dev, workspace: Workspace | None, key: str, size, fn):
     """fn(pointer, bytes, stream) with `dev` current and size() bytes of scratch, from `workspace` or, for
     this call alone, from the caching allocator: in the stream's order, as a tensor's memory would be, but
-    without the tensor (3 us of a call of 22)."""
+    without the tensor. (A call of one row on 2048 keys takes the host 19.2 us so, 23.3 with a tensor, 22.1
+    with the allocator's calls in torch.cuda.)"""
     def run(stream):
         nbytes = max(256, size())
         if workspace is not None:

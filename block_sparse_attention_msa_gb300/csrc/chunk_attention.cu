@@ -30,7 +30,7 @@
 //
 // Per lane S = Q K^T (128 x 64 x 128) and O += P V run on tcgen05 with S, P and O in tensor memory; one
 // softmax warpgroup per lane keeps the running reference and sum in fp32. P is rounded to bf16 for its
-// product, as tensor cores take it beside V in bf16 (2^-9 of each weight at most); its sum l is taken
+// product, as tensor cores take it beside V in bf16 (2^-8 of each weight at most); its sum l is taken
 // before that rounding. A step is 64 keys because then S has two buffers per lane next to O (2 lanes x
 // (2 x 64 + 128) = 512 columns): S(i+1) is ready when the softmax of step i ends. K and V come through a
 // ring and a producer warp each: one warp for both needs 1.4 us a step, as long as the decode rows' step.
@@ -39,7 +39,7 @@
 //   one prompt of 16384             3.00-3.15 ms  (1.40-1.47 PFLOP/s, 75-78 % of the burst rate)
 //   2048 tokens on 60032 keys       2.83-2.87 ms  (1.43-1.45 PFLOP/s)
 //   64 decode rows, 4k-16k keys     0.381-0.391 ms (the copy rate: HBM)
-//   64 chunks of 64 tokens          0.117 ms; 1 row on 2048 keys 13 us (latency, two launches)
+//   64 chunks of 32-64 tokens behind 250-1000   0.117 ms; 1 row on 2048 keys 13.4 us (latency, two launches)
 // Long chunks are bound by the S products. An N = 64 product reads its 128 x 16 Q operand from shared
 // memory again at every instruction: 48 cycles measured where its arithmetic takes 32 (N = 128: 64 of 64; P
 // from tensor memory, N = 128: 64 of 64). Without the S products 3.09 ms became 2.22, without the O products
