@@ -606,16 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) B.w_sum[warp] = (int32_t)incl;
     if (tid == 0) B.start_b = p.B;
     __syncthreads();
-    uint32_t at = incl - sum, all = 0;
+    uint32_t at = incl - sum;
+    uint64_t all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at = min(at + (uint32_t)B.w_sum[w], kMostCost);
-      all = min(all + (uint32_t)B.w_sum[w], kMostCost);
+      const uint32_t x = (uint32_t)B.w_sum[w];
+      if (w < warp) at += x;  // means nothing where `all` is over
+      all += x;
     }
     const int32_t total = all < kMostCost ? (int32_t)all : 0, before = (int32_t)at;
     const int32_t workers = max(1, min((int32_t)gridDim.x, total / kLeastRun));
     const int32_t x0 = (int32_t)((int64_t)total * min((int32_t)blockIdx.x, workers) / workers);
-    if (before <= x0 && x0 - before < (int32_t)sum && total > 0) {  // this CTA starts in one of the thread's requests
+    if (total > 0 && before <= x0 && x0 - before < (int32_t)sum) {  // this CTA starts in one of the thread's requests
       int32_t off = x0 - before;
       int b = b0;
 #pragma unroll 1
