@@ -39,7 +39,7 @@
 //
 // Measured, Hq/Hkv/D = 64/8/128, top 16: 64 rows on 8k-128k 50 us (264 MB, 5.3 TB/s, 78 % of the
 // copy rate; the bf16 form reads 528 MB), 4 rows on 1M 11.0 us, 1 row on 2048 8 us; 16 heads per group (Hq 128),
-// 64 rows: 56 us. With two warps per scheduler the issue slots are 40 % used and DRAM 71 %: what is left is the
+// 64 rows: 56 us. With two warps per scheduler the issue slots are 40 % used and DRAM 70 %: what is left is the
 // latency from a step's arrival to its products' results, which more warps or stages do not hide (they were
 // slower, above).
 #include <cooperative_groups.h>
